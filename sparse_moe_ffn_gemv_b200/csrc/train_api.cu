@@ -1,0 +1,652 @@
+// train_api.cu -- the C ABI of moe_train.h: validation, workspace layout, launch order.
+#include <algorithm>
+#include <cmath>
+
+#include "common.cuh"
+#include "train_internal.h"
+
+using namespace moe;
+
+namespace {
+
+#define MOE_CHECK(expr)                          \
+    do {                                         \
+        const moe_status _s = (expr);            \
+        if (_s != MOE_OK) return _s;             \
+    } while (0)
+#define MOE_CUDA(expr)                                  \
+    do {                                                \
+        if ((expr) != cudaSuccess) return MOE_ERR_CUDA; \
+    } while (0)
+
+constexpr int64_t kMaxRows = int64_t(1) << 30;   // slots (their padded rows fit 32 bits)
+constexpr int64_t kMaxElems = int64_t(1) << 46;  // elements of any one tensor
+
+int esize(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
+
+moe_status need(const void* p) {
+    return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0 ? MOE_OK : MOE_ERR_INVALID_ARGUMENT;
+}
+moe_status maybe(const void* p) { return p ? need(p) : MOE_OK; }
+// Row stride of a [T, cols] tensor. One row has no stride to speak of, but its address
+// arithmetic and tensor maps use it, so it is checked all the same.
+moe_status stride(int64_t ld, int64_t cols, int dtype) {
+    if (ld < cols || (ld * esize(dtype)) % 16 != 0) return MOE_ERR_INVALID_ARGUMENT;
+    return ld >= (int64_t(1) << 36) ? MOE_ERR_SHAPE_OVERFLOW : MOE_OK;
+}
+moe_status check_status_ptr(const int32_t* p) {
+    return (reinterpret_cast<uintptr_t>(p) & 3u) == 0 ? MOE_OK : MOE_ERR_INVALID_ARGUMENT;
+}
+
+struct Carver {
+    size_t off = 0;
+    size_t take(int64_t bytes) {
+        const size_t o = off;
+        off = align256(off + size_t(bytes > 0 ? bytes : 0));
+        return o;
+    }
+};
+template <typename P> P* at(void* ws, size_t off) { return reinterpret_cast<P*>(static_cast<char*>(ws) + off); }
+
+moe_status check_ws(const void* ws, size_t have, size_t want) {
+    if (want == 0) return MOE_OK;
+    MOE_CHECK(need(ws));
+    return have < want ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
+}
+
+// ------------------------------------------------------------------ linear
+moe_status check_linear(const moe_linear_desc* d, int64_t T) {
+    if (!d || d->in_features <= 0 || d->out_features <= 0) return MOE_ERR_INVALID_ARGUMENT;
+    if (d->activation < MOE_LINEAR_NONE || d->activation > MOE_LINEAR_GELU) return MOE_ERR_INVALID_ARGUMENT;
+    if (d->dtype != MOE_DTYPE_F32 && d->dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARGUMENT;
+    const int q = 16 / esize(d->dtype);
+    if (d->in_features % q || d->out_features % q) return MOE_ERR_INVALID_ARGUMENT;
+    if (T < 0) return MOE_ERR_INVALID_ARGUMENT;
+    if (T > kMaxRows || T * std::max(d->in_features, d->out_features) > kMaxElems) return MOE_ERR_SHAPE_OVERFLOW;
+    return MOE_OK;
+}
+
+struct LinearWs {
+    size_t dz, partial, total;
+};
+LinearWs linear_ws(const moe_linear_desc* d, int64_t T, bool backward) {
+    LinearWs L{};
+    Carver c;
+    if (backward && T > 0) {
+        L.dz = c.take(d->activation != MOE_LINEAR_NONE ? T * d->out_features * esize(d->dtype) : 0);
+        L.partial = c.take(int64_t(dact_splits(T, d->out_features)) * d->out_features * 4);
+    }
+    L.total = c.off;
+    return L;
+}
+
+// ------------------------------------------------------------------ ffn
+struct FfnShape {
+    int E, k, I, K, es, dtype;
+    bool il, bias;
+    int64_t T, S, rows;  // rows: padded rows at most (dense: T)
+    bool dense;
+};
+
+moe_status check_ffn(const moe_config* c, int64_t T, bool dense, FfnShape* f) {
+    MOE_CHECK(moe_config_validate(c));
+    if (c->weight_format != MOE_DTYPE_F32 && c->weight_format != MOE_DTYPE_BF16) return MOE_ERR_UNSUPPORTED;
+    if (dense && (c->num_experts != 1 || c->top_k != 1)) return MOE_ERR_INVALID_ARGUMENT;
+    if (T < 0) return MOE_ERR_INVALID_ARGUMENT;
+    f->E = c->num_experts;
+    f->k = c->top_k;
+    f->I = c->intermediate;
+    f->K = expert_in(*c);
+    f->dtype = c->act_dtype;
+    f->es = esize(c->act_dtype);
+    f->il = c->gate_up_interleaved != 0;
+    f->bias = c->has_expert_bias != 0;
+    f->T = T;
+    f->dense = dense;
+    if (T > kMaxRows || T * f->k > kMaxRows) return MOE_ERR_SHAPE_OVERFLOW;
+    f->S = T * f->k;
+    f->rows = dense ? T : max_padded_rows(f->S, f->E);
+    if (f->rows * std::max<int64_t>(f->K, 2 * int64_t(f->I)) > kMaxElems) return MOE_ERR_SHAPE_OVERFLOW;
+    return MOE_OK;
+}
+
+// The gate/up, down and bias planes the config has.
+moe_status check_planes(const FfnShape& f, const void* gate, const void* up, const void* gate_up, const void* gate_b,
+                        const void* up_b, const void* gate_up_b, const void* down, const void* down_b) {
+    const void* want[6] = {};
+    int n = 0;
+    if (f.il) {
+        want[n++] = gate_up;
+        if (f.bias) want[n++] = gate_up_b;
+    } else {
+        want[n++] = gate;
+        want[n++] = up;
+        if (f.bias) {
+            want[n++] = gate_b;
+            want[n++] = up_b;
+        }
+    }
+    want[n++] = down;
+    for (int i = 0; i < n; ++i) {
+        if (!want[i]) return MOE_ERR_MISSING_TENSOR;
+        MOE_CHECK(need(want[i]));
+    }
+    if (f.bias) {
+        if (!down_b) return MOE_ERR_MISSING_TENSOR;
+        MOE_CHECK(need(down_b));
+    }
+    return MOE_OK;
+}
+
+struct FfnWs {
+    size_t poff, uoff, row_slot, slot_row;
+    size_t up, dyp;   // gathered rows of u and dy (routed)
+    size_t gp, h;     // forward
+    size_t rows_out;  // [rows, K] slot rows of y or du (routed)
+    size_t dh, dgu, hw, partial;
+    size_t total;
+};
+FfnWs ffn_ws(const FfnShape& f, bool backward) {
+    FfnWs L{};
+    Carver c;
+    if (f.T == 0) return L;
+    if (!f.dense) {
+        L.poff = c.take((f.E + 1) * 4);
+        L.uoff = c.take((f.E + 1) * 4);
+        L.row_slot = c.take(f.rows * 4);
+        L.slot_row = c.take(f.S * 4);
+        L.up = c.take(f.rows * f.K * f.es);
+        if (backward) L.dyp = c.take(f.rows * f.K * f.es);
+        L.rows_out = c.take(f.rows * f.K * f.es);
+    }
+    if (backward) {
+        L.dh = c.take(f.rows * f.I * 4);
+        L.dgu = c.take(f.rows * 2 * f.I * f.es);
+        L.hw = c.take(f.rows * f.I * f.es);
+        if (f.bias)
+            L.partial = c.take(std::max(int64_t(colsum_splits(f.rows, f.E, 2 * f.I)) * f.E * 2 * f.I,
+                                        int64_t(colsum_splits(f.rows, f.E, f.K)) * f.E * f.K) * 4);
+    } else {
+        L.gp = c.take(f.rows * 2 * f.I * 4);
+        L.h = c.take(f.rows * f.I * f.es);
+    }
+    L.total = c.off;
+    return L;
+}
+
+RowPlan row_plan(const FfnShape& f, const int32_t* offsets, const int32_t* sorted_slot, void* ws, const FfnWs& L,
+                 int32_t* status) {
+    RowPlan p;
+    p.T = f.T;
+    p.S = f.S;
+    p.E = f.E;
+    p.k = f.k;
+    p.max_rows = f.rows;
+    p.status = status;
+    if (!f.dense) {
+        p.offsets = offsets;
+        p.sorted_slot = sorted_slot;
+        p.poff = at<int32_t>(ws, L.poff);
+        p.uoff = at<int32_t>(ws, L.uoff);
+        p.row_slot = at<int32_t>(ws, L.row_slot);
+        p.slot_row = at<int32_t>(ws, L.slot_row);
+    }
+    return p;
+}
+
+// All three of the permutation's tensors, or none of them (dense). Without tokens the slots'
+// tensors are empty and may have no address.
+moe_status check_routing(const int32_t* offsets, const int32_t* sorted_slot, const float* topk_w, int64_t T,
+                         bool* dense) {
+    *dense = !offsets && !sorted_slot && !topk_w;
+    if (*dense || T == 0) return MOE_OK;
+    MOE_CHECK(need(offsets));
+    MOE_CHECK(need(sorted_slot));
+    return need(topk_w);
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_linear_workspace_size(const moe_linear_desc* d, int64_t T, int32_t backward, size_t* bytes) {
+    MOE_CHECK(check_linear(d, T));
+    if (!bytes) return MOE_ERR_INVALID_ARGUMENT;
+    *bytes = linear_ws(d, T, backward != 0).total;
+    return MOE_OK;
+}
+
+moe_status moe_linear_forward(const moe_linear_desc* d, const void* x, int64_t ldx, const void* w, const void* bias,
+                              const void* residual, int64_t ldr, int64_t T, void* y, int64_t ldy, void* pre, void* ws,
+                              size_t ws_bytes, int32_t* device_status, moe_stream_t stream) {
+    MOE_CHECK(check_linear(d, T));
+    if (T == 0) return MOE_OK;
+    const int K = d->in_features, N = d->out_features;
+    MOE_CHECK(need(x));
+    MOE_CHECK(need(w));
+    MOE_CHECK(need(y));
+    MOE_CHECK(maybe(bias));
+    MOE_CHECK(maybe(residual));
+    MOE_CHECK(maybe(pre));
+    MOE_CHECK(check_status_ptr(device_status));
+    MOE_CHECK(stride(ldx, K, d->dtype));
+    MOE_CHECK(stride(ldy, N, d->dtype));
+    if (residual) MOE_CHECK(stride(ldr, N, d->dtype));
+    MOE_CHECK(check_ws(ws, ws_bytes, linear_ws(d, T, false).total));
+    GemmArgs g;
+    g.kind = kNT;
+    g.a = x; g.lda = ldx;
+    g.b = w; g.ldb = K;
+    g.M = T; g.N = N; g.R = K;
+    g.bias = bias;
+    g.act = d->activation;
+    g.residual = residual; g.ldr = ldr;
+    g.pre = pre; g.ldp = N;
+    g.out = y; g.ldo = ldy;
+    g.dtype = d->dtype;
+    MOE_CUDA(launch_simt_gemm(g, (cudaStream_t)stream));
+    return MOE_OK;
+}
+
+moe_status moe_linear_backward(const moe_linear_desc* d, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                               const void* w, const void* pre, int64_t T, void* dx, int64_t lddx, void* dw, void* db,
+                               void* ws, size_t ws_bytes, int32_t* device_status, moe_stream_t stream) {
+    MOE_CHECK(check_linear(d, T));
+    const int K = d->in_features, N = d->out_features;
+    cudaStream_t s = (cudaStream_t)stream;
+    MOE_CHECK(maybe(dx));
+    MOE_CHECK(maybe(dw));
+    MOE_CHECK(maybe(db));
+    MOE_CHECK(check_status_ptr(device_status));
+    if (T == 0) {
+        if (dw) MOE_CUDA(cudaMemsetAsync(dw, 0, size_t(N) * K * esize(d->dtype), s));
+        if (db) MOE_CUDA(cudaMemsetAsync(db, 0, size_t(N) * esize(d->dtype), s));
+        return MOE_OK;
+    }
+    const bool act = d->activation != MOE_LINEAR_NONE;
+    MOE_CHECK(need(dy));
+    MOE_CHECK(stride(lddy, N, d->dtype));
+    if (act && !pre) return MOE_ERR_MISSING_TENSOR;
+    if (act) MOE_CHECK(need(pre));
+    if (dx) {
+        MOE_CHECK(need(w));
+        MOE_CHECK(stride(lddx, K, d->dtype));
+    }
+    if (dw) {
+        MOE_CHECK(need(x));
+        MOE_CHECK(stride(ldx, K, d->dtype));
+    }
+    const LinearWs L = linear_ws(d, T, true);
+    MOE_CHECK(check_ws(ws, ws_bytes, L.total));
+    const void* dz = dy;
+    int64_t lddz = lddy;
+    if (act || db) {
+        DactArgs a;
+        a.T = T; a.N = N; a.act = d->activation; a.dtype = d->dtype;
+        a.dy = dy; a.lddy = lddy;
+        a.pre = pre;
+        if (act) {
+            a.dz = at<void>(ws, L.dz);
+            dz = a.dz;
+            lddz = N;
+        }
+        if (db) {
+            a.partial = at<float>(ws, L.partial);
+            a.db = db;
+        }
+        MOE_CUDA(launch_dact(a, s));
+    }
+    GemmArgs g;
+    g.dtype = d->dtype;
+    if (dx) {
+        g.kind = kNN;
+        g.a = dz; g.lda = lddz;
+        g.b = w; g.ldb = K;
+        g.M = T; g.N = K; g.R = N;
+        g.out = dx; g.ldo = lddx;
+        MOE_CUDA(launch_simt_gemm(g, s));
+    }
+    if (dw) {
+        g.kind = kTN;
+        g.a = dz; g.lda = lddz;
+        g.b = x; g.ldb = ldx;
+        g.M = N; g.N = K; g.R = T;
+        g.out = dw; g.ldo = K;
+        MOE_CUDA(launch_simt_gemm(g, s));
+    }
+    return MOE_OK;
+}
+
+moe_status moe_ffn_workspace_size(const moe_config* cfg, int64_t T, int32_t backward, size_t* bytes) {
+    FfnShape f;
+    MOE_CHECK(check_ffn(cfg, T, false, &f));
+    if (!bytes) return MOE_ERR_INVALID_ARGUMENT;
+    size_t n = ffn_ws(f, backward != 0).total;
+    *bytes = n;
+    return MOE_OK;
+}
+
+moe_status moe_ffn_forward(const moe_config* cfg, const moe_weights* w, const void* u, int64_t ldu, int64_t T,
+                           const int32_t* expert_offsets, const int32_t* sorted_slot, const float* topk_w,
+                           const void* residual, int64_t ldr, void* y, int64_t ldy, void* pre, void* ws,
+                           size_t ws_bytes, int32_t* device_status, moe_stream_t stream) {
+    bool dense;
+    FfnShape f;
+    MOE_CHECK(check_routing(expert_offsets, sorted_slot, topk_w, T, &dense));
+    MOE_CHECK(check_ffn(cfg, T, dense, &f));
+    if (!w) return MOE_ERR_INVALID_ARGUMENT;
+    MOE_CHECK(check_planes(f, w->gate_w, w->up_w, w->gate_up_w, w->gate_b, w->up_b, w->gate_up_b, w->down_w,
+                           w->down_b));
+    if (T == 0) return MOE_OK;
+    MOE_CHECK(need(u));
+    MOE_CHECK(need(y));
+    MOE_CHECK(maybe(residual));
+    MOE_CHECK(maybe(pre));
+    MOE_CHECK(check_status_ptr(device_status));
+    MOE_CHECK(stride(ldu, f.K, f.dtype));
+    MOE_CHECK(stride(ldy, f.K, f.dtype));
+    if (residual) MOE_CHECK(stride(ldr, f.K, f.dtype));
+    const FfnWs L = ffn_ws(f, false);
+    MOE_CHECK(check_ws(ws, ws_bytes, L.total));
+    cudaStream_t s = (cudaStream_t)stream;
+    const RowPlan p = row_plan(f, expert_offsets, sorted_slot, ws, L, device_status);
+    if (!dense) {
+        GatherArgs ga;
+        ga.plan = p;
+        ga.src[0] = u; ga.ld[0] = ldu; ga.dst[0] = at<void>(ws, L.up);
+        ga.K = f.K; ga.es = f.es;
+        MOE_CUDA(launch_gather_padded(ga, s));
+    }
+    GemmArgs g;
+    g.kind = kNT;
+    g.plan = p;
+    g.dtype = f.dtype;
+    g.a = dense ? u : at<void>(ws, L.up); g.lda = dense ? ldu : f.K;
+    g.ldb = f.K; g.sb = int64_t(f.I) * f.K * (f.il ? 2 : 1);
+    g.b = f.il ? w->gate_up_w : w->gate_w;
+    if (!f.il) {
+        g.b1 = w->up_w;
+        g.split = f.I;
+    }
+    if (f.bias) {
+        g.bias = f.il ? w->gate_up_b : w->gate_b;
+        g.bias1 = f.il ? nullptr : w->up_b;
+        g.sbias = int64_t(f.I) * (f.il ? 2 : 1);
+    }
+    g.M = f.T; g.N = 2 * f.I; g.R = f.K;
+    g.out = at<void>(ws, L.gp); g.ldo = 2 * f.I; g.out_f32 = 1;
+    MOE_CUDA(launch_simt_gemm(g, s));
+    GatedArgs ga;
+    ga.plan = p;
+    ga.I = f.I; ga.interleaved = f.il; ga.act = cfg->activation; ga.limit = cfg->swiglu_limit;
+    ga.alpha = cfg->swiglu_alpha;
+    ga.dtype = f.dtype;
+    ga.gp = at<float>(ws, L.gp);
+    ga.pre = pre;
+    ga.h = at<void>(ws, L.h);
+    MOE_CUDA(launch_gated_forward(ga, s));
+    GemmArgs o;
+    o.kind = kNT;
+    o.plan = p;
+    o.dtype = f.dtype;
+    o.a = ga.h; o.lda = f.I;
+    o.b = w->down_w; o.ldb = f.I; o.sb = int64_t(f.K) * f.I;
+    o.M = f.T; o.N = f.K; o.R = f.I;
+    if (f.bias) {
+        o.bias = w->down_b;
+        o.sbias = f.K;
+    }
+    if (dense) {
+        o.residual = residual; o.ldr = ldr;
+        o.out = y; o.ldo = ldy;
+        MOE_CUDA(launch_simt_gemm(o, s));
+        return MOE_OK;
+    }
+    o.row_scale = topk_w;
+    o.out = at<void>(ws, L.rows_out); o.ldo = f.K;
+    MOE_CUDA(launch_simt_gemm(o, s));
+    SumSlotsArgs sa;
+    sa.plan = p;
+    sa.rows = o.out;
+    sa.residual = residual; sa.ldr = ldr;
+    sa.out = y; sa.ldo = ldy;
+    sa.K = f.K;
+    sa.dtype = f.dtype;
+    MOE_CUDA(launch_sum_slots(sa, s));
+    return MOE_OK;
+}
+
+moe_status moe_ffn_backward(const moe_config* cfg, const moe_weights* w, const void* u, int64_t ldu, int64_t T,
+                            const int32_t* expert_offsets, const int32_t* sorted_slot, const float* topk_w,
+                            const void* pre, const void* dy, int64_t lddy, void* du, int64_t lddu, float* dtopk_w,
+                            const moe_ffn_grads* gr, void* ws, size_t ws_bytes, int32_t* device_status,
+                            moe_stream_t stream) {
+    bool dense;
+    FfnShape f;
+    MOE_CHECK(check_routing(expert_offsets, sorted_slot, topk_w, T, &dense));
+    MOE_CHECK(check_ffn(cfg, T, dense, &f));
+    if (!w || !gr) return MOE_ERR_INVALID_ARGUMENT;
+    if (dense && dtopk_w) return MOE_ERR_INVALID_ARGUMENT;
+    MOE_CHECK(check_planes(f, w->gate_w, w->up_w, w->gate_up_w, w->gate_b, w->up_b, w->gate_up_b, w->down_w,
+                           w->down_b));
+    MOE_CHECK(check_planes(f, gr->gate_w, gr->up_w, gr->gate_up_w, gr->gate_b, gr->up_b, gr->gate_up_b, gr->down_w,
+                           gr->down_b));
+    cudaStream_t s = (cudaStream_t)stream;
+    const size_t plane = size_t(f.E) * f.I * f.K * f.es;
+    if (T == 0) {
+        if (f.il) {
+            MOE_CUDA(cudaMemsetAsync(gr->gate_up_w, 0, 2 * plane, s));
+            if (f.bias) MOE_CUDA(cudaMemsetAsync(gr->gate_up_b, 0, size_t(f.E) * 2 * f.I * f.es, s));
+        } else {
+            MOE_CUDA(cudaMemsetAsync(gr->gate_w, 0, plane, s));
+            MOE_CUDA(cudaMemsetAsync(gr->up_w, 0, plane, s));
+            if (f.bias) {
+                MOE_CUDA(cudaMemsetAsync(gr->gate_b, 0, size_t(f.E) * f.I * f.es, s));
+                MOE_CUDA(cudaMemsetAsync(gr->up_b, 0, size_t(f.E) * f.I * f.es, s));
+            }
+        }
+        MOE_CUDA(cudaMemsetAsync(gr->down_w, 0, plane, s));
+        if (f.bias) MOE_CUDA(cudaMemsetAsync(gr->down_b, 0, size_t(f.E) * f.K * f.es, s));
+        return MOE_OK;
+    }
+    MOE_CHECK(need(u));
+    MOE_CHECK(need(dy));
+    MOE_CHECK(need(pre));
+    MOE_CHECK(maybe(du));
+    MOE_CHECK(maybe(dtopk_w));
+    MOE_CHECK(check_status_ptr(device_status));
+    MOE_CHECK(stride(ldu, f.K, f.dtype));
+    MOE_CHECK(stride(lddy, f.K, f.dtype));
+    if (du) MOE_CHECK(stride(lddu, f.K, f.dtype));
+    const FfnWs L = ffn_ws(f, true);
+    MOE_CHECK(check_ws(ws, ws_bytes, L.total));
+    const RowPlan p = row_plan(f, expert_offsets, sorted_slot, ws, L, device_status);
+    const void *up = u, *dyp = dy;
+    int64_t ldup = ldu, lddyp = lddy;
+    if (!dense) {
+        GatherArgs ga;
+        ga.plan = p;
+        ga.src[0] = u; ga.ld[0] = ldu; ga.dst[0] = at<void>(ws, L.up);
+        ga.src[1] = dy; ga.ld[1] = lddy; ga.dst[1] = at<void>(ws, L.dyp);
+        ga.K = f.K; ga.es = f.es;
+        MOE_CUDA(launch_gather_padded(ga, s));
+        up = ga.dst[0];
+        dyp = ga.dst[1];
+        ldup = lddyp = f.K;
+        // slots without a row (dropped) have no gradient
+        if (dtopk_w) MOE_CUDA(cudaMemsetAsync(dtopk_w, 0, size_t(f.S) * 4, s));
+    }
+    // dh = dy Wd
+    GemmArgs g;
+    g.kind = kNN;
+    g.plan = p;
+    g.dtype = f.dtype;
+    g.a = dyp; g.lda = lddyp;
+    g.b = w->down_w; g.ldb = f.I; g.sb = int64_t(f.K) * f.I;
+    g.M = f.T; g.N = f.I; g.R = f.K;
+    g.out = at<void>(ws, L.dh); g.ldo = f.I; g.out_f32 = 1;
+    MOE_CUDA(launch_simt_gemm(g, s));
+    GatedArgs ga;
+    ga.plan = p;
+    ga.I = f.I; ga.interleaved = f.il; ga.act = cfg->activation; ga.limit = cfg->swiglu_limit;
+    ga.alpha = cfg->swiglu_alpha;
+    ga.dtype = f.dtype;
+    ga.dh = at<float>(ws, L.dh);
+    ga.topk_w = topk_w;
+    ga.pre = const_cast<void*>(pre);
+    ga.dgu = at<void>(ws, L.dgu);
+    ga.hw = at<void>(ws, L.hw);
+    ga.dtopk_w = dtopk_w;
+    ga.dyp = dyp;
+    ga.down_b = f.bias ? w->down_b : nullptr;
+    ga.K = f.K;
+    MOE_CUDA(launch_gated_backward(ga, s));
+    // du = dg Wg + dv Wu
+    if (du) {
+        GemmArgs x;
+        x.kind = kNN;
+        x.plan = p;
+        x.dtype = f.dtype;
+        x.a = ga.dgu; x.lda = 2 * f.I;
+        x.b = f.il ? w->gate_up_w : w->gate_w; x.ldb = f.K; x.sb = int64_t(f.I) * f.K * (f.il ? 2 : 1);
+        if (!f.il) {
+            x.b1 = w->up_w;
+            x.split = f.I;
+        }
+        x.M = f.T; x.N = f.K; x.R = 2 * f.I;
+        x.out = dense ? du : at<void>(ws, L.rows_out); x.ldo = dense ? lddu : f.K;
+        MOE_CUDA(launch_simt_gemm(x, s));
+        if (!dense) {
+            SumSlotsArgs sa;
+            sa.plan = p;
+            sa.rows = x.out;
+            sa.out = du; sa.ldo = lddu;
+            sa.K = f.K;
+            sa.dtype = f.dtype;
+            MOE_CUDA(launch_sum_slots(sa, s));
+        }
+    }
+    // dWd = dy^T (w h),  [dWg; dWu] = [dg dv]^T u
+    GemmArgs t;
+    t.kind = kTN;
+    t.plan = p;
+    t.dtype = f.dtype;
+    t.a = dyp; t.lda = lddyp;
+    t.b = ga.hw; t.ldb = f.I;
+    t.M = f.K; t.N = f.I; t.R = f.T;
+    t.out = gr->down_w; t.ldo = f.I; t.so = int64_t(f.K) * f.I;
+    MOE_CUDA(launch_simt_gemm(t, s));
+    t.a = ga.dgu; t.lda = 2 * f.I;
+    t.b = up; t.ldb = ldup;
+    t.M = 2 * f.I; t.N = f.K;
+    t.out = f.il ? gr->gate_up_w : gr->gate_w; t.ldo = f.K; t.so = int64_t(f.I) * f.K * (f.il ? 2 : 1);
+    if (!f.il) {
+        t.out1 = gr->up_w;
+        t.split = f.I;
+    }
+    MOE_CUDA(launch_simt_gemm(t, s));
+    if (f.bias) {
+        ColsumArgs c;
+        c.plan = p;
+        c.dtype = f.dtype;
+        c.partial = at<float>(ws, L.partial);
+        c.x = ga.dgu; c.ldx = 2 * f.I; c.cols = 2 * f.I;
+        c.out = f.il ? gr->gate_up_b : gr->gate_b; c.so = int64_t(f.I) * (f.il ? 2 : 1);
+        if (!f.il) {
+            c.out1 = gr->up_b;
+            c.split = f.I;
+        }
+        MOE_CUDA(launch_colsum(c, s));
+        c.x = dyp; c.ldx = lddyp; c.cols = f.K;
+        c.row_scale = topk_w;
+        c.out = gr->down_b; c.so = f.K;
+        c.out1 = nullptr;
+        c.split = 0;
+        MOE_CUDA(launch_colsum(c, s));
+    }
+    return MOE_OK;
+}
+
+}  // extern "C"
+
+namespace {
+moe_status check_norm(const moe_norm_desc* d, int64_t T) {
+    if (!d || d->width <= 0) return MOE_ERR_INVALID_ARGUMENT;
+    if (d->kind != MOE_NORM_LAYER && d->kind != MOE_NORM_RMS) return MOE_ERR_INVALID_ARGUMENT;
+    if (d->dtype != MOE_DTYPE_F32 && d->dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARGUMENT;
+    if (!std::isfinite(d->eps) || d->eps <= 0.f) return MOE_ERR_INVALID_ARGUMENT;
+    if (d->width % (16 / esize(d->dtype))) return MOE_ERR_INVALID_ARGUMENT;
+    if (T < 0) return MOE_ERR_INVALID_ARGUMENT;
+    if (T > kMaxRows || T * d->width > kMaxElems) return MOE_ERR_SHAPE_OVERFLOW;
+    return MOE_OK;
+}
+size_t norm_ws(const moe_norm_desc* d, int64_t T, bool backward) {
+    return backward && T > 0 ? align256(size_t(norm_blocks(T, d->width)) * 2 * d->width * 4) : 0;
+}
+}  // namespace
+
+extern "C" {
+
+moe_status moe_norm_workspace_size(const moe_norm_desc* d, int64_t T, int32_t backward, size_t* bytes) {
+    MOE_CHECK(check_norm(d, T));
+    if (!bytes) return MOE_ERR_INVALID_ARGUMENT;
+    *bytes = norm_ws(d, T, backward != 0);
+    return MOE_OK;
+}
+
+moe_status moe_norm_forward(const moe_norm_desc* d, const void* x, int64_t ldx, const void* w, const void* b,
+                            int64_t T, void* y, int64_t ldy, float* stats, moe_stream_t stream) {
+    MOE_CHECK(check_norm(d, T));
+    if (b && d->kind == MOE_NORM_RMS) return MOE_ERR_INVALID_ARGUMENT;
+    if (T == 0) return MOE_OK;
+    MOE_CHECK(need(x));
+    MOE_CHECK(need(w));
+    MOE_CHECK(maybe(b));
+    MOE_CHECK(need(y));
+    MOE_CHECK(maybe(stats));
+    MOE_CHECK(stride(ldx, d->width, d->dtype));
+    MOE_CHECK(stride(ldy, d->width, d->dtype));
+    NormArgs a;
+    a.T = T; a.H = d->width; a.kind = d->kind; a.dtype = d->dtype; a.eps = d->eps;
+    a.x = x; a.ldx = ldx; a.w = w; a.b = b;
+    a.y = y; a.ldy = ldy;
+    a.stats = stats;
+    MOE_CUDA(launch_norm_forward(a, (cudaStream_t)stream));
+    return MOE_OK;
+}
+
+moe_status moe_norm_backward(const moe_norm_desc* d, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                             const void* w, const float* stats, int64_t T, void* dx, int64_t lddx, void* dw, void* db,
+                             void* ws, size_t ws_bytes, moe_stream_t stream) {
+    MOE_CHECK(check_norm(d, T));
+    if (db && d->kind == MOE_NORM_RMS) return MOE_ERR_INVALID_ARGUMENT;
+    MOE_CHECK(maybe(dx));
+    MOE_CHECK(maybe(dw));
+    MOE_CHECK(maybe(db));
+    cudaStream_t s = (cudaStream_t)stream;
+    if (T == 0) {
+        if (dw) MOE_CUDA(cudaMemsetAsync(dw, 0, size_t(d->width) * esize(d->dtype), s));
+        if (db) MOE_CUDA(cudaMemsetAsync(db, 0, size_t(d->width) * esize(d->dtype), s));
+        return MOE_OK;
+    }
+    MOE_CHECK(need(dy));
+    MOE_CHECK(need(x));
+    MOE_CHECK(need(w));
+    MOE_CHECK(need(stats));
+    MOE_CHECK(stride(lddy, d->width, d->dtype));
+    MOE_CHECK(stride(ldx, d->width, d->dtype));
+    if (dx) MOE_CHECK(stride(lddx, d->width, d->dtype));
+    MOE_CHECK(check_ws(ws, ws_bytes, norm_ws(d, T, true)));
+    NormArgs a;
+    a.T = T; a.H = d->width; a.kind = d->kind; a.dtype = d->dtype; a.eps = d->eps;
+    a.x = x; a.ldx = ldx; a.w = w;
+    a.dy = dy; a.lddy = lddy;
+    a.cstats = stats;
+    a.dx = dx; a.lddx = lddx;
+    a.dw = dw; a.db = db;
+    a.partial = static_cast<float*>(ws);
+    MOE_CUDA(launch_norm_backward(a, s));
+    return MOE_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,384 @@
+// train_rows.cu -- the padded row order of routed slots, and the row and column passes of the
+// training operators: gather, per-token sum over slots, the gated activation and its
+// derivative, column sums (bias gradients). All bound by HBM; every sum has a fixed order.
+#include <algorithm>
+
+#include "permute_dev.cuh"
+#include "train_dev.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kGatherThreads = 512;
+
+// Every block derives the padded order from the offsets itself (E <= 512: one scan in shared
+// memory), so that building the plan needs no launch of its own; block 0 writes it down.
+// Offsets that are not a rising sequence within [0, S] give an empty plan and the status.
+__global__ void __launch_bounds__(kGatherThreads) gather_padded_kernel(const GatherArgs a) {
+    __shared__ int32_t cnt[kPermE], start[kPermE], pad[kPermE + 1];
+    __shared__ int warp_tot[kGatherThreads / 32 + 1];
+    const RowPlan& p = a.plan;
+    const int tid = threadIdx.x;
+    int bad = 0;
+    for (int e = tid; e < p.E; e += kGatherThreads) {
+        const int lo = p.offsets[e], hi = p.offsets[e + 1];
+        bad |= lo < 0 || hi < lo || hi > p.S;
+        start[e] = lo;
+        cnt[e] = hi - lo;
+    }
+    bad = __syncthreads_or(bad);
+    for (int e = tid; e < p.E; e += kGatherThreads) {
+        if (bad) cnt[e] = start[e] = 0;
+        pad[e] = (cnt[e] + kRowTile - 1) / kRowTile * kRowTile;
+    }
+    __syncthreads();
+    const int total = block_exclusive_scan<kGatherThreads>(pad, p.E, warp_tot);
+    if (tid == 0) pad[p.E] = total;
+    if (blockIdx.x == 0) {
+        for (int e = tid; e < p.E; e += kGatherThreads) {
+            p.poff[e] = pad[e];
+            p.uoff[e] = start[e];
+        }
+        if (tid == 0) {
+            p.poff[p.E] = total;
+            p.uoff[p.E] = p.E ? start[p.E - 1] + cnt[p.E - 1] : 0;
+            if (bad) set_status(p.status, MOE_ERR_DEVICE_CHECK);
+        }
+    }
+    __syncthreads();
+    const int lane = tid & 31;
+    const int64_t vpr = int64_t(a.K) * a.es / 16;
+    const int warps = gridDim.x * (kGatherThreads / 32);
+    for (int r = blockIdx.x * (kGatherThreads / 32) + (tid >> 5); r < total; r += warps) {
+        const int e = expert_of_row(pad, p.E, r);
+        const int i = r - pad[e];
+        int slot = -1;
+        if (i < cnt[e]) {
+            slot = p.sorted_slot[start[e] + i];
+            if (slot < 0 || slot >= p.S) {
+                if (lane == 0) set_status(p.status, MOE_ERR_DEVICE_CHECK);
+                slot = -1;
+            }
+        }
+        if (lane == 0) {
+            p.row_slot[r] = slot;
+            if (slot >= 0) p.slot_row[slot] = r;
+        }
+        const int64_t t = slot < 0 ? 0 : slot / p.k;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (!a.src[j]) continue;
+            const uint4* s = reinterpret_cast<const uint4*>(static_cast<const char*>(a.src[j]) + t * a.ld[j] * a.es);
+            uint4* d = static_cast<uint4*>(a.dst[j]) + int64_t(r) * vpr;
+            if (slot < 0) {
+                for (int c = lane; c < vpr; c += 32) d[c] = make_uint4(0, 0, 0, 0);
+            } else {
+                int c = lane;
+                for (; c + 96 < vpr; c += 128) {  // four vectors in flight per lane
+                    const uint4 v0 = __ldg(s + c), v1 = __ldg(s + c + 32), v2 = __ldg(s + c + 64), v3 = __ldg(s + c + 96);
+                    d[c] = v0; d[c + 32] = v1; d[c + 64] = v2; d[c + 96] = v3;
+                }
+                for (; c < vpr; c += 32) d[c] = __ldg(s + c);
+            }
+        }
+    }
+}
+
+// One block row per token: its slots' rows added in slot order in f32.
+template <typename T>
+__global__ void __launch_bounds__(256) sum_slots_kernel(const SumSlotsArgs a) {
+    constexpr int V = Vec<T>::N;
+    const int vpr = a.K / V;
+    const int64_t n = a.plan.T * vpr;
+    for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x) {
+        const int64_t t = i / vpr;
+        const int c = int(i - t * vpr) * V;
+        float acc[V] = {};
+        const int32_t* sr = a.plan.slot_row + t * a.plan.k;
+        for (int j = 0; j < a.plan.k; ++j) {
+            const int r = sr[j];
+            if (r < 0) continue;
+            float f[V];
+            load_vec(static_cast<const T*>(a.rows) + int64_t(r) * a.K + c, f);
+#pragma unroll
+            for (int q = 0; q < V; ++q) acc[q] += f[q];
+        }
+        if (a.residual) {
+            float f[V];
+            load_vec(static_cast<const T*>(a.residual) + t * a.ldr + c, f);
+#pragma unroll
+            for (int q = 0; q < V; ++q) acc[q] += f[q];
+        }
+        store_vec(static_cast<T*>(a.out) + t * a.ldo + c, acc);
+    }
+}
+
+// Rows of the plan: how many, and per row its slot and its row in the caller's sorted order
+// (-1 for padding).
+struct RowRef {
+    int e;
+    int64_t pos;  // caller's sorted position, or -1
+    int slot;
+};
+__device__ __forceinline__ int64_t plan_rows(const RowPlan& p) { return p.offsets ? p.poff[p.E] : p.T; }
+__device__ __forceinline__ RowRef row_ref(const RowPlan& p, int64_t r) {
+    RowRef o;
+    if (!p.offsets) {
+        o.e = 0;
+        o.pos = r;
+        o.slot = int(r);
+        return o;
+    }
+    o.slot = p.row_slot[r];
+    o.e = expert_of_row(p.poff, p.E, int(r));
+    o.pos = o.slot < 0 ? -1 : int64_t(p.uoff[o.e]) + (r - p.poff[o.e]);
+    return o;
+}
+
+// One warp per row; gate and up of unit i.
+template <typename T>
+__global__ void __launch_bounds__(256) gated_forward_kernel(const GatedArgs a) {
+    constexpr bool FAST = Vec<T>::N == 8;
+    const int lane = threadIdx.x & 31;
+    const int64_t rows = plan_rows(a.plan), warps = int64_t(gridDim.x) * 8;
+    for (int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); r < rows; r += warps) {
+        const RowRef o = row_ref(a.plan, r);
+        const float* gp = a.gp + r * 2 * a.I;
+        T* h = static_cast<T*>(a.h) + r * a.I;
+        T* pre = a.pre && o.pos >= 0 ? static_cast<T*>(a.pre) + o.pos * 2 * a.I : nullptr;
+        for (int i = lane; i < a.I; i += 32) {
+            const int cg = a.interleaved ? 2 * i : i, cv = a.interleaved ? 2 * i + 1 : a.I + i;
+            const float g = gp[cg], v = gp[cv];
+            h[i] = from_f<T>(gated_h<FAST>(a.act, g, v, a.limit, a.alpha));
+            if (pre) {
+                pre[cg] = from_f<T>(g);
+                pre[cv] = from_f<T>(v);
+            }
+        }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) gated_backward_kernel(const GatedArgs a) {
+    constexpr bool FAST = Vec<T>::N == 8;
+    const int lane = threadIdx.x & 31;
+    const int64_t rows = plan_rows(a.plan), warps = int64_t(gridDim.x) * 8;
+    for (int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); r < rows; r += warps) {
+        const RowRef o = row_ref(a.plan, r);
+        T* dgu = static_cast<T*>(a.dgu) + r * 2 * a.I;
+        T* hw = static_cast<T*>(a.hw) + r * a.I;
+        const T* pre = static_cast<const T*>(a.pre) + o.pos * 2 * a.I;
+        const float wt = a.topk_w && o.slot >= 0 ? a.topk_w[o.slot] : 1.0f;
+        float dw = 0.0f;
+        for (int i = lane; i < a.I; i += 32) {
+            const int cg = a.interleaved ? 2 * i : i, cv = a.interleaved ? 2 * i + 1 : a.I + i;
+            float dg = 0.f, dv = 0.f, hh = 0.f;
+            if (o.pos >= 0) {
+                float hg, hv;
+                gated_grad<FAST>(a.act, to_f<T>(pre[cg]), to_f<T>(pre[cv]), a.limit, a.alpha, hh, hg, hv);
+                const float d = a.dh[r * a.I + i];
+                dw += d * hh;
+                dg = d * wt * hg;
+                dv = d * wt * hv;
+                hh *= wt;
+            }
+            dgu[cg] = from_f<T>(dg);
+            dgu[cv] = from_f<T>(dv);
+            hw[i] = from_f<T>(hh);
+        }
+        if (!a.dtopk_w || o.slot < 0) continue;
+        if (a.down_b)
+            for (int c = lane; c < a.K; c += 32)
+                dw += to_f<T>(static_cast<const T*>(a.dyp)[r * a.K + c]) *
+                      to_f<T>(static_cast<const T*>(a.down_b)[int64_t(o.e) * a.K + c]);
+        dw = warp_sum(dw);
+        if (lane == 0) a.dtopk_w[o.slot] = dw;
+    }
+}
+
+// Column sums, first pass: block (x: 64 16-byte column vectors' worth, y: expert, z: split of
+// the expert's rows). Each thread owns one vector of columns and every 4th row of the split.
+constexpr int kColVecs = 64, kColRows = 4;
+template <typename T>
+__global__ void __launch_bounds__(kColVecs * kColRows) colsum_kernel(const ColsumArgs a, int splits) {
+    constexpr int V = Vec<T>::N;
+    const int e = blockIdx.y, z = blockIdx.z;
+    int64_t r0 = 0, r1 = a.plan.T;
+    if (a.plan.offsets) {
+        r0 = a.plan.poff[e];
+        r1 = a.plan.poff[e + 1];
+    }
+    const int64_t per = (r1 - r0 + splits - 1) / splits;
+    const int64_t b = r0 + z * per, end = min(r1, b + per);
+    const int c = (blockIdx.x * kColVecs + threadIdx.x % kColVecs) * V;
+    const int ry = threadIdx.x / kColVecs;
+    float acc[V] = {};
+    if (c < a.cols) {
+        for (int64_t r = b + ry; r < end; r += kColRows) {
+            float f[V];
+            load_vec(static_cast<const T*>(a.x) + r * a.ldx + c, f);
+            float sc = 1.0f;
+            if (a.row_scale) {
+                const int slot = a.plan.row_slot[r];
+                if (slot < 0) continue;
+                sc = a.row_scale[slot];
+            }
+#pragma unroll
+            for (int q = 0; q < V; ++q) acc[q] += f[q] * sc;
+        }
+    }
+    __shared__ float sm[kColRows][kColVecs][V + 1];
+#pragma unroll
+    for (int q = 0; q < V; ++q) sm[ry][threadIdx.x % kColVecs][q] = acc[q];
+    __syncthreads();
+    if (ry == 0 && c < a.cols) {
+        float* o = a.partial + (int64_t(z) * a.plan.E + e) * a.cols + c;
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+            float s = 0.f;
+#pragma unroll
+            for (int y = 0; y < kColRows; ++y) s += sm[y][threadIdx.x][q];
+            o[q] = s;
+        }
+    }
+}
+
+// Second pass: the splits' partial sums added in order and rounded once.
+template <typename T>
+__global__ void __launch_bounds__(256) colsum_finish_kernel(const ColsumArgs a, int splits) {
+    const int64_t n = int64_t(a.plan.E) * a.cols;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
+        float s = 0.f;
+        for (int z = 0; z < splits; ++z) s += a.partial[z * n + i];
+        const int64_t e = i / a.cols;
+        const int c = int(i - e * a.cols);
+        T* o = a.split && c >= a.split ? static_cast<T*>(a.out1) + e * a.so + (c - a.split)
+                                       : static_cast<T*>(a.out) + e * a.so + c;
+        *o = from_f<T>(s);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kColVecs * kColRows) dact_kernel(const DactArgs a, int splits) {
+    constexpr int V = Vec<T>::N;
+    constexpr bool FAST = V == 8;
+    const int64_t per = (a.T + splits - 1) / splits;
+    const int64_t b = blockIdx.y * per, end = min(a.T, b + per);
+    const int c = (blockIdx.x * kColVecs + threadIdx.x % kColVecs) * V;
+    const int ry = threadIdx.x / kColVecs;
+    float acc[V] = {};
+    if (c < a.N) {
+        for (int64_t r = b + ry; r < end; r += kColRows) {
+            float f[V];
+            load_vec(static_cast<const T*>(a.dy) + r * a.lddy + c, f);
+            if (a.act != MOE_LINEAR_NONE) {
+                float z[V];
+                load_vec(static_cast<const T*>(a.pre) + r * a.N + c, z);
+#pragma unroll
+                for (int q = 0; q < V; ++q) f[q] *= linear_dact<FAST>(a.act, z[q]);
+                store_vec(static_cast<T*>(a.dz) + r * a.N + c, f);
+            }
+#pragma unroll
+            for (int q = 0; q < V; ++q) acc[q] += f[q];
+        }
+    }
+    if (!a.partial) return;
+    __shared__ float sm[kColRows][kColVecs][V + 1];
+#pragma unroll
+    for (int q = 0; q < V; ++q) sm[ry][threadIdx.x % kColVecs][q] = acc[q];
+    __syncthreads();
+    if (ry == 0 && c < a.N) {
+        float* o = a.partial + int64_t(blockIdx.y) * a.N + c;
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+            float s = 0.f;
+#pragma unroll
+            for (int y = 0; y < kColRows; ++y) s += sm[y][threadIdx.x][q];
+            o[q] = s;
+        }
+    }
+}
+
+unsigned grid_for(int64_t items, int64_t per_block, int64_t most) {
+    return unsigned(std::max<int64_t>(1, std::min(most, (items + per_block - 1) / per_block)));
+}
+
+}  // namespace
+
+cudaError_t launch_gather_padded(const GatherArgs& a, cudaStream_t s) {
+    const cudaError_t e = cudaMemsetAsync(a.plan.slot_row, 0xFF, size_t(a.plan.S) * 4, s);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = grid_for(a.plan.max_rows, kGatherThreads / 32, 148 * 4);
+    gather_padded_kernel<<<grid, kGatherThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_sum_slots(const SumSlotsArgs& a, cudaStream_t s) {
+    const int V = a.dtype == MOE_DTYPE_F32 ? 4 : 8;
+    const unsigned grid = grid_for(a.plan.T * (a.K / V), 256, 148 * 16);
+    if (a.dtype == MOE_DTYPE_F32) sum_slots_kernel<float><<<grid, 256, 0, s>>>(a);
+    else sum_slots_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_gated_forward(const GatedArgs& a, cudaStream_t s) {
+    const unsigned grid = grid_for(a.plan.max_rows, 8, 148 * 8);
+    if (a.dtype == MOE_DTYPE_F32) gated_forward_kernel<float><<<grid, 256, 0, s>>>(a);
+    else gated_forward_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_gated_backward(const GatedArgs& a, cudaStream_t s) {
+    const unsigned grid = grid_for(a.plan.max_rows, 8, 148 * 8);
+    if (a.dtype == MOE_DTYPE_F32) gated_backward_kernel<float><<<grid, 256, 0, s>>>(a);
+    else gated_backward_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+// Enough blocks to fill the GPU, at least 64 rows each.
+int colsum_splits(int64_t rows, int E, int cols) {
+    const int64_t cb = (cols + 511) / 512;
+    const int64_t want = std::max<int64_t>(1, 592 / (cb * E));
+    return int(std::max<int64_t>(1, std::min<int64_t>(want, rows / E / 64)));
+}
+
+cudaError_t launch_colsum(const ColsumArgs& a, cudaStream_t s) {
+    const int V = a.dtype == MOE_DTYPE_F32 ? 4 : 8;
+    const int splits = colsum_splits(a.plan.max_rows, a.plan.E, a.cols);
+    const dim3 grid((a.cols / V + kColVecs - 1) / kColVecs, a.plan.E, splits);
+    const unsigned fin = grid_for(int64_t(a.plan.E) * a.cols, 256, 148 * 8);
+    if (a.dtype == MOE_DTYPE_F32) {
+        colsum_kernel<float><<<grid, kColVecs * kColRows, 0, s>>>(a, splits);
+        colsum_finish_kernel<float><<<fin, 256, 0, s>>>(a, splits);
+    } else {
+        colsum_kernel<__nv_bfloat16><<<grid, kColVecs * kColRows, 0, s>>>(a, splits);
+        colsum_finish_kernel<__nv_bfloat16><<<fin, 256, 0, s>>>(a, splits);
+    }
+    return cudaGetLastError();
+}
+
+int dact_splits(int64_t T, int N) {
+    const int64_t cb = (N + 511) / 512;
+    return int(std::max<int64_t>(1, std::min<int64_t>(592 / cb, T / 16)));
+}
+
+cudaError_t launch_dact(const DactArgs& a, cudaStream_t s) {
+    const int V = a.dtype == MOE_DTYPE_F32 ? 4 : 8;
+    const int splits = dact_splits(a.T, a.N);
+    const dim3 grid((a.N / V + kColVecs - 1) / kColVecs, splits);
+    if (a.dtype == MOE_DTYPE_F32) dact_kernel<float><<<grid, kColVecs * kColRows, 0, s>>>(a, splits);
+    else dact_kernel<__nv_bfloat16><<<grid, kColVecs * kColRows, 0, s>>>(a, splits);
+    if (a.partial) {
+        ColsumArgs c;
+        c.cols = a.N;
+        c.out = a.db;
+        c.partial = a.partial;
+        const unsigned fin = grid_for(a.N, 256, 148 * 8);
+        if (a.dtype == MOE_DTYPE_F32) colsum_finish_kernel<float><<<fin, 256, 0, s>>>(c, splits);
+        else colsum_finish_kernel<__nv_bfloat16><<<fin, 256, 0, s>>>(c, splits);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace moe

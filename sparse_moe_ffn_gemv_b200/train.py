@@ -1,0 +1,338 @@
+"""Python binding of include/moe_train.h: the operators that train the block.
+
+    Linear    y = act(x W^T + b) + r        forward, backward
+    GatedFfn  the routed experts of a MoeSpec, or one dense gated FFN   forward, backward
+    Norm      layer norm, RMS norm          forward, backward
+
+Argument marshalling only: every step runs in the library's CUDA kernels. A handle holds the
+operator's shape and one status word; weights are passed at each call (a training step changes
+them), outputs and workspaces come from PyTorch's allocator at each call, so calls on several
+streams and captured graphs share nothing but the status word. Tensors are [rows, width], rows
+may be strided. A call runs on `stream`, or on the current stream of the handle's device.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import functools
+from typing import Dict, Optional, Tuple
+
+import torch
+
+from . import inputs
+from . import moe as M
+
+# The entry points include/moe_train.h declares.
+EXPORTS = [
+    "moe_linear_workspace_size", "moe_linear_forward", "moe_linear_backward",
+    "moe_ffn_workspace_size", "moe_ffn_forward", "moe_ffn_backward",
+    "moe_norm_workspace_size", "moe_norm_forward", "moe_norm_backward",
+]
+
+LINEAR_ACTIVATION = {"none": 0, "silu": 1, "gelu": 2}
+NORM_KIND = {"layer": 0, "rms": 1}
+GRAD_FIELDS = ["gate_w", "up_w", "gate_up_w", "gate_b", "up_b", "gate_up_b", "down_w", "down_b"]
+_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+class MoeLinearDesc(ctypes.Structure):
+    _fields_ = [("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class MoeNormDesc(ctypes.Structure):
+    _fields_ = [("width", ctypes.c_int32), ("kind", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+class MoeFfnGrads(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in GRAD_FIELDS]
+
+
+@functools.lru_cache(maxsize=None)
+def lib():
+    """The loaded library with this header's signatures."""
+    L = M.lib()
+    vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+    szp = ctypes.POINTER(ctypes.c_size_t)
+    lin, nrm = ctypes.POINTER(MoeLinearDesc), ctypes.POINTER(MoeNormDesc)
+    cfg, wts, gr = ctypes.POINTER(M.MoeConfig), ctypes.POINTER(M.MoeWeights), ctypes.POINTER(MoeFfnGrads)
+    sig = {
+        "moe_linear_workspace_size": [lin, i64, i32, szp],
+        "moe_linear_forward": [lin, vp, i64, vp, vp, vp, i64, i64, vp, i64, vp, vp, sz, vp, vp],
+        "moe_linear_backward": [lin, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, sz, vp, vp],
+        "moe_ffn_workspace_size": [cfg, i64, i32, szp],
+        "moe_ffn_forward": [cfg, wts, vp, i64, i64, vp, vp, vp, vp, i64, vp, i64, vp, vp, sz, vp, vp],
+        "moe_ffn_backward": [cfg, wts, vp, i64, i64, vp, vp, vp, vp, vp, i64, vp, i64, vp, gr, vp, sz, vp, vp],
+        "moe_norm_workspace_size": [nrm, i64, i32, szp],
+        "moe_norm_forward": [nrm, vp, i64, vp, vp, i64, vp, i64, vp, vp],
+        "moe_norm_backward": [nrm, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, sz, vp],
+    }
+    for name, args in sig.items():
+        fn = getattr(L, name)
+        fn.argtypes = args
+        fn.restype = ctypes.c_int
+    return L
+
+
+def _p(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+class _Operator:
+    """What the handles share: device, dtype, status word, checks, workspace, stream."""
+
+    def __init__(self, dtype: str, device):
+        if dtype not in _DTYPE:
+            raise ValueError(f"dtype {dtype!r}: 'f32' or 'bf16'")
+        self.dtype = _DTYPE[dtype]
+        self.device = torch.device(device)
+        if self.device.type != "cuda":
+            raise ValueError(f"device {device!r}: the operators run on CUDA devices")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.lib = lib()
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._ws_bytes: Dict[Tuple[int, int], int] = {}
+
+    def device_status(self) -> int:
+        """The status device-side checks left since the last call (0: none). Synchronises."""
+        v = int(self.status.item())
+        self.status.zero_()
+        return v
+
+    @contextlib.contextmanager
+    def _on(self, stream):
+        """The handle's device and the call's stream made current: what is allocated in the
+        call belongs to the stream that uses it."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                yield
+        else:
+            with torch.cuda.device(self.device):
+                yield
+
+    def _guard(self, stream):
+        if stream is None and torch.cuda.current_device() == self.device.index:
+            return contextlib.nullcontext()
+        if stream is not None and stream.device != self.device:
+            raise ValueError(f"stream of {stream.device}, handle of {self.device}")
+        return self._on(stream)
+
+    def _flat(self, name: str, t: torch.Tensor, numel: int, dtype=None) -> int:
+        """A contiguous tensor of a given size: its address."""
+        if t.dtype != (dtype or self.dtype) or t.device != self.device:
+            raise ValueError(f"{name}: {t.dtype} on {t.device}, wanted {dtype or self.dtype} on {self.device}")
+        if t.numel() != numel or not t.is_contiguous():
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, strides {t.stride()}; wanted {numel} contiguous values")
+        return t.data_ptr()
+
+    def _rows(self, name: str, t: torch.Tensor, width: int, rows: Optional[int] = None) -> Tuple[int, int]:
+        """A [rows, width] tensor with unit column stride: its address and row stride."""
+        if t.dtype != self.dtype or t.device != self.device:
+            raise ValueError(f"{name}: {t.dtype} on {t.device}, wanted {self.dtype} on {self.device}")
+        if t.dim() != 2 or t.shape[1] != width or (rows is not None and t.shape[0] != rows):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted [{'rows' if rows is None else rows}, {width}]")
+        n, st = t.shape[0], t.stride()
+        if n and width > 1 and st[1] != 1:
+            raise ValueError(f"{name}: strides {st}: the columns of a row must be contiguous")
+        return t.data_ptr(), st[0] if n > 1 else width
+
+    def _workspace(self, size_fn, desc, T: int, backward: int):
+        n = self._ws_bytes.get((T, backward))
+        if n is None:
+            out = ctypes.c_size_t(0)
+            M._check(size_fn(ctypes.byref(desc), T, backward, ctypes.byref(out)), size_fn.__name__)
+            if len(self._ws_bytes) >= 1024:
+                self._ws_bytes.clear()
+            n = self._ws_bytes[(T, backward)] = out.value
+        return (torch.empty(n, dtype=torch.uint8, device=self.device), n) if n else (None, 0)
+
+    def _empty(self, *shape, dtype=None):
+        return torch.empty(shape, dtype=dtype or self.dtype, device=self.device)
+
+    def _stream(self):
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+
+class Linear(_Operator):
+    """y = act(x W^T + b) + r with x [T, in], W [out, in] (moe_linear_forward / _backward)."""
+
+    def __init__(self, in_features: int, out_features: int, activation: str = "none", dtype: str = "bf16",
+                 device="cuda"):
+        if activation not in LINEAR_ACTIVATION:
+            raise ValueError(f"activation {activation!r}: one of {sorted(LINEAR_ACTIVATION)}")
+        super().__init__(dtype, device)
+        self.n_in, self.n_out, self.activation = in_features, out_features, activation
+        self.desc = MoeLinearDesc(in_features, out_features, LINEAR_ACTIVATION[activation], inputs.DTYPE[dtype])
+        self._workspace(self.lib.moe_linear_workspace_size, self.desc, 0, 0)  # checks the shape
+
+    def forward(self, x, w, bias=None, residual=None, keep: bool = False, out=None, stream=None):
+        """y, or (y, pre) with keep: pre = x W^T + b is what backward needs of an activation."""
+        with self._guard(stream):
+            T, K, N = x.shape[0], self.n_in, self.n_out
+            xp, ldx = self._rows("x", x, K)
+            wp = self._flat("w", w, N * K)
+            bp = None if bias is None else self._flat("bias", bias, N)
+            rp, ldr = (None, 0) if residual is None else self._rows("residual", residual, N, T)
+            y = self._empty(T, N) if out is None else out
+            yp, ldy = self._rows("out", y, N, T)
+            pre = self._empty(T, N) if keep else None
+            ws, n = self._workspace(self.lib.moe_linear_workspace_size, self.desc, T, 0)
+            M._check(self.lib.moe_linear_forward(ctypes.byref(self.desc), xp, ldx, wp, bp, rp, ldr, T, yp, ldy,
+                                                 _p(pre), _p(ws), n, self.status.data_ptr(), self._stream()),
+                     "moe_linear_forward")
+        return (y, pre) if keep else y
+
+    def backward(self, dy, x, w, pre=None, bias_grad: bool = True, input_grad: bool = True,
+                 weight_grad: bool = True, stream=None):
+        """(dx, dw, db); None for a gradient not asked for. A residual's gradient is dy."""
+        with self._guard(stream):
+            T, K, N = x.shape[0], self.n_in, self.n_out
+            gp, ldg = self._rows("dy", dy, N, T)
+            xp, ldx = self._rows("x", x, K)
+            wp = self._flat("w", w, N * K)
+            pp = None if pre is None else self._flat("pre", pre, T * N)
+            dx = self._empty(T, K) if input_grad else None
+            dw = self._empty(N, K) if weight_grad else None
+            db = self._empty(N) if bias_grad else None
+            ws, n = self._workspace(self.lib.moe_linear_workspace_size, self.desc, T, 1)
+            M._check(self.lib.moe_linear_backward(ctypes.byref(self.desc), gp, ldg, xp, ldx, wp, pp, T, _p(dx), K,
+                                                  _p(dw), _p(db), _p(ws), n, self.status.data_ptr(),
+                                                  self._stream()), "moe_linear_backward")
+        return dx, dw, db
+
+
+class GatedFfn(_Operator):
+    """The routed experts of a MoeSpec (f32 or bf16 planes), or, with one expert, top_k 1 and
+    no routing, a dense gated FFN (moe_ffn_forward / _backward).
+
+    weights: the planes by their moe_weights names (gate_w, up_w or gate_up_w, down_w, and the
+    biases of a spec with has_expert_bias); other entries are not read. routing:
+    (expert_offsets, sorted_slot, topk_w) from moe_route and moe_permute."""
+
+    def __init__(self, spec, device="cuda"):
+        super().__init__(spec.act_dtype, device)
+        self.spec = spec
+        self.cfg = M.config_from_spec(spec)
+        M._check(M.moe_config_validate(self.cfg), "moe_config_validate")
+        E, I, K = spec.num_experts, spec.intermediate, spec.expert_in
+        self.E, self.k, self.I, self.K = E, spec.top_k, I, K
+        self._workspace(self.lib.moe_ffn_workspace_size, self.cfg, 0, 0)  # checks the weight format
+        shapes = {"gate_up_w": (E, 2 * I, K)} if spec.gate_up_interleaved else {"gate_w": (E, I, K), "up_w": (E, I, K)}
+        shapes["down_w"] = (E, K, I)
+        if spec.has_expert_bias:
+            shapes.update({"gate_up_b": (E, 2 * I)} if spec.gate_up_interleaved else {"gate_b": (E, I), "up_b": (E, I)})
+            shapes["down_b"] = (E, K)
+        self.shapes = shapes
+        self._numel = {f: functools.reduce(int.__mul__, s) for f, s in shapes.items()}
+
+    def _planes(self, struct, tensors, what: str):
+        for f, n in self._numel.items():
+            t = tensors.get(f)
+            if t is None:
+                raise M.MoeError(M.STATUS_CODE["MOE_ERR_MISSING_TENSOR"], f"{what} {f}")
+            setattr(struct, f, self._flat(f, t, n))
+        return struct
+
+    def _routing(self, routing, T: int):
+        if routing is None:
+            if self.E != 1 or self.k != 1:
+                raise ValueError(f"{self.E} experts, top_k {self.k}: routing is needed")
+            return None, None, None
+        off, slots, wts = routing
+        return (self._flat("expert_offsets", off, self.E + 1, torch.int32),
+                self._flat("sorted_slot", slots, T * self.k, torch.int32),
+                self._flat("topk_w", wts, T * self.k, torch.float32))
+
+    def forward(self, u, weights: Dict[str, torch.Tensor], routing=None, residual=None, keep: bool = True,
+                out=None, stream=None):
+        """(y, pre): y [T, K], and the pre-activations [T*k, 2I] in sorted order that backward
+        takes (None without keep)."""
+        with self._guard(stream):
+            T = u.shape[0]
+            up, ldu = self._rows("u", u, self.K)
+            w = self._planes(M.MoeWeights(), weights, "weights")
+            off, slots, wts = self._routing(routing, T)
+            rp, ldr = (None, 0) if residual is None else self._rows("residual", residual, self.K, T)
+            y = self._empty(T, self.K) if out is None else out
+            yp, ldy = self._rows("out", y, self.K, T)
+            pre = self._empty(T * self.k, 2 * self.I) if keep else None
+            ws, n = self._workspace(self.lib.moe_ffn_workspace_size, self.cfg, T, 0)
+            M._check(self.lib.moe_ffn_forward(ctypes.byref(self.cfg), ctypes.byref(w), up, ldu, T, off, slots, wts, rp,
+                                              ldr, yp, ldy, _p(pre), _p(ws), n, self.status.data_ptr(),
+                                              self._stream()), "moe_ffn_forward")
+        return y, pre
+
+    def backward(self, dy, u, weights: Dict[str, torch.Tensor], pre, routing=None, input_grad: bool = True,
+                 stream=None) -> Dict[str, torch.Tensor]:
+        """Gradients by name: "x" (of u), "topk_w" (routed), and those of the weight planes."""
+        with self._guard(stream):
+            T = u.shape[0]
+            gp, ldg = self._rows("dy", dy, self.K, T)
+            up, ldu = self._rows("u", u, self.K)
+            w = self._planes(M.MoeWeights(), weights, "weights")
+            off, slots, wts = self._routing(routing, T)
+            pp = self._flat("pre", pre, T * self.k * 2 * self.I)
+            grads = {f: self._empty(*s) for f, s in self.shapes.items()}
+            g = MoeFfnGrads()
+            for f, t in grads.items():
+                setattr(g, f, t.data_ptr())
+            dwt = None if off is None else self._empty(T, self.k, dtype=torch.float32)
+            du = self._empty(T, self.K) if input_grad else None
+            ws, n = self._workspace(self.lib.moe_ffn_workspace_size, self.cfg, T, 1)
+            M._check(self.lib.moe_ffn_backward(ctypes.byref(self.cfg), ctypes.byref(w), up, ldu, T, off, slots, wts, pp,
+                                               gp, ldg, _p(du), self.K, _p(dwt), ctypes.byref(g), _p(ws), n,
+                                               self.status.data_ptr(), self._stream()), "moe_ffn_backward")
+        if du is not None:
+            grads["x"] = du
+        if dwt is not None:
+            grads["topk_w"] = dwt
+        return grads
+
+
+class Norm(_Operator):
+    """Layer norm or RMS norm over the last axis (moe_norm_forward / _backward)."""
+
+    def __init__(self, width: int, kind: str = "rms", eps: float = 1e-6, dtype: str = "bf16", device="cuda"):
+        if kind not in NORM_KIND:
+            raise ValueError(f"kind {kind!r}: one of {sorted(NORM_KIND)}")
+        super().__init__(dtype, device)
+        self.width, self.kind = width, kind
+        self.desc = MoeNormDesc(width, NORM_KIND[kind], inputs.DTYPE[dtype], eps)
+        self._workspace(self.lib.moe_norm_workspace_size, self.desc, 0, 0)  # checks the shape
+
+    def forward(self, x, w, bias=None, out=None, stream=None):
+        """(y, stats): stats [T, 2] f32 (mean, 1 / sqrt(var + eps)) is what backward takes."""
+        with self._guard(stream):
+            T, H = x.shape[0], self.width
+            xp, ldx = self._rows("x", x, H)
+            wp = self._flat("w", w, H)
+            bp = None if bias is None else self._flat("bias", bias, H)
+            y = self._empty(T, H) if out is None else out
+            yp, ldy = self._rows("out", y, H, T)
+            stats = self._empty(T, 2, dtype=torch.float32)
+            M._check(self.lib.moe_norm_forward(ctypes.byref(self.desc), xp, ldx, wp, bp, T, yp, ldy, stats.data_ptr(),
+                                               self._stream()), "moe_norm_forward")
+        return y, stats
+
+    def backward(self, dy, x, w, stats, bias_grad: Optional[bool] = None, input_grad: bool = True,
+                 stream=None):
+        """(dx, dw, db); db is None for RMS norm or with bias_grad False."""
+        with self._guard(stream):
+            T, H = x.shape[0], self.width
+            if bias_grad and self.kind == "rms":
+                raise ValueError("RMS norm has no bias")
+            if bias_grad is None:
+                bias_grad = self.kind == "layer"
+            gp, ldg = self._rows("dy", dy, H, T)
+            xp, ldx = self._rows("x", x, H)
+            wp = self._flat("w", w, H)
+            sp = self._flat("stats", stats, 2 * T, torch.float32)
+            dx = self._empty(T, H) if input_grad else None
+            dw = self._empty(H)
+            db = self._empty(H) if bias_grad else None
+            ws, n = self._workspace(self.lib.moe_norm_workspace_size, self.desc, T, 1)
+            M._check(self.lib.moe_norm_backward(ctypes.byref(self.desc), gp, ldg, xp, ldx, wp, sp, T, _p(dx), H,
+                                                _p(dw), _p(db), _p(ws), n, self._stream()), "moe_norm_backward")
+        return dx, dw, db
