@@ -95,8 +95,8 @@ MOE_API moe_status moe_ffn_workspace_size(const moe_config *cfg, int64_t T, int3
 
 /* y [T, K] (row stride ldy) from u [T, K] (row stride ldu), plus residual [T, K] (row stride
  * ldr) or NULL. pre (optional) is kept for the backward pass; its rows of dropped slots are
- * not written. bf16: h is rounded to bf16 before the down product, and for routed slots each
- * slot's weighted output row before the sum over the token's slots. */
+ * not written. bf16: h is rounded to bf16 before the down product (the operand type of the
+ * matrix instructions); the slots' weighted output rows are summed in f32. */
 MOE_API moe_status moe_ffn_forward(const moe_config *cfg, const moe_weights *w, const void *u, int64_t ldu,
                                    int64_t T, const int32_t *expert_offsets, const int32_t *sorted_slot,
                                    const float *topk_w, const void *residual, int64_t ldr, void *y, int64_t ldy,
@@ -107,8 +107,7 @@ MOE_API moe_status moe_ffn_forward(const moe_config *cfg, const moe_weights *w, 
  * (routed; may be NULL) and the gradients of the planes, [E, rows, cols] like the planes
  * (experts without rows get zeros). Required gradients: those of the planes that the config
  * has; du may be NULL. The activations are recomputed from pre. bf16: dg, dv and w h are
- * rounded to bf16 before their products, and for routed slots each slot's row of du before
- * the sum over the token's slots. T == 0 clears the gradients. */
+ * rounded to bf16 before their products; the slots' rows of du are summed in f32. T == 0 clears the gradients. */
 MOE_API moe_status moe_ffn_backward(const moe_config *cfg, const moe_weights *w, const void *u, int64_t ldu,
                                     int64_t T, const int32_t *expert_offsets, const int32_t *sorted_slot,
                                     const float *topk_w, const void *pre, const void *dy, int64_t lddy, void *du,

@@ -66,6 +66,10 @@ moe_status check_linear(const moe_linear_desc* d, int64_t T) {
     return MOE_OK;
 }
 
+cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t s) {
+    return g.dtype == MOE_DTYPE_F32 ? launch_simt_gemm(g, s) : launch_tc_gemm_train(g, s);
+}
+
 struct LinearWs {
     size_t dz, partial, total;
 };
@@ -142,14 +146,16 @@ struct FfnWs {
     size_t poff, uoff, row_slot, slot_row;
     size_t up, dyp;   // gathered rows of u and dy (routed)
     size_t gp, h;     // forward
-    size_t rows_out;  // [rows, K] slot rows of y or du (routed)
+    size_t rows_out;  // [rows, K] f32 slot rows of y or du (routed)
     size_t dh, dgu, hw, partial;
+    size_t parts;     // [rows, dgated_parts] partial sums of dtopk_w (bf16, routed)
     size_t total;
 };
 FfnWs ffn_ws(const FfnShape& f, bool backward) {
     FfnWs L{};
     Carver c;
     if (f.T == 0) return L;
+    const bool f32 = f.dtype == MOE_DTYPE_F32;
     if (!f.dense) {
         L.poff = c.take((f.E + 1) * 4);
         L.uoff = c.take((f.E + 1) * 4);
@@ -157,17 +163,18 @@ FfnWs ffn_ws(const FfnShape& f, bool backward) {
         L.slot_row = c.take(f.S * 4);
         L.up = c.take(f.rows * f.K * f.es);
         if (backward) L.dyp = c.take(f.rows * f.K * f.es);
-        L.rows_out = c.take(f.rows * f.K * f.es);
+        L.rows_out = c.take(f.rows * f.K * 4);
+        if (backward && !f32) L.parts = c.take(f.rows * dgated_parts(f.I) * 4);
     }
     if (backward) {
-        L.dh = c.take(f.rows * f.I * 4);
+        if (f32) L.dh = c.take(f.rows * f.I * 4);
         L.dgu = c.take(f.rows * 2 * f.I * f.es);
         L.hw = c.take(f.rows * f.I * f.es);
         if (f.bias)
             L.partial = c.take(std::max(int64_t(colsum_splits(f.rows, f.E, 2 * f.I)) * f.E * 2 * f.I,
                                         int64_t(colsum_splits(f.rows, f.E, f.K)) * f.E * f.K) * 4);
     } else {
-        L.gp = c.take(f.rows * 2 * f.I * 4);
+        if (f32) L.gp = c.take(f.rows * 2 * f.I * 4);
         L.h = c.take(f.rows * f.I * f.es);
     }
     L.total = c.off;
@@ -234,6 +241,7 @@ moe_status moe_linear_forward(const moe_linear_desc* d, const void* x, int64_t l
     if (residual) MOE_CHECK(stride(ldr, N, d->dtype));
     MOE_CHECK(check_ws(ws, ws_bytes, linear_ws(d, T, false).total));
     GemmArgs g;
+    g.plan.status = device_status;
     g.kind = kNT;
     g.a = x; g.lda = ldx;
     g.b = w; g.ldb = K;
@@ -244,7 +252,7 @@ moe_status moe_linear_forward(const moe_linear_desc* d, const void* x, int64_t l
     g.pre = pre; g.ldp = N;
     g.out = y; g.ldo = ldy;
     g.dtype = d->dtype;
-    MOE_CUDA(launch_simt_gemm(g, (cudaStream_t)stream));
+    MOE_CUDA(launch_gemm(g, (cudaStream_t)stream));
     return MOE_OK;
 }
 
@@ -297,6 +305,7 @@ moe_status moe_linear_backward(const moe_linear_desc* d, const void* dy, int64_t
         MOE_CUDA(launch_dact(a, s));
     }
     GemmArgs g;
+    g.plan.status = device_status;
     g.dtype = d->dtype;
     if (dx) {
         g.kind = kNN;
@@ -304,7 +313,7 @@ moe_status moe_linear_backward(const moe_linear_desc* d, const void* dy, int64_t
         g.b = w; g.ldb = K;
         g.M = T; g.N = K; g.R = N;
         g.out = dx; g.ldo = lddx;
-        MOE_CUDA(launch_simt_gemm(g, s));
+        MOE_CUDA(launch_gemm(g, s));
     }
     if (dw) {
         g.kind = kTN;
@@ -312,7 +321,7 @@ moe_status moe_linear_backward(const moe_linear_desc* d, const void* dy, int64_t
         g.b = x; g.ldb = ldx;
         g.M = N; g.N = K; g.R = T;
         g.out = dw; g.ldo = K;
-        MOE_CUDA(launch_simt_gemm(g, s));
+        MOE_CUDA(launch_gemm(g, s));
     }
     return MOE_OK;
 }
@@ -374,17 +383,21 @@ moe_status moe_ffn_forward(const moe_config* cfg, const moe_weights* w, const vo
         g.sbias = int64_t(f.I) * (f.il ? 2 : 1);
     }
     g.M = f.T; g.N = 2 * f.I; g.R = f.K;
-    g.out = at<void>(ws, L.gp); g.ldo = 2 * f.I; g.out_f32 = 1;
-    MOE_CUDA(launch_simt_gemm(g, s));
     GatedArgs ga;
     ga.plan = p;
     ga.I = f.I; ga.interleaved = f.il; ga.act = cfg->activation; ga.limit = cfg->swiglu_limit;
     ga.alpha = cfg->swiglu_alpha;
     ga.dtype = f.dtype;
-    ga.gp = at<float>(ws, L.gp);
     ga.pre = pre;
     ga.h = at<void>(ws, L.h);
-    MOE_CUDA(launch_gated_forward(ga, s));
+    if (f.dtype == MOE_DTYPE_F32) {
+        g.out = at<void>(ws, L.gp); g.ldo = 2 * f.I;
+        ga.gp = at<float>(ws, L.gp);
+        MOE_CUDA(launch_simt_gemm(g, s));
+        MOE_CUDA(launch_gated_forward(ga, s));
+    } else {
+        MOE_CUDA(launch_tc_gateup(g, ga, s));
+    }
     GemmArgs o;
     o.kind = kNT;
     o.plan = p;
@@ -399,15 +412,15 @@ moe_status moe_ffn_forward(const moe_config* cfg, const moe_weights* w, const vo
     if (dense) {
         o.residual = residual; o.ldr = ldr;
         o.out = y; o.ldo = ldy;
-        MOE_CUDA(launch_simt_gemm(o, s));
+        MOE_CUDA(launch_gemm(o, s));
         return MOE_OK;
     }
     o.row_scale = topk_w;
-    o.out = at<void>(ws, L.rows_out); o.ldo = f.K;
-    MOE_CUDA(launch_simt_gemm(o, s));
+    o.out = at<void>(ws, L.rows_out); o.ldo = f.K; o.out_f32 = 1;
+    MOE_CUDA(launch_gemm(o, s));
     SumSlotsArgs sa;
     sa.plan = p;
-    sa.rows = o.out;
+    sa.rows = at<float>(ws, L.rows_out);
     sa.residual = residual; sa.ldr = ldr;
     sa.out = y; sa.ldo = ldy;
     sa.K = f.K;
@@ -484,14 +497,11 @@ moe_status moe_ffn_backward(const moe_config* cfg, const moe_weights* w, const v
     g.a = dyp; g.lda = lddyp;
     g.b = w->down_w; g.ldb = f.I; g.sb = int64_t(f.K) * f.I;
     g.M = f.T; g.N = f.I; g.R = f.K;
-    g.out = at<void>(ws, L.dh); g.ldo = f.I; g.out_f32 = 1;
-    MOE_CUDA(launch_simt_gemm(g, s));
     GatedArgs ga;
     ga.plan = p;
     ga.I = f.I; ga.interleaved = f.il; ga.act = cfg->activation; ga.limit = cfg->swiglu_limit;
     ga.alpha = cfg->swiglu_alpha;
     ga.dtype = f.dtype;
-    ga.dh = at<float>(ws, L.dh);
     ga.topk_w = topk_w;
     ga.pre = const_cast<void*>(pre);
     ga.dgu = at<void>(ws, L.dgu);
@@ -500,7 +510,16 @@ moe_status moe_ffn_backward(const moe_config* cfg, const moe_weights* w, const v
     ga.dyp = dyp;
     ga.down_b = f.bias ? w->down_b : nullptr;
     ga.K = f.K;
-    MOE_CUDA(launch_gated_backward(ga, s));
+    if (f.dtype == MOE_DTYPE_F32) {
+        g.out = at<void>(ws, L.dh); g.ldo = f.I;
+        ga.dh = at<float>(ws, L.dh);
+        MOE_CUDA(launch_simt_gemm(g, s));
+        MOE_CUDA(launch_gated_backward(ga, s));
+    } else {
+        float* parts = dtopk_w ? at<float>(ws, L.parts) : nullptr;
+        MOE_CUDA(launch_tc_dgated(g, ga, parts, s));
+        if (dtopk_w) MOE_CUDA(launch_dtopk(ga, parts, dgated_parts(f.I), s));
+    }
     // du = dg Wg + dv Wu
     if (du) {
         GemmArgs x;
@@ -514,12 +533,12 @@ moe_status moe_ffn_backward(const moe_config* cfg, const moe_weights* w, const v
             x.split = f.I;
         }
         x.M = f.T; x.N = f.K; x.R = 2 * f.I;
-        x.out = dense ? du : at<void>(ws, L.rows_out); x.ldo = dense ? lddu : f.K;
-        MOE_CUDA(launch_simt_gemm(x, s));
+        x.out = dense ? du : at<void>(ws, L.rows_out); x.ldo = dense ? lddu : f.K; x.out_f32 = !dense;
+        MOE_CUDA(launch_gemm(x, s));
         if (!dense) {
             SumSlotsArgs sa;
             sa.plan = p;
-            sa.rows = x.out;
+            sa.rows = at<float>(ws, L.rows_out);
             sa.out = du; sa.ldo = lddu;
             sa.K = f.K;
             sa.dtype = f.dtype;
@@ -535,7 +554,7 @@ moe_status moe_ffn_backward(const moe_config* cfg, const moe_weights* w, const v
     t.b = ga.hw; t.ldb = f.I;
     t.M = f.K; t.N = f.I; t.R = f.T;
     t.out = gr->down_w; t.ldo = f.I; t.so = int64_t(f.K) * f.I;
-    MOE_CUDA(launch_simt_gemm(t, s));
+    MOE_CUDA(launch_gemm(t, s));
     t.a = ga.dgu; t.lda = 2 * f.I;
     t.b = up; t.ldb = ldup;
     t.M = 2 * f.I; t.N = f.K;
@@ -544,7 +563,7 @@ moe_status moe_ffn_backward(const moe_config* cfg, const moe_weights* w, const v
         t.out1 = gr->up_w;
         t.split = f.I;
     }
-    MOE_CUDA(launch_simt_gemm(t, s));
+    MOE_CUDA(launch_gemm(t, s));
     if (f.bias) {
         ColsumArgs c;
         c.plan = p;

@@ -49,7 +49,7 @@ cudaError_t launch_gather_padded(const GatherArgs& a, cudaStream_t s);
 // out[t] = sum over the token's slots of rows[slot_row] (+ residual[t]), slots in order.
 struct SumSlotsArgs {
     RowPlan plan;
-    const void* rows = nullptr;  // [padded rows, K], activation dtype
+    const float* rows = nullptr;  // [padded rows, K] f32
     const void* residual = nullptr;
     int64_t ldr = 0;
     void* out = nullptr;
@@ -90,11 +90,11 @@ struct GemmArgs {
     int dtype = MOE_DTYPE_BF16;        // a, b, bias, residual, pre
     int out_f32 = 0;                   // out is f32 instead
 };
-cudaError_t launch_simt_gemm(const GemmArgs& a, cudaStream_t s);
+cudaError_t launch_simt_gemm(const GemmArgs& a, cudaStream_t s);     // f32
+cudaError_t launch_tc_gemm_train(const GemmArgs& a, cudaStream_t s);  // bf16, any kind
 
 // ------------------------------------------------------------------ element-wise passes
-// h = act(pre) for every row: gp (padded order, activation dtype or f32) -> pre (user order)
-// and h (padded order).
+// The gated activation of every row and its derivative.
 struct GatedArgs {
     RowPlan plan;
     int I = 0;
@@ -115,8 +115,16 @@ struct GatedArgs {
     const void* down_b = nullptr;   // [E, K]
     int K = 0;
 };
+// f32: on the results of launch_simt_gemm.
 cudaError_t launch_gated_forward(const GatedArgs& a, cudaStream_t s);
 cudaError_t launch_gated_backward(const GatedArgs& a, cudaStream_t s);
+// bf16: in the epilogue of the product g = (gate/up forward; dy Wd backward), which writes
+// pre and h, or dgu, hw and per row dgated_parts(I) partial sums of dh . h.
+cudaError_t launch_tc_gateup(const GemmArgs& g, const GatedArgs& ga, cudaStream_t s);
+cudaError_t launch_tc_dgated(const GemmArgs& g, const GatedArgs& ga, float* partial, cudaStream_t s);
+int dgated_parts(int I);
+// dtopk_w[slot] = the row's partial sums (+ dyp . down_b), from GatedArgs' plan, dtopk_w, dyp, down_b, K.
+cudaError_t launch_dtopk(const GatedArgs& a, const float* partial, int parts, cudaStream_t s);
 
 // Column sums of each expert's rows: out[e, c] = sum_r x[r, c] (* topk_w[slot of r]).
 struct ColsumArgs {

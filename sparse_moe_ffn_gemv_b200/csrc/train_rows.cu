@@ -100,7 +100,11 @@ __global__ void __launch_bounds__(256) sum_slots_kernel(const SumSlotsArgs a) {
             const int r = sr[j];
             if (r < 0) continue;
             float f[V];
-            load_vec(static_cast<const T*>(a.rows) + int64_t(r) * a.K + c, f);
+#pragma unroll
+            for (int q = 0; q < V; q += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(a.rows + int64_t(r) * a.K + c + q);
+                f[q] = v.x; f[q + 1] = v.y; f[q + 2] = v.z; f[q + 3] = v.w;
+            }
 #pragma unroll
             for (int q = 0; q < V; ++q) acc[q] += f[q];
         }
@@ -136,10 +140,10 @@ __device__ __forceinline__ RowRef row_ref(const RowPlan& p, int64_t r) {
     return o;
 }
 
-// One warp per row; gate and up of unit i.
-template <typename T>
+// One warp per row; gate and up of unit i. (f32; bf16 has both passes in its products' epilogues.)
 __global__ void __launch_bounds__(256) gated_forward_kernel(const GatedArgs a) {
-    constexpr bool FAST = Vec<T>::N == 8;
+    using T = float;
+    constexpr bool FAST = false;
     const int lane = threadIdx.x & 31;
     const int64_t rows = plan_rows(a.plan), warps = int64_t(gridDim.x) * 8;
     for (int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); r < rows; r += warps) {
@@ -159,9 +163,9 @@ __global__ void __launch_bounds__(256) gated_forward_kernel(const GatedArgs a) {
     }
 }
 
-template <typename T>
 __global__ void __launch_bounds__(256) gated_backward_kernel(const GatedArgs a) {
-    constexpr bool FAST = Vec<T>::N == 8;
+    using T = float;
+    constexpr bool FAST = false;
     const int lane = threadIdx.x & 31;
     const int64_t rows = plan_rows(a.plan), warps = int64_t(gridDim.x) * 8;
     for (int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); r < rows; r += warps) {
@@ -194,6 +198,32 @@ __global__ void __launch_bounds__(256) gated_backward_kernel(const GatedArgs a) 
                       to_f<T>(static_cast<const T*>(a.down_b)[int64_t(o.e) * a.K + c]);
         dw = warp_sum(dw);
         if (lane == 0) a.dtopk_w[o.slot] = dw;
+    }
+}
+
+// One warp per row: its partial sums in order, and with a down bias the row's dy . down_b.
+__global__ void __launch_bounds__(256) dtopk_kernel(const GatedArgs a, const float* partial, int parts) {
+    const int lane = threadIdx.x & 31;
+    const int64_t rows = plan_rows(a.plan), warps = int64_t(gridDim.x) * 8;
+    for (int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); r < rows; r += warps) {
+        const int slot = a.plan.row_slot[r];
+        if (slot < 0) continue;
+        float dw = 0.0f;
+        for (int i = lane; i < parts; i += 32) dw += partial[r * parts + i];
+        if (a.down_b) {
+            const int e = expert_of_row(a.plan.poff, a.plan.E, int(r));
+            const __nv_bfloat16* d = static_cast<const __nv_bfloat16*>(a.dyp) + r * a.K;
+            const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(a.down_b) + int64_t(e) * a.K;
+            for (int c = lane * 8; c < a.K; c += 256) {
+                float x[8], y[8];
+                load_vec(d + c, x);
+                load_vec(b + c, y);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) dw = fmaf(x[q], y[q], dw);
+            }
+        }
+        dw = warp_sum(dw);
+        if (lane == 0) a.dtopk_w[slot] = dw;
     }
 }
 
@@ -323,16 +353,17 @@ cudaError_t launch_sum_slots(const SumSlotsArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_gated_forward(const GatedArgs& a, cudaStream_t s) {
-    const unsigned grid = grid_for(a.plan.max_rows, 8, 148 * 8);
-    if (a.dtype == MOE_DTYPE_F32) gated_forward_kernel<float><<<grid, 256, 0, s>>>(a);
-    else gated_forward_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
+    gated_forward_kernel<<<grid_for(a.plan.max_rows, 8, 148 * 8), 256, 0, s>>>(a);
     return cudaGetLastError();
 }
 
 cudaError_t launch_gated_backward(const GatedArgs& a, cudaStream_t s) {
-    const unsigned grid = grid_for(a.plan.max_rows, 8, 148 * 8);
-    if (a.dtype == MOE_DTYPE_F32) gated_backward_kernel<float><<<grid, 256, 0, s>>>(a);
-    else gated_backward_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
+    gated_backward_kernel<<<grid_for(a.plan.max_rows, 8, 148 * 8), 256, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_dtopk(const GatedArgs& a, const float* partial, int parts, cudaStream_t s) {
+    dtopk_kernel<<<grid_for(a.plan.max_rows, 8, 148 * 8), 256, 0, s>>>(a, partial, parts);
     return cudaGetLastError();
 }
 

@@ -38,8 +38,9 @@ __device__ __forceinline__ void stash(float (&sm)[kBR][64 + 4], const float (&v)
     }
 }
 
-template <typename T, int KIND>
+template <int KIND>
 __global__ void __launch_bounds__(kThreads) simt_gemm_kernel(const GemmArgs a) {
+    using T = float;
     constexpr bool AR = KIND == kTN, BR = KIND != kNT;  // operand rows are reduction indices
     __shared__ float sa[kBR][kBM + 4], sb[kBR][kBN + 4];
     const RowPlan& p = a.plan;
@@ -134,30 +135,24 @@ __global__ void __launch_bounds__(kThreads) simt_gemm_kernel(const GemmArgs a) {
                 z += a.split && n >= a.split ? to_f<T>(static_cast<const T*>(a.bias1)[int64_t(e) * a.sbias + n - a.split])
                                              : to_f<T>(static_cast<const T*>(a.bias)[int64_t(e) * a.sbias + n]);
             if (a.pre) static_cast<T*>(a.pre)[m * a.ldp + n] = from_f<T>(z);
-            z = linear_act<Vec<T>::N == 8>(a.act, z) * rs;
+            z = linear_act<false>(a.act, z) * rs;
             if (a.residual) z += to_f<T>(static_cast<const T*>(a.residual)[m * a.ldr + n]);
-            if (a.out_f32) static_cast<float*>(a.out)[m * a.ldo + n] = z;
-            else static_cast<T*>(a.out)[m * a.ldo + n] = from_f<T>(z);
+            static_cast<T*>(a.out)[m * a.ldo + n] = z;
         }
     }
-}
-
-template <typename T>
-cudaError_t launch_t(const GemmArgs& a, cudaStream_t s) {
-    const bool grouped = a.plan.offsets != nullptr;
-    const int64_t rows = a.kind == kTN ? a.M : grouped ? a.plan.max_rows : a.M;
-    const dim3 grid(unsigned((rows + kBM - 1) / kBM), unsigned((a.N + kBN - 1) / kBN),
-                    a.kind == kTN && grouped ? unsigned(a.plan.E) : 1u);
-    if (a.kind == kNT) simt_gemm_kernel<T, kNT><<<grid, kThreads, 0, s>>>(a);
-    else if (a.kind == kNN) simt_gemm_kernel<T, kNN><<<grid, kThreads, 0, s>>>(a);
-    else simt_gemm_kernel<T, kTN><<<grid, kThreads, 0, s>>>(a);
-    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_simt_gemm(const GemmArgs& a, cudaStream_t s) {
-    return a.dtype == MOE_DTYPE_F32 ? launch_t<float>(a, s) : launch_t<__nv_bfloat16>(a, s);
+    const bool grouped = a.plan.offsets != nullptr;
+    const int64_t rows = a.kind == kTN ? a.M : grouped ? a.plan.max_rows : a.M;
+    const dim3 grid(unsigned((rows + kBM - 1) / kBM), unsigned((a.N + kBN - 1) / kBN),
+                    a.kind == kTN && grouped ? unsigned(a.plan.E) : 1u);
+    if (a.kind == kNT) simt_gemm_kernel<kNT><<<grid, kThreads, 0, s>>>(a);
+    else if (a.kind == kNN) simt_gemm_kernel<kNN><<<grid, kThreads, 0, s>>>(a);
+    else simt_gemm_kernel<kTN><<<grid, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace moe

@@ -1,0 +1,1002 @@
+// train_tc.cu -- bf16 matrix products of the training operators on the 5th-generation tensor
+// cores (tcgen05, accumulators in TMEM), fed by TMA, with the element-wise work of each
+// product in its epilogue.
+//
+//   D[m, n] = sum_r A(m, r) B(n, r)       f32 accumulation
+//   kNT  A [m][r], B [n][r]  both operands with the reduction contiguous (K-major)
+//   kNN  A [m][r], B [r][n]  B with n contiguous (MN-major): dz times a weight plane
+//   kTN  A [r][m], B [r][n]  both MN-major: dz^T times the tokens, reduced over an expert's rows
+//
+// No operand is transposed in memory: the matrix instructions read either order from shared
+// memory, and TMA brings either as 64 x 64 (MN-major) or 64 x 128 (K-major) boxes with the
+// 128-byte swizzle. Tiles are 128 x 256 on one CTA, or 256 x 256 on a pair of CTAs
+// (cta_group::2: each CTA loads half of both operands, which halves the operand traffic per
+// product; one CTA's tile needs 96 bytes per cycle of L2 reads to keep its tensor core busy,
+// a pair's 64).
+//
+// One persistent CTA (pair) per SM (pair):
+//   warp 0      TMA producer into a ring of 64-deep reduction blocks
+//   warp 1      MMA issuer (one thread; of a pair, the leader's)
+//   warps 2..9  epilogue, two accumulator sets in TMEM so that it overlaps the next tile's
+//               products: one accumulator row per lane, 32 columns at a time, results turned
+//               through 2 KB of shared memory per warp so that global rows are written and
+//               read in whole 32-byte sectors
+// Every wait gives up after 2 s, records MOE_ERR_DEVICE_TIMEOUT, lets its own copies and
+// products finish and returns; TMEM is always freed.
+#include <cuda.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "ptx.cuh"
+#include "train_dev.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kBR = 64;        // reduction block: 128 bytes of bf16, one swizzle atom
+constexpr int kCols = 256;     // columns of a tile (N of the matrix instruction)
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kMaxE = 512;
+constexpr int kABytes = 128 * kBR * 2;  // one 128-row operand tile
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+enum Epi { kStore = 0, kGateUp = 1, kDGated = 2 };
+
+struct TcTrain {
+    CUtensorMap a, b0, b1;
+    // rows
+    const int32_t *offsets, *poff, *uoff, *row_slot;  // grouped (offsets != null)
+    int E;
+    int64_t rows;           // dense: rows of A (kNT, kNN) or reduction rows (kTN)
+    // tile grid: rows of D in row tiles (kTN: of `halves` planes of `mrows` rows each), n_blocks
+    int64_t mrows;
+    int halves, m_blocks, n_blocks, band;
+    int N;                  // columns of D (kGateUp: units)
+    int nk, nk_half;        // reduction blocks (kNT, kNN) and of one half (kNN split)
+    int interleaved;        // kGateUp, kDGated: alternating gate / up columns
+    int b_split;            // kNN: the second half reads b1
+    // epilogue
+    const __nv_bfloat16 *bias0, *bias1;
+    int64_t sbias;
+    int act;
+    const float* row_scale;
+    const __nv_bfloat16* residual;
+    int64_t ldr;
+    __nv_bfloat16* pre;     // kStore: z; kGateUp: out; kDGated: in
+    int64_t ldp;
+    void *out, *out1;
+    int64_t ldo, so;
+    int out_f32;
+    float limit, alpha;
+    __nv_bfloat16 *dgu, *hw;
+    float* partial;         // kDGated: [rows, parts]
+    int parts;
+    int* status;
+};
+
+// ------------------------------------------------------------------ tcgen05
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Shared-memory operand descriptors, 128-byte swizzle. K-major: 8-row groups 1024 B apart.
+// MN-major: 64-element blocks of m (n) 8192 B apart, groups of 8 reduction rows 1024 B apart.
+template <bool MN>
+__device__ __forceinline__ uint64_t operand(uint32_t saddr) {
+    const uint64_t lbo = MN ? 8192 >> 4 : 1, sbo = 1024 >> 4;
+    return uint64_t((saddr & 0x3FFFFu) >> 4) | (lbo << 16) | (sbo << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+// Bytes from one 16-deep reduction step to the next within a block.
+template <bool MN> constexpr uint32_t kStep = MN ? 16 * 128 : 32;
+
+constexpr uint32_t idesc(bool a_mn, bool b_mn, int m, int n) {  // bf16 x bf16 -> f32
+    return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
+           (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, uint32_t acc) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(desc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(desc), "r"(acc)
+            : "memory");
+}
+// Arrive on the barrier (of both CTAs of a pair) once the products issued so far are done.
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    if constexpr (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                su32(bar)),
+            "h"(uint16_t(3))
+            : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(bar))
+                     : "memory");
+}
+// 32 accumulator columns of this lane's row; valid after tmem_wait.
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+
+// Bounded wait; the clock starts when the wait does, so that a long launch is no timeout.
+__device__ __forceinline__ bool wait_bar(uint64_t* b, uint32_t parity) {
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try(b, parity)) return true;
+    return mbar_wait(b, parity, gtimer() + kWaitNs);
+}
+__device__ __forceinline__ bool wait_bar_sleep(uint64_t* b, uint32_t parity) {
+    if (mbar_try(b, parity)) return true;
+    return mbar_wait_sleep(b, parity, gtimer() + kWaitNs);
+}
+
+// ------------------------------------------------------------------ 64-byte row segments
+// A warp's 32 rows of 64 bytes: lane r holds row r (four 16-byte pieces). In shared memory
+// piece c of row r sits at place c ^ (r / 2 % 4) of its row, so that neither side of the turn
+// has bank conflicts.
+__device__ __forceinline__ uint32_t seg(int r, int c) { return uint32_t(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); }
+
+// Writes rows [0, rows) of the segment, its first `bytes` bytes (a multiple of 16).
+__device__ __forceinline__ void store_rows(uint8_t* sm, int lane, const uint4 (&v)[4], void* base, int64_t ld_bytes,
+                                           int rows, int bytes) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(sm + seg(lane, c)) = v[c];
+    __syncwarp();
+    const int c = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2);
+        const uint4 x = *reinterpret_cast<const uint4*>(sm + seg(r, c));
+        if (r < rows && c * 16 < bytes) *reinterpret_cast<uint4*>(static_cast<char*>(base) + r * ld_bytes + c * 16) = x;
+    }
+    __syncwarp();
+}
+// Reads them; rows and bytes past the limits give zeros.
+__device__ __forceinline__ void load_rows(uint8_t* sm, int lane, uint4 (&v)[4], const void* base, int64_t ld_bytes,
+                                          int rows, int bytes) {
+    const int c = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2);
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < rows && c * 16 < bytes)
+            x = *reinterpret_cast<const uint4*>(static_cast<const char*>(base) + r * ld_bytes + c * 16);
+        *reinterpret_cast<uint4*>(sm + seg(r, c)) = x;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int c2 = 0; c2 < 4; ++c2) v[c2] = *reinterpret_cast<const uint4*>(sm + seg(lane, c2));
+    __syncwarp();
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void pack_row(const float (&f)[32], uint4 (&v)[4]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        v[c] = make_uint4(pack2(f[8 * c], f[8 * c + 1]), pack2(f[8 * c + 2], f[8 * c + 3]),
+                          pack2(f[8 * c + 4], f[8 * c + 5]), pack2(f[8 * c + 6], f[8 * c + 7]));
+}
+__device__ __forceinline__ void unpack_row(const uint4 (&v)[4], float (&f)[32]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        float t[8];
+        unpack8(v[c], t);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[8 * c + j] = t[j];
+    }
+}
+// Alternating columns of 16 units: f[2i] = a[i0 + i], f[2i + 1] = b[i0 + i].
+__device__ __forceinline__ void weave(const float (&a)[32], const float (&b)[32], int i0, float (&f)[32]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        f[2 * i] = a[i0 + i];
+        f[2 * i + 1] = b[i0 + i];
+    }
+}
+// 32 bias values from column c on, columns past `limit` zero (limit and c multiples of 8).
+__device__ __forceinline__ void add_bias(const __nv_bfloat16* b, int c, int limit, float (&f)[32]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        if (c + 8 * q >= limit) break;
+        float t[8];
+        unpack8(__ldg(reinterpret_cast<const uint4*>(b + c + 8 * q)), t);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[8 * q + j] += t[j];
+    }
+}
+
+// ------------------------------------------------------------------ tiles
+struct Tile {
+    int e;          // expert, or 0
+    int half;       // kTN: plane of D
+    int64_t row0;   // first row of D in A's row space (kTN: in the plane)
+    int limit;      // rows of D this tile owns (up to the tile's height)
+    int nvalid;     // of those, rows that hold slots (kNT, kNN grouped)
+    int n0;         // first column
+    int nk;         // reduction blocks
+    int64_t r0;     // kTN: first reduction row
+    int64_t pos0;   // first row in the caller's sorted order
+};
+
+struct Tables {
+    int poff[kMaxE + 1], ts[kMaxE + 1], uoff[kMaxE + 1];
+};
+
+template <int KIND, int EPI, bool PAIR>
+struct Shape {
+    static constexpr int BM = PAIR ? 256 : 128;
+    static constexpr bool AMN = KIND == kTN, BMN = KIND != kNT;
+    static constexpr int B_BYTES = PAIR ? kABytes : 2 * kABytes;
+    static constexpr int STAGE = kABytes + B_BYTES;
+    static constexpr int STAGES = PAIR ? 6 : 4;
+    static constexpr int RING = STAGES * STAGE;
+    static constexpr int STG = kEpiWarps * 2048;
+    static constexpr int SMEM = RING + STG + 256 + int(sizeof(Tables)) + 1024;
+    static constexpr int UNITS = EPI == kGateUp ? 128 : kCols;  // columns (units) a tile covers
+    static_assert(SMEM <= 232448, "dynamic shared memory per block");
+};
+
+template <int KIND, int EPI, bool PAIR>
+__device__ __forceinline__ Tile tile_of(const TcTrain& P, const Tables& tb, int idx) {
+    using S = Shape<KIND, EPI, PAIR>;
+    Tile t;
+    t.half = 0;
+    t.e = 0;
+    t.r0 = t.pos0 = 0;
+    if constexpr (KIND == kTN) {
+        // expert by expert; within one, the row blocks of a column block in turn
+        const int per = P.m_blocks * P.halves * P.n_blocks;
+        t.e = idx / per;
+        int l = idx - t.e * per;
+        int mb, nb;
+        if (P.band > 0) {  // dense: bands of column blocks, every row block in turn
+            const int mt = P.m_blocks * P.halves;
+            const int b = l / (P.band * mt), w = l - b * P.band * mt;
+            const int width = min(P.band, P.n_blocks - b * P.band);
+            mb = w / width;
+            nb = b * P.band + (w - mb * width);
+        } else {
+            nb = l / (P.m_blocks * P.halves);
+            mb = l - nb * P.m_blocks * P.halves;
+        }
+        t.half = mb / P.m_blocks;
+        t.row0 = int64_t(mb - t.half * P.m_blocks) * S::BM;
+        t.limit = int(min(int64_t(S::BM), P.mrows - t.row0));
+        t.nvalid = t.limit;
+        t.n0 = nb * kCols;
+        int64_t n = P.rows;
+        if (P.offsets) {
+            t.r0 = tb.poff[t.e];
+            n = tb.uoff[t.e + 1] - tb.uoff[t.e];
+        }
+        t.nk = int((n + kBR - 1) / kBR);
+        return t;
+    }
+    t.nk = P.nk;
+    if (!P.offsets) {  // bands of row tiles, every column block in turn
+        const int per = P.band * P.n_blocks;
+        const int b = idx / per, w = idx - b * per;
+        const int width = min(P.band, P.m_blocks - b * P.band);
+        const int nb = w / width;
+        t.row0 = (int64_t(b) * P.band + (w - nb * width)) * S::BM;
+        t.n0 = nb * S::UNITS;
+        t.limit = int(min(int64_t(S::BM), P.rows - t.row0));
+        t.nvalid = t.limit;
+        t.pos0 = t.row0;
+        return t;
+    }
+    int lo = 0, hi = P.E - 1;  // largest e whose tiles start at or before idx
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tb.ts[mid] * P.n_blocks <= idx) lo = mid;
+        else hi = mid - 1;
+    }
+    const int nt = tb.ts[lo + 1] - tb.ts[lo];
+    const int l = idx - tb.ts[lo] * P.n_blocks;
+    const int nb = l / nt, mt = l - nb * nt;
+    t.e = lo;
+    t.row0 = tb.poff[lo] + int64_t(mt) * S::BM;
+    t.n0 = nb * S::UNITS;
+    t.limit = min(S::BM, int(tb.poff[lo + 1] - t.row0));
+    t.nvalid = max(0, min(S::BM, tb.uoff[lo + 1] - tb.uoff[lo] - mt * S::BM));
+    t.pos0 = tb.uoff[lo] + int64_t(mt) * S::BM;
+    return t;
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void load3(void* dst, const CUtensorMap* m, uint64_t* bar, uint32_t bar_c, int c0, int c1,
+                                      int c2, uint64_t pol) {
+    if constexpr (PAIR) tma_3d_pair(dst, m, bar_c, c0, c1, c2, pol);
+    else tma_3d(dst, m, bar, c0, c1, c2, pol);
+}
+template <bool PAIR>
+__device__ __forceinline__ void load4(void* dst, const CUtensorMap* m, uint64_t* bar, uint32_t bar_c, int c0, int c1,
+                                      int c2, int c3, uint64_t pol) {
+    if constexpr (PAIR) tma_4d_pair(dst, m, bar_c, c0, c1, c2, c3, pol);
+    else tma_4d(dst, m, bar, c0, c1, c2, c3, pol);
+}
+
+template <int KIND, int EPI, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_constant__ TcTrain P) {
+    using S = Shape<KIND, EPI, PAIR>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* stg = smem + S::RING;
+    uint64_t* full = reinterpret_cast<uint64_t*>(stg + S::STG);
+    uint64_t* empty = full + S::STAGES;
+    uint64_t* acc_full = empty + S::STAGES;
+    uint64_t* acc_empty = acc_full + 2;
+    uint64_t* drain = acc_empty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    Tables& tb = *reinterpret_cast<Tables*>(stg + S::STG + 256);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t crank = PAIR ? cluster_rank() : 0u;
+    const int tile0 = PAIR ? int(blockIdx.x >> 1) : int(blockIdx.x);
+    const int tstep = PAIR ? int(gridDim.x >> 1) : int(gridDim.x);
+    if (warp == 0) {
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(tmem_slot)));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(tmem_slot)));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        }
+    }
+    if (warp == 1 && lane == 0) {
+        for (int s = 0; s < S::STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], (PAIR ? 2 : 1) * kEpiWarps);
+        }
+        mbar_init(drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (P.offsets) {
+        for (int e = threadIdx.x; e <= P.E; e += kThreads) {
+            tb.poff[e] = P.poff[e];
+            tb.uoff[e] = P.uoff[e];
+        }
+        __syncthreads();
+        if (warp == 2) {  // row tiles of each expert, summed up (16 experts per lane)
+            int n = 0;
+            for (int i = 0; i < kMaxE / 32; ++i) {
+                const int e = lane * (kMaxE / 32) + i;
+                if (e < P.E) n += (tb.poff[e + 1] - tb.poff[e] + S::BM - 1) / S::BM;
+            }
+            int incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            int run = incl - n;
+            for (int i = 0; i < kMaxE / 32; ++i) {
+                const int e = lane * (kMaxE / 32) + i;
+                if (e < P.E) {
+                    tb.ts[e] = run;
+                    run += (tb.poff[e + 1] - tb.poff[e] + S::BM - 1) / S::BM;
+                    if (e == P.E - 1) tb.ts[P.E] = run;
+                }
+            }
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync();
+    fence_after();
+    const uint32_t tmem = *tmem_slot;
+    int total;
+    if (KIND == kTN) total = P.E * P.m_blocks * P.halves * P.n_blocks;
+    else total = (P.offsets ? tb.ts[P.E] : P.m_blocks) * P.n_blocks;
+    bool gave_up = false;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0, armed = 0, last = 0;
+            const uint64_t pol = policy_evict_normal();
+            for (int idx = tile0; idx < total && !gave_up; idx += tstep) {
+                const Tile t = tile_of<KIND, EPI, PAIR>(P, tb, idx);
+                const int arow = int(t.row0) + 128 * int(crank);
+                for (int kb = 0; kb < t.nk; ++kb) {
+                    if (!wait_bar(&empty[stage], phase ^ 1u)) {
+                        gave_up = true;
+                        break;
+                    }
+                    uint8_t* sa = smem + stage * S::STAGE;
+                    uint8_t* sb = sa + kABytes;
+                    const uint32_t fb = PAIR ? mapa_shared(&full[stage], 0) : 0u;
+                    if (crank == 0) mbar_expect_tx(&full[stage], (PAIR ? 2 : 1) * S::STAGE);
+                    const int half = KIND == kNN && kb >= P.nk_half ? 1 : 0;
+                    const int kc = (kb - half * P.nk_half) * kBR;
+                    if constexpr (KIND == kTN) {
+                        const int r = int(t.r0) + kb * kBR;
+                        load3<PAIR>(sa, &P.a, &full[stage], fb, arow, t.half, r, pol);
+                        load3<PAIR>(sa + 8192, &P.a, &full[stage], fb, arow + 64, t.half, r, pol);
+                        const int nb = t.n0 + 128 * int(crank);
+#pragma unroll
+                        for (int j = 0; j < S::B_BYTES / 8192; ++j)
+                            load3<PAIR>(sb + j * 8192, &P.b0, &full[stage], fb, nb + 64 * j, r, 0, pol);
+                    } else {
+                        load3<PAIR>(sa, &P.a, &full[stage], fb, kc, half, arow, pol);
+                        if constexpr (KIND == kNN) {
+                            const CUtensorMap* mb = half && P.b_split ? &P.b1 : &P.b0;
+                            const int nb = t.n0 + 128 * int(crank);
+#pragma unroll
+                            for (int j = 0; j < S::B_BYTES / 8192; ++j)
+                                load3<PAIR>(sb + j * 8192, mb, &full[stage], fb, nb + 64 * j, kc, t.e, pol);
+                        } else if constexpr (EPI == kGateUp) {
+                            // gate rows, then up rows; of a pair, CTA 0 gate and CTA 1 up
+                            if constexpr (PAIR) {
+                                if (P.interleaved) load4<PAIR>(sb, &P.b0, &full[stage], fb, kc, int(crank), t.n0, t.e, pol);
+                                else load4<PAIR>(sb, crank ? &P.b1 : &P.b0, &full[stage], fb, kc, 0, t.n0, t.e, pol);
+                            } else {
+                                load4<PAIR>(sb, &P.b0, &full[stage], fb, kc, 0, t.n0, t.e, pol);
+                                if (P.interleaved) load4<PAIR>(sb + kABytes, &P.b0, &full[stage], fb, kc, 1, t.n0, t.e, pol);
+                                else load4<PAIR>(sb + kABytes, &P.b1, &full[stage], fb, kc, 0, t.n0, t.e, pol);
+                            }
+                        } else {
+                            const int nb = t.n0 + 128 * int(crank);
+#pragma unroll
+                            for (int j = 0; j < S::B_BYTES / kABytes; ++j)
+                                load4<PAIR>(sb + j * kABytes, &P.b0, &full[stage], fb, kc, 0, nb + 128 * j, t.e, pol);
+                        }
+                    }
+                    armed |= 1u << stage;
+                    last = (last & ~(1u << stage)) | (phase << stage);
+                    if (++stage == S::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // every copy has landed (of a pair: and been read) before this CTA may leave
+            for (int s = 0; s < S::STAGES; ++s)
+                if ((armed >> s) & 1u) wait_bar(PAIR ? &empty[s] : &full[s], (last >> s) & 1u);
+            if (gave_up) set_status(P.status, MOE_ERR_DEVICE_TIMEOUT);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && crank == 0) {
+            // -------------------------------------------------------- MMA issuer
+            uint32_t stage = 0, phase = 0, it = 0;
+            for (int idx = tile0; idx < total && !gave_up; idx += tstep) {
+                const Tile t = tile_of<KIND, EPI, PAIR>(P, tb, idx);
+                if (t.nk == 0) continue;
+                const uint32_t ab = it & 1u, ph = (it >> 1) & 1u;
+                ++it;
+                if (!wait_bar(&acc_empty[ab], ph ^ 1u)) {
+                    gave_up = true;
+                    break;
+                }
+                fence_after();
+                const uint32_t d0 = tmem + ab * kCols;
+                constexpr uint32_t desc = idesc(S::AMN, S::BMN, S::BM, kCols);
+                for (int kb = 0; kb < t.nk; ++kb) {
+                    if (!wait_bar(&full[stage], phase)) {
+                        gave_up = true;
+                        break;
+                    }
+                    fence_after();
+                    const uint32_t sa = su32(smem + stage * S::STAGE), sb = sa + kABytes;
+#pragma unroll
+                    for (int k = 0; k < kBR / 16; ++k)
+                        mma<PAIR>(d0, operand<S::AMN>(sa + k * kStep<S::AMN>), operand<S::BMN>(sb + k * kStep<S::BMN>),
+                                  desc, kb > 0 || k > 0 ? 1u : 0u);
+                    commit<PAIR>(&empty[stage]);
+                    if (++stage == S::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (gave_up) break;
+                commit<PAIR>(&acc_full[ab]);
+            }
+            commit<PAIR>(drain);
+            wait_bar(drain, 0);
+            if (gave_up) set_status(P.status, MOE_ERR_DEVICE_TIMEOUT);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ epilogue
+        const int q = warp & 3;                    // TMEM lane quarter of this warp
+        const int ch = (warp - 2) >> 2;            // column half
+        uint8_t* sm = stg + (warp - 2) * 2048;
+        const int wrow = int(crank) * 128 + q * 32;  // first tile row of the warp
+        uint32_t it = 0;
+        for (int idx = tile0; idx < total; idx += tstep) {
+            const Tile t = tile_of<KIND, EPI, PAIR>(P, tb, idx);
+            const int rows = min(32, t.limit - wrow);     // may be negative
+            const int vrows = min(32, t.nvalid - wrow);
+            const int64_t row = t.row0 + wrow;            // the warp's first row
+            const uint32_t ab = it & 1u, ph = (it >> 1) & 1u;
+            float rs = 1.0f;
+            if (KIND != kTN && P.offsets && P.row_scale && lane < vrows) {
+                const int slot = P.row_slot[row + lane];
+                rs = slot < 0 ? 0.0f : P.row_scale[slot];
+            }
+            if (t.nk > 0) {
+                ++it;
+                if (!wait_bar_sleep(&acc_full[ab], ph)) {
+                    set_status(P.status, MOE_ERR_DEVICE_TIMEOUT);
+                    break;
+                }
+                fence_after();
+            }
+            const uint32_t tacc = tmem + (uint32_t(q * 32) << 16) + ab * kCols;
+            auto release = [&]() {  // this warp has read its part of the accumulators
+                fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR) mbar_arrive_cluster(mapa_shared(&acc_empty[ab], 0));
+                    else mbar_arrive(&acc_empty[ab]);
+                }
+            };
+            if constexpr (EPI == kGateUp) {
+                // units n0 + 64 ch .. + 63: gate in columns 0..127, up in 128..255
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    const int cu = 64 * ch + 32 * c;
+                    uint32_t gr[32], vr[32];
+                    tmem_load(tacc + cu, gr);
+                    tmem_load(tacc + 128 + cu, vr);
+                    tmem_wait(gr);
+                    tmem_wait(vr);
+                    if (c == 1) release();
+                    const int u0 = t.n0 + cu;
+                    if (u0 >= P.N || vrows <= 0) continue;
+                    float g[32], v[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        g[j] = __uint_as_float(gr[j]);
+                        v[j] = __uint_as_float(vr[j]);
+                    }
+                    if (P.bias0) {
+                        if (P.interleaved) {
+                            float z[32] = {};
+                            add_bias(P.bias0 + t.e * P.sbias, 2 * u0, 2 * P.N, z);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) { g[j] += z[2 * j]; v[j] += z[2 * j + 1]; z[2 * j] = z[2 * j + 1] = 0.f; }
+                            add_bias(P.bias0 + t.e * P.sbias, 2 * u0 + 32, 2 * P.N, z);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) { g[16 + j] += z[2 * j]; v[16 + j] += z[2 * j + 1]; }
+                        } else {
+                            add_bias(P.bias0 + t.e * P.sbias, u0, P.N, g);
+                            add_bias(P.bias1 + t.e * P.sbias, u0, P.N, v);
+                        }
+                    }
+                    const int bytes = (P.N - u0) * 2;  // of a row of units from u0 on
+                    uint4 w[4];
+                    if (P.pre) {
+                        __nv_bfloat16* pr = P.pre + (t.pos0 + wrow) * P.ldp;
+                        if (P.interleaved) {
+                            float f[32];
+                            weave(g, v, 0, f);
+                            pack_row(f, w);
+                            store_rows(sm, lane, w, pr + 2 * u0, P.ldp * 2, vrows, 2 * bytes);
+                            weave(g, v, 16, f);
+                            pack_row(f, w);
+                            store_rows(sm, lane, w, pr + 2 * u0 + 32, P.ldp * 2, vrows, 2 * bytes - 64);
+                        } else {
+                            pack_row(g, w);
+                            store_rows(sm, lane, w, pr + u0, P.ldp * 2, vrows, bytes);
+                            pack_row(v, w);
+                            store_rows(sm, lane, w, pr + P.N + u0, P.ldp * 2, vrows, bytes);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) g[j] = gated_h<true>(P.act, g[j], v[j], P.limit, P.alpha);
+                    pack_row(g, w);
+                    store_rows(sm, lane, w, static_cast<__nv_bfloat16*>(P.out) + row * P.ldo + u0, P.ldo * 2, vrows, bytes);
+                }
+            } else if constexpr (EPI == kDGated) {
+                float dw = 0.0f;
+                const bool valid = lane < vrows;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    const int col = t.n0 + 128 * ch + 32 * c;
+                    const int bytes = (P.N - col) * 2;
+                    float g[32], v[32];
+                    if (bytes > 0) {
+                        uint4 w[4];
+                        const __nv_bfloat16* pr = P.pre + (t.pos0 + wrow) * P.ldp;
+                        if (P.interleaved) {
+                            float f[32];
+                            load_rows(sm, lane, w, pr + 2 * col, P.ldp * 2, vrows, 2 * bytes);
+                            unpack_row(w, f);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) { g[j] = f[2 * j]; v[j] = f[2 * j + 1]; }
+                            load_rows(sm, lane, w, pr + 2 * col + 32, P.ldp * 2, vrows, 2 * bytes - 64);
+                            unpack_row(w, f);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) { g[16 + j] = f[2 * j]; v[16 + j] = f[2 * j + 1]; }
+                        } else {
+                            load_rows(sm, lane, w, pr + col, P.ldp * 2, vrows, bytes);
+                            unpack_row(w, g);
+                            load_rows(sm, lane, w, pr + P.N + col, P.ldp * 2, vrows, bytes);
+                            unpack_row(w, v);
+                        }
+                    }
+                    uint32_t dr[32];
+                    tmem_load(tacc + 128 * ch + 32 * c, dr);
+                    tmem_wait(dr);
+                    if (c == 3) release();
+                    if (bytes <= 0 || rows <= 0) continue;
+                    float hh[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        float h, hg, hv;
+                        gated_grad<true>(P.act, g[j], v[j], P.limit, P.alpha, h, hg, hv);
+                        const float d = __uint_as_float(dr[j]);
+                        if (8 * (j / 8) * 2 < bytes) dw += d * h;  // columns past N hold no unit
+                        const float dwt = d * rs;
+                        // rows without a slot are zeros: the weight gradients reduce over them
+                        g[j] = valid ? dwt * hg : 0.0f;
+                        v[j] = valid ? dwt * hv : 0.0f;
+                        hh[j] = valid ? h * rs : 0.0f;
+                    }
+                    uint4 w[4];
+                    __nv_bfloat16* o = P.dgu + row * 2 * P.N;
+                    const int64_t ldb = int64_t(P.N) * 4;
+                    if (P.interleaved) {
+                        float f[32];
+                        weave(g, v, 0, f);
+                        pack_row(f, w);
+                        store_rows(sm, lane, w, o + 2 * col, ldb, rows, 2 * bytes);
+                        weave(g, v, 16, f);
+                        pack_row(f, w);
+                        store_rows(sm, lane, w, o + 2 * col + 32, ldb, rows, 2 * bytes - 64);
+                    } else {
+                        pack_row(g, w);
+                        store_rows(sm, lane, w, o + col, ldb, rows, bytes);
+                        pack_row(v, w);
+                        store_rows(sm, lane, w, o + P.N + col, ldb, rows, bytes);
+                    }
+                    pack_row(hh, w);
+                    store_rows(sm, lane, w, P.hw + row * P.N + col, int64_t(P.N) * 2, rows, bytes);
+                }
+                if (P.partial && valid) P.partial[(row + lane) * P.parts + (t.n0 / kCols) * 2 + ch] = dw;
+            } else {
+                char* ob;
+                if constexpr (KIND == kTN)
+                    ob = static_cast<char*>(t.half ? P.out1 : P.out) + (t.e * P.so + row * P.ldo) * 2;
+                else
+                    ob = static_cast<char*>(P.out) + row * P.ldo * (P.out_f32 ? 4 : 2);
+                const int orows = KIND == kTN ? rows : vrows;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    const int col = t.n0 + 128 * ch + 32 * c;
+                    float f[32];
+                    if (t.nk > 0) {
+                        uint32_t dr[32];
+                        tmem_load(tacc + 128 * ch + 32 * c, dr);
+                        tmem_wait(dr);
+                        if (c == 3) release();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(dr[j]);
+                    } else {  // an expert without rows: its gradient is zero
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) f[j] = 0.0f;
+                    }
+                    const int bytes = (P.N - col) * 2;
+                    if (bytes <= 0 || orows <= 0) continue;
+                    uint4 w[4];
+                    if constexpr (KIND != kTN) {
+                        if (P.bias0) add_bias(P.bias0 + t.e * P.sbias, col, P.N, f);
+                        if (P.pre) {
+                            pack_row(f, w);
+                            store_rows(sm, lane, w, P.pre + row * P.ldp + col, P.ldp * 2, orows, bytes);
+                        }
+                        if (P.act != MOE_LINEAR_NONE) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) f[j] = linear_act<true>(P.act, f[j]);
+                        }
+                        if (P.row_scale) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) f[j] *= rs;
+                        }
+                        if (P.residual) {
+                            float z[32];
+                            load_rows(sm, lane, w, P.residual + row * P.ldr + col, P.ldr * 2, orows, bytes);
+                            unpack_row(w, z);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) f[j] += z[j];
+                        }
+                        if (P.out_f32) {
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                                for (int p = 0; p < 4; ++p)
+                                    w[p] = make_uint4(__float_as_uint(f[16 * b + 4 * p]), __float_as_uint(f[16 * b + 4 * p + 1]),
+                                                      __float_as_uint(f[16 * b + 4 * p + 2]), __float_as_uint(f[16 * b + 4 * p + 3]));
+                                store_rows(sm, lane, w, ob + (col + 16 * b) * 4, P.ldo * 4, orows, 2 * bytes - 64 * b);
+                            }
+                            continue;
+                        }
+                    }
+                    pack_row(f, w);
+                    store_rows(sm, lane, w, ob + col * 2, P.ldo * 2, orows, bytes);
+                }
+            }
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync();
+    if (warp == 0) {
+        fence_after();
+        if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
+}
+
+// ------------------------------------------------------------------ host side
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static EncodeFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeFn>(p);
+    });
+    return fn;
+}
+
+// bf16 tensor map, innermost dimension first; ld[i]: elements between indices of dimension i + 1.
+bool encode(CUtensorMap* m, const void* base, int rank, const int64_t* dims, const int64_t* ld, const int* box) {
+    EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t d[4], st[3];
+    cuuint32_t b[4], es[4] = {1, 1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = cuuint64_t(dims[i]);
+        b[i] = cuuint32_t(box[i]);
+        if (i < rank - 1) st[i] = cuuint64_t(ld[i]) * 2;
+    }
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void*>(base), d, st, b, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int sms() {
+    int dev = 0, n = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n;
+}
+
+template <int KIND, int EPI, bool PAIR>
+cudaError_t launch_t(const TcTrain& P, int64_t max_tiles, cudaStream_t s) {
+    using S = Shape<KIND, EPI, PAIR>;
+    auto kern = tc_train_kernel<KIND, EPI, PAIR>;
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = S::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = PAIR ? 2 : 1;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = PAIR ? 1 : 0;
+    int most = sms();
+    if (PAIR) {  // pairs that can be resident at once (an odd SM of a GPC stays out)
+        cfg.gridDim = dim3(2 * (most / 2));
+        int resident = 0;
+        if ((err = cudaOccupancyMaxActiveClusters(&resident, kern, &cfg)) != cudaSuccess) return err;
+        if (resident <= 0) return cudaErrorInvalidConfiguration;
+        most = std::min(resident, most / 2);
+    }
+    const int n = int(std::min<int64_t>(max_tiles, most));
+    if (n <= 0) return cudaSuccess;
+    cfg.gridDim = dim3(PAIR ? 2 * n : n);
+    if ((err = cudaLaunchKernelEx(&cfg, kern, P)) != cudaSuccess) return err;
+    return cudaGetLastError();
+}
+
+int64_t blocks_of(int64_t n, int64_t b) { return (n + b - 1) / b; }
+
+TcTrain base_of(const RowPlan& p) {
+    TcTrain P;
+    memset(&P, 0, sizeof(P));
+    P.offsets = p.offsets;
+    P.poff = p.poff;
+    P.uoff = p.uoff;
+    P.row_slot = p.row_slot;
+    P.E = p.E;
+    P.rows = p.T;
+    P.halves = 1;
+    P.status = p.status;
+    return P;
+}
+
+// A as [rows][halves][cols of a half]: K-major boxes of 64 columns x 128 rows, MN-major 64 x 64.
+bool map_a(CUtensorMap* m, const void* a, int64_t rows, int64_t ld, int64_t cols, int halves, bool mn) {
+    const int64_t d[3] = {cols, halves, rows}, st[2] = {halves > 1 ? cols : ld, ld};
+    const int box[3] = {64, 1, mn ? 64 : 128};
+    return encode(m, a, 3, d, st, box);
+}
+// Weight planes [E][rows][halves][K] as the K-major B operand.
+bool map_b_k(CUtensorMap* m, const void* b, int64_t E, int64_t rows, int halves, int64_t K) {
+    const int64_t d[4] = {K, halves, rows, E}, st[3] = {K, halves * K, rows * halves * K};
+    const int box[4] = {64, 1, 128, 1};
+    return encode(m, b, 4, d, st, box);
+}
+// [E][r][n] as the MN-major B operand.
+bool map_b_n(CUtensorMap* m, const void* b, int64_t E, int64_t r, int64_t n, int64_t ld, int64_t plane) {
+    const int64_t d[3] = {n, r, E}, st[2] = {ld, plane};
+    const int box[3] = {64, 64, 1};
+    return encode(m, b, 3, d, st, box);
+}
+
+// 256-row tiles on CTA pairs where they fill the GPU about as well as 128-row tiles.
+bool use_pair(const RowPlan& p, int64_t rows, int64_t n_blocks) {
+    if (p.offsets) return p.S >= 384 * int64_t(p.E);
+    return blocks_of(rows, 256) * n_blocks >= sms() / 2;
+}
+
+// Row tiles at most, and the dense problem's bands (as many row tiles as, with every column
+// block, fill the GPU: the tiles running together share both operands in L2).
+int64_t row_grid(TcTrain& P, const RowPlan& p, bool pair) {
+    const int BM = pair ? 256 : 128;
+    P.m_blocks = int(p.offsets ? blocks_of(p.max_rows, BM) + (pair ? std::min<int64_t>(p.E, p.S) : 0)
+                               : blocks_of(p.T, BM));
+    const int conc = pair ? sms() / 2 : sms();
+    P.band = std::max(1, std::min(P.m_blocks, conc / std::max(1, P.n_blocks)));
+    return int64_t(P.m_blocks) * P.n_blocks;
+}
+
+}  // namespace
+
+cudaError_t launch_tc_gemm_train(const GemmArgs& a, cudaStream_t s) {
+    TcTrain P = base_of(a.plan);
+    const bool grouped = a.plan.offsets != nullptr;
+    P.N = a.N;
+    P.n_blocks = int(blocks_of(a.N, kCols));
+    P.out = a.out;
+    P.out1 = a.out1;
+    P.ldo = a.ldo;
+    P.so = a.so;
+    if (a.kind == kTN) {
+        P.halves = a.split ? 2 : 1;
+        P.mrows = a.M / P.halves;
+        const int64_t rows = grouped ? a.plan.max_rows : a.R;
+        P.rows = a.R;
+        P.E = grouped ? a.plan.E : 1;
+        const int64_t tiles256 = blocks_of(P.mrows, 256) * P.halves * P.n_blocks * P.E;
+        const bool pair = tiles256 >= sms() / 2;
+        P.m_blocks = int(blocks_of(P.mrows, pair ? 256 : 128));
+        P.band = grouped ? 0 : std::max(1, std::min(P.n_blocks, (pair ? sms() / 2 : sms()) / (P.m_blocks * P.halves)));
+        if (!map_a(&P.a, a.a, rows, a.lda, P.mrows, P.halves, true) ||
+            !map_b_n(&P.b0, a.b, 1, rows, a.N, a.ldb, rows * a.ldb))
+            return cudaErrorInvalidValue;
+        const int64_t tiles = int64_t(P.E) * P.m_blocks * P.halves * P.n_blocks;
+        return pair ? launch_t<kTN, kStore, true>(P, tiles, s) : launch_t<kTN, kStore, false>(P, tiles, s);
+    }
+    const bool pair = use_pair(a.plan, a.M, P.n_blocks);
+    const int64_t rows = grouped ? a.plan.max_rows : a.M;
+    if (!grouped) P.rows = a.M;
+    RowPlan rp = a.plan;
+    rp.T = a.M;
+    const int64_t tiles = row_grid(P, rp, pair);
+    P.bias0 = static_cast<const __nv_bfloat16*>(a.bias);
+    P.sbias = a.sbias;
+    P.act = a.act;
+    P.row_scale = a.row_scale;
+    P.residual = static_cast<const __nv_bfloat16*>(a.residual);
+    P.ldr = a.ldr;
+    P.pre = static_cast<__nv_bfloat16*>(a.pre);
+    P.ldp = a.ldp;
+    P.out_f32 = a.out_f32;
+    const int64_t E = grouped ? a.plan.E : 1;
+    if (a.kind == kNT) {
+        P.nk = P.nk_half = int(blocks_of(a.R, kBR));
+        if (!map_a(&P.a, a.a, rows, a.lda, a.R, 1, false) || !map_b_k(&P.b0, a.b, E, a.N, 1, a.R)) return cudaErrorInvalidValue;
+        return pair ? launch_t<kNT, kStore, true>(P, tiles, s) : launch_t<kNT, kStore, false>(P, tiles, s);
+    }
+    const int halves = a.split ? 2 : 1;
+    const int64_t R = a.R / halves;
+    P.nk_half = int(blocks_of(R, kBR));
+    P.nk = P.nk_half * halves;
+    P.b_split = halves > 1;
+    if (!map_a(&P.a, a.a, rows, a.lda, R, halves, false) || !map_b_n(&P.b0, a.b, E, R, a.N, a.ldb, R * a.ldb))
+        return cudaErrorInvalidValue;
+    if (halves > 1 && !map_b_n(&P.b1, a.b1, E, R, a.N, a.ldb, R * a.ldb)) return cudaErrorInvalidValue;
+    return pair ? launch_t<kNN, kStore, true>(P, tiles, s) : launch_t<kNN, kStore, false>(P, tiles, s);
+}
+
+cudaError_t launch_tc_gateup(const GemmArgs& g, const GatedArgs& ga, cudaStream_t s) {
+    TcTrain P = base_of(g.plan);
+    const bool grouped = g.plan.offsets != nullptr;
+    P.N = ga.I;
+    P.n_blocks = int(blocks_of(ga.I, 128));
+    const bool pair = use_pair(g.plan, g.plan.T, P.n_blocks);
+    const int64_t tiles = row_grid(P, g.plan, pair);
+    const int64_t rows = grouped ? g.plan.max_rows : g.plan.T, E = grouped ? g.plan.E : 1;
+    P.nk = P.nk_half = int(blocks_of(g.R, kBR));
+    P.interleaved = ga.interleaved;
+    P.bias0 = static_cast<const __nv_bfloat16*>(g.bias);
+    P.bias1 = static_cast<const __nv_bfloat16*>(g.bias1);
+    P.sbias = g.sbias;
+    P.act = ga.act;
+    P.limit = ga.limit;
+    P.alpha = ga.alpha;
+    P.pre = static_cast<__nv_bfloat16*>(ga.pre);
+    P.ldp = 2 * ga.I;
+    P.out = ga.h;
+    P.ldo = ga.I;
+    if (!map_a(&P.a, g.a, rows, g.lda, g.R, 1, false) || !map_b_k(&P.b0, g.b, E, ga.I, ga.interleaved ? 2 : 1, g.R))
+        return cudaErrorInvalidValue;
+    if (!ga.interleaved && !map_b_k(&P.b1, g.b1, E, ga.I, 1, g.R)) return cudaErrorInvalidValue;
+    return pair ? launch_t<kNT, kGateUp, true>(P, tiles, s) : launch_t<kNT, kGateUp, false>(P, tiles, s);
+}
+
+int dgated_parts(int I) { return 2 * int(blocks_of(I, kCols)); }
+
+cudaError_t launch_tc_dgated(const GemmArgs& g, const GatedArgs& ga, float* partial, cudaStream_t s) {
+    TcTrain P = base_of(g.plan);
+    const bool grouped = g.plan.offsets != nullptr;
+    P.N = ga.I;
+    P.n_blocks = int(blocks_of(ga.I, kCols));
+    const bool pair = use_pair(g.plan, g.plan.T, P.n_blocks);
+    const int64_t tiles = row_grid(P, g.plan, pair);
+    const int64_t rows = grouped ? g.plan.max_rows : g.plan.T, E = grouped ? g.plan.E : 1;
+    P.nk = P.nk_half = int(blocks_of(g.R, kBR));
+    P.interleaved = ga.interleaved;
+    P.act = ga.act;
+    P.limit = ga.limit;
+    P.alpha = ga.alpha;
+    P.row_scale = ga.topk_w;
+    P.pre = static_cast<__nv_bfloat16*>(ga.pre);
+    P.ldp = 2 * ga.I;
+    P.dgu = static_cast<__nv_bfloat16*>(ga.dgu);
+    P.hw = static_cast<__nv_bfloat16*>(ga.hw);
+    P.partial = partial;
+    P.parts = dgated_parts(ga.I);
+    if (!map_a(&P.a, g.a, rows, g.lda, g.R, 1, false) || !map_b_n(&P.b0, g.b, E, g.R, ga.I, g.ldb, g.sb))
+        return cudaErrorInvalidValue;
+    return pair ? launch_t<kNN, kDGated, true>(P, tiles, s) : launch_t<kNN, kDGated, false>(P, tiles, s);
+}
+
+}  // namespace moe
