@@ -480,6 +480,7 @@ moe_status moe_ffn_backward(const moe_config* cfg, const moe_weights* w, const v
         GatherArgs ga;
         ga.plan = p;
         ga.src[0] = u; ga.ld[0] = ldu; ga.dst[0] = at<void>(ws, L.up);
+        ga.zero_pad = true;
         ga.src[1] = dy; ga.ld[1] = lddy; ga.dst[1] = at<void>(ws, L.dyp);
         ga.K = f.K; ga.es = f.es;
         MOE_CUDA(launch_gather_padded(ga, s));

@@ -43,6 +43,7 @@ struct GatherArgs {
     void* dst[2] = {nullptr, nullptr};
     int K = 0;
     int es = 2;  // bytes per element
+    bool zero_pad = false;  // the rows are reduced over (weight gradients)
 };
 cudaError_t launch_gather_padded(const GatherArgs& a, cudaStream_t s);
 

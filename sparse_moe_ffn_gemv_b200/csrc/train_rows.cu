@@ -65,6 +65,9 @@ __global__ void __launch_bounds__(kGatherThreads) gather_padded_kernel(const Gat
             p.row_slot[r] = slot;
             if (slot >= 0) p.slot_row[slot] = r;
         }
+        // padding: zeros as far as a reduction over the expert's rows reads (the next multiple
+        // of 64); rows of dropped slots are zeros too
+        if (i >= cnt[e] && (!a.zero_pad || i >= (cnt[e] + 63) / 64 * 64)) continue;
         const int64_t t = slot < 0 ? 0 : slot / p.k;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -237,7 +240,7 @@ __global__ void __launch_bounds__(kColVecs * kColRows) colsum_kernel(const Colsu
     int64_t r0 = 0, r1 = a.plan.T;
     if (a.plan.offsets) {
         r0 = a.plan.poff[e];
-        r1 = a.plan.poff[e + 1];
+        r1 = r0 + (a.plan.uoff[e + 1] - a.plan.uoff[e]);
     }
     const int64_t per = (r1 - r0 + splits - 1) / splits;
     const int64_t b = r0 + z * per, end = min(r1, b + per);

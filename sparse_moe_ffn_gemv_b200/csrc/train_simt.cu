@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kThreads) simt_gemm_kernel(const GemmArgs a) {
         e = blockIdx.z;
         if (grouped) {
             r0 = p.poff[e];
-            R = p.poff[e + 1];
+            R = r0 + (p.uoff[e + 1] - p.uoff[e]);
         }
     } else if (grouped) {
         M = p.poff[p.E];

@@ -43,7 +43,8 @@ constexpr int kMaxE = 512;
 constexpr int kABytes = 128 * kBR * 2;  // one 128-row operand tile
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-enum Epi { kStore = 0, kGateUp = 1, kDGated = 2 };
+// kGateUpI, kDGatedI: alternating gate / up columns.
+enum Epi { kStore = 0, kGateUp = 1, kGateUpI = 2, kDGated = 3, kDGatedI = 4 };
 
 struct TcTrain {
     CUtensorMap a, b0, b1;
@@ -56,7 +57,6 @@ struct TcTrain {
     int halves, m_blocks, n_blocks, band;
     int N;                  // columns of D (kGateUp: units)
     int nk, nk_half;        // reduction blocks (kNT, kNN) and of one half (kNN split)
-    int interleaved;        // kGateUp, kDGated: alternating gate / up columns
     int b_split;            // kNN: the second half reads b1
     // epilogue
     const __nv_bfloat16 *bias0, *bias1;
@@ -124,6 +124,12 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
         asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(bar))
                      : "memory");
 }
+// Arrive on the leader's barrier. CTA scope: what is handed over is TMEM, ordered by the tcgen05
+// fence before it; a release at cluster scope would first wait for the warp's global stores
+// (a third of the weight gradients' epilogue went there).
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(bar, 0)) : "memory");
+}
 // 32 accumulator columns of this lane's row; valid after tmem_wait.
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[32]) {
     asm volatile(
@@ -178,21 +184,26 @@ __device__ __forceinline__ void store_rows(uint8_t* sm, int lane, const uint4 (&
     }
     __syncwarp();
 }
-// Reads them; rows and bytes past the limits give zeros.
-__device__ __forceinline__ void load_rows(uint8_t* sm, int lane, uint4 (&v)[4], const void* base, int64_t ld_bytes,
-                                          int rows, int bytes) {
+// Reading them: fetch issues the loads (rows and bytes past the limits give zeros), turn hands
+// each lane its row.
+__device__ __forceinline__ void fetch_rows(int lane, uint4 (&x)[4], const void* base, int64_t ld_bytes, int rows,
+                                           int bytes) {
     const int c = lane & 3;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = i * 8 + (lane >> 2);
-        uint4 x = make_uint4(0, 0, 0, 0);
+        x[i] = make_uint4(0, 0, 0, 0);
         if (r < rows && c * 16 < bytes)
-            x = *reinterpret_cast<const uint4*>(static_cast<const char*>(base) + r * ld_bytes + c * 16);
-        *reinterpret_cast<uint4*>(sm + seg(r, c)) = x;
+            x[i] = *reinterpret_cast<const uint4*>(static_cast<const char*>(base) + r * ld_bytes + c * 16);
     }
+}
+__device__ __forceinline__ void turn_rows(uint8_t* sm, int lane, uint4 (&x)[4]) {
+    const int c = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(sm + seg(i * 8 + (lane >> 2), c)) = x[i];
     __syncwarp();
 #pragma unroll
-    for (int c2 = 0; c2 < 4; ++c2) v[c2] = *reinterpret_cast<const uint4*>(sm + seg(lane, c2));
+    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const uint4*>(sm + seg(lane, i));
     __syncwarp();
 }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -214,14 +225,6 @@ __device__ __forceinline__ void unpack_row(const uint4 (&v)[4], float (&f)[32]) 
         for (int j = 0; j < 8; ++j) f[8 * c + j] = t[j];
     }
 }
-// Alternating columns of 16 units: f[2i] = a[i0 + i], f[2i + 1] = b[i0 + i].
-__device__ __forceinline__ void weave(const float (&a)[32], const float (&b)[32], int i0, float (&f)[32]) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        f[2 * i] = a[i0 + i];
-        f[2 * i + 1] = b[i0 + i];
-    }
-}
 // 32 bias values from column c on, columns past `limit` zero (limit and c multiples of 8).
 __device__ __forceinline__ void add_bias(const __nv_bfloat16* b, int c, int limit, float (&f)[32]) {
 #pragma unroll
@@ -239,8 +242,8 @@ struct Tile {
     int e;          // expert, or 0
     int half;       // kTN: plane of D
     int64_t row0;   // first row of D in A's row space (kTN: in the plane)
-    int limit;      // rows of D this tile owns (up to the tile's height)
-    int nvalid;     // of those, rows that hold slots (kNT, kNN grouped)
+    int limit;      // rows of D to write (grouped: up to the next reduction block of kTN)
+    int nvalid;     // of those, rows that hold slots
     int n0;         // first column
     int nk;         // reduction blocks
     int64_t r0;     // kTN: first reduction row
@@ -261,7 +264,9 @@ struct Shape {
     static constexpr int RING = STAGES * STAGE;
     static constexpr int STG = kEpiWarps * 2048;
     static constexpr int SMEM = RING + STG + 256 + int(sizeof(Tables)) + 1024;
-    static constexpr int UNITS = EPI == kGateUp ? 128 : kCols;  // columns (units) a tile covers
+    static constexpr bool GATEUP = EPI == kGateUp || EPI == kGateUpI, DGATED = EPI == kDGated || EPI == kDGatedI;
+    static constexpr bool IL = EPI == kGateUpI || EPI == kDGatedI;
+    static constexpr int UNITS = GATEUP ? 128 : kCols;  // columns (units) a tile covers
     static_assert(SMEM <= 232448, "dynamic shared memory per block");
 };
 
@@ -326,8 +331,9 @@ __device__ __forceinline__ Tile tile_of(const TcTrain& P, const Tables& tb, int 
     t.e = lo;
     t.row0 = tb.poff[lo] + int64_t(mt) * S::BM;
     t.n0 = nb * S::UNITS;
-    t.limit = min(S::BM, int(tb.poff[lo + 1] - t.row0));
-    t.nvalid = max(0, min(S::BM, tb.uoff[lo + 1] - tb.uoff[lo] - mt * S::BM));
+    const int left = tb.uoff[lo + 1] - tb.uoff[lo] - mt * S::BM;
+    t.limit = max(0, min(S::BM, (left + kBR - 1) / kBR * kBR));
+    t.nvalid = max(0, min(S::BM, left));
     t.pos0 = tb.uoff[lo] + int64_t(mt) * S::BM;
     return t;
 }
@@ -459,14 +465,14 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
 #pragma unroll
                             for (int j = 0; j < S::B_BYTES / 8192; ++j)
                                 load3<PAIR>(sb + j * 8192, mb, &full[stage], fb, nb + 64 * j, kc, t.e, pol);
-                        } else if constexpr (EPI == kGateUp) {
+                        } else if constexpr (S::GATEUP) {
                             // gate rows, then up rows; of a pair, CTA 0 gate and CTA 1 up
                             if constexpr (PAIR) {
-                                if (P.interleaved) load4<PAIR>(sb, &P.b0, &full[stage], fb, kc, int(crank), t.n0, t.e, pol);
+                                if (S::IL) load4<PAIR>(sb, &P.b0, &full[stage], fb, kc, int(crank), t.n0, t.e, pol);
                                 else load4<PAIR>(sb, crank ? &P.b1 : &P.b0, &full[stage], fb, kc, 0, t.n0, t.e, pol);
                             } else {
                                 load4<PAIR>(sb, &P.b0, &full[stage], fb, kc, 0, t.n0, t.e, pol);
-                                if (P.interleaved) load4<PAIR>(sb + kABytes, &P.b0, &full[stage], fb, kc, 1, t.n0, t.e, pol);
+                                if (S::IL) load4<PAIR>(sb + kABytes, &P.b0, &full[stage], fb, kc, 1, t.n0, t.e, pol);
                                 else load4<PAIR>(sb + kABytes, &P.b1, &full[stage], fb, kc, 0, t.n0, t.e, pol);
                             }
                         } else {
@@ -537,6 +543,20 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
         const int ch = (warp - 2) >> 2;            // column half
         uint8_t* sm = stg + (warp - 2) * 2048;
         const int wrow = int(crank) * 128 + q * 32;  // first tile row of the warp
+        // kDGated: pre-activations of the next 32 columns (gate, up), one chunk ahead
+        uint4 x0[4], x1[4];
+        auto fetch_pre = [&](const Tile& t, int c, int vrows) {
+            const int col = t.n0 + 128 * ch + 32 * c;
+            const int bytes = (P.N - col) * 2;
+            const __nv_bfloat16* pr = P.pre + (t.pos0 + wrow) * P.ldp;
+            if constexpr (S::IL) {
+                fetch_rows(lane, x0, pr + 2 * col, P.ldp * 2, vrows, 2 * bytes);
+                fetch_rows(lane, x1, pr + 2 * col + 32, P.ldp * 2, vrows, 2 * bytes - 64);
+            } else {
+                fetch_rows(lane, x0, pr + col, P.ldp * 2, vrows, bytes);
+                fetch_rows(lane, x1, pr + P.N + col, P.ldp * 2, vrows, bytes);
+            }
+        };
         uint32_t it = 0;
         for (int idx = tile0; idx < total; idx += tstep) {
             const Tile t = tile_of<KIND, EPI, PAIR>(P, tb, idx);
@@ -549,6 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                 const int slot = P.row_slot[row + lane];
                 rs = slot < 0 ? 0.0f : P.row_scale[slot];
             }
+            if constexpr (S::DGATED) fetch_pre(t, 0, vrows);
             if (t.nk > 0) {
                 ++it;
                 if (!wait_bar_sleep(&acc_full[ab], ph)) {
@@ -562,11 +583,11 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                 fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if constexpr (PAIR) mbar_arrive_cluster(mapa_shared(&acc_empty[ab], 0));
+                    if constexpr (PAIR) arrive_leader(&acc_empty[ab]);
                     else mbar_arrive(&acc_empty[ab]);
                 }
             };
-            if constexpr (EPI == kGateUp) {
+            if constexpr (S::GATEUP) {
                 // units n0 + 64 ch .. + 63: gate in columns 0..127, up in 128..255
 #pragma unroll 1
                 for (int c = 0; c < 2; ++c) {
@@ -586,14 +607,17 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                         v[j] = __uint_as_float(vr[j]);
                     }
                     if (P.bias0) {
-                        if (P.interleaved) {
-                            float z[32] = {};
-                            add_bias(P.bias0 + t.e * P.sbias, 2 * u0, 2 * P.N, z);
+                        if constexpr (S::IL) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) { g[j] += z[2 * j]; v[j] += z[2 * j + 1]; z[2 * j] = z[2 * j + 1] = 0.f; }
-                            add_bias(P.bias0 + t.e * P.sbias, 2 * u0 + 32, 2 * P.N, z);
+                            for (int b = 0; b < 2; ++b) {
+                                float z[32] = {};
+                                add_bias(P.bias0 + t.e * P.sbias, 2 * u0 + 32 * b, 2 * P.N, z);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) { g[16 + j] += z[2 * j]; v[16 + j] += z[2 * j + 1]; }
+                                for (int j = 0; j < 16; ++j) {
+                                    g[16 * b + j] += z[2 * j];
+                                    v[16 * b + j] += z[2 * j + 1];
+                                }
+                            }
                         } else {
                             add_bias(P.bias0 + t.e * P.sbias, u0, P.N, g);
                             add_bias(P.bias1 + t.e * P.sbias, u0, P.N, v);
@@ -603,14 +627,17 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                     uint4 w[4];
                     if (P.pre) {
                         __nv_bfloat16* pr = P.pre + (t.pos0 + wrow) * P.ldp;
-                        if (P.interleaved) {
-                            float f[32];
-                            weave(g, v, 0, f);
-                            pack_row(f, w);
-                            store_rows(sm, lane, w, pr + 2 * u0, P.ldp * 2, vrows, 2 * bytes);
-                            weave(g, v, 16, f);
-                            pack_row(f, w);
-                            store_rows(sm, lane, w, pr + 2 * u0 + 32, P.ldp * 2, vrows, 2 * bytes - 64);
+                        if constexpr (S::IL) {
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const int j = 16 * b + 4 * i;
+                                    w[i] = make_uint4(pack2(g[j], v[j]), pack2(g[j + 1], v[j + 1]),
+                                                      pack2(g[j + 2], v[j + 2]), pack2(g[j + 3], v[j + 3]));
+                                }
+                                store_rows(sm, lane, w, pr + 2 * u0 + 32 * b, P.ldp * 2, vrows, 2 * bytes - 64 * b);
+                            }
                         } else {
                             pack_row(g, w);
                             store_rows(sm, lane, w, pr + u0, P.ldp * 2, vrows, bytes);
@@ -623,133 +650,151 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                     pack_row(g, w);
                     store_rows(sm, lane, w, static_cast<__nv_bfloat16*>(P.out) + row * P.ldo + u0, P.ldo * 2, vrows, bytes);
                 }
-            } else if constexpr (EPI == kDGated) {
+            } else if constexpr (S::DGATED) {
                 float dw = 0.0f;
                 const bool valid = lane < vrows;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     const int col = t.n0 + 128 * ch + 32 * c;
                     const int bytes = (P.N - col) * 2;
-                    float g[32], v[32];
-                    if (bytes > 0) {
-                        uint4 w[4];
-                        const __nv_bfloat16* pr = P.pre + (t.pos0 + wrow) * P.ldp;
-                        if (P.interleaved) {
-                            float f[32];
-                            load_rows(sm, lane, w, pr + 2 * col, P.ldp * 2, vrows, 2 * bytes);
-                            unpack_row(w, f);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) { g[j] = f[2 * j]; v[j] = f[2 * j + 1]; }
-                            load_rows(sm, lane, w, pr + 2 * col + 32, P.ldp * 2, vrows, 2 * bytes - 64);
-                            unpack_row(w, f);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) { g[16 + j] = f[2 * j]; v[16 + j] = f[2 * j + 1]; }
-                        } else {
-                            load_rows(sm, lane, w, pr + col, P.ldp * 2, vrows, bytes);
-                            unpack_row(w, g);
-                            load_rows(sm, lane, w, pr + P.N + col, P.ldp * 2, vrows, bytes);
-                            unpack_row(w, v);
-                        }
-                    }
+                    turn_rows(sm, lane, x0);
+                    turn_rows(sm, lane, x1);
+                    const uint32_t a0[16] = {x0[0].x, x0[0].y, x0[0].z, x0[0].w, x0[1].x, x0[1].y, x0[1].z, x0[1].w,
+                                             x0[2].x, x0[2].y, x0[2].z, x0[2].w, x0[3].x, x0[3].y, x0[3].z, x0[3].w};
+                    const uint32_t a1[16] = {x1[0].x, x1[0].y, x1[0].z, x1[0].w, x1[1].x, x1[1].y, x1[1].z, x1[1].w,
+                                             x1[2].x, x1[2].y, x1[2].z, x1[2].w, x1[3].x, x1[3].y, x1[3].z, x1[3].w};
+                    if (c < 3) fetch_pre(t, c + 1, vrows);
                     uint32_t dr[32];
                     tmem_load(tacc + 128 * ch + 32 * c, dr);
                     tmem_wait(dr);
                     if (c == 3) release();
                     if (bytes <= 0 || rows <= 0) continue;
-                    float hh[32];
+                    uint32_t o0[16], o1[16], oh[16];  // dg and dv (or alternating), w h
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        float h, hg, hv;
-                        gated_grad<true>(P.act, g[j], v[j], P.limit, P.alpha, h, hg, hv);
-                        const float d = __uint_as_float(dr[j]);
-                        if (8 * (j / 8) * 2 < bytes) dw += d * h;  // columns past N hold no unit
-                        const float dwt = d * rs;
-                        // rows without a slot are zeros: the weight gradients reduce over them
-                        g[j] = valid ? dwt * hg : 0.0f;
-                        v[j] = valid ? dwt * hv : 0.0f;
-                        hh[j] = valid ? h * rs : 0.0f;
+                    for (int j = 0; j < 32; j += 2) {
+                        float d[2], dg[2], dv[2], h[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int u = j + i;
+                            float g, v;
+                            if constexpr (S::IL) {
+                                const uint32_t x = u < 16 ? a0[u] : a1[u - 16];
+                                g = bf16lo(x);
+                                v = bf16hi(x);
+                            } else {
+                                g = i ? bf16hi(a0[u / 2]) : bf16lo(a0[u / 2]);
+                                v = i ? bf16hi(a1[u / 2]) : bf16lo(a1[u / 2]);
+                            }
+                            float hg, hv;
+                            gated_grad<true>(P.act, g, v, P.limit, P.alpha, h[i], hg, hv);
+                            d[i] = __uint_as_float(dr[u]);
+                            if (8 * (j / 8) * 2 < bytes) dw += d[i] * h[i];  // columns past N hold no unit
+                            // rows without a slot are zeros: the weight gradients reduce over them
+                            dg[i] = valid ? d[i] * rs * hg : 0.0f;
+                            dv[i] = valid ? d[i] * rs * hv : 0.0f;
+                            h[i] = valid ? h[i] * rs : 0.0f;
+                        }
+                        if constexpr (S::IL) {
+                            (j < 16 ? o0[j % 16] : o1[j % 16]) = pack2(dg[0], dv[0]);
+                            (j < 16 ? o0[j % 16 + 1] : o1[j % 16 + 1]) = pack2(dg[1], dv[1]);
+                        } else {
+                            o0[j / 2] = pack2(dg[0], dg[1]);
+                            o1[j / 2] = pack2(dv[0], dv[1]);
+                        }
+                        oh[j / 2] = pack2(h[0], h[1]);
                     }
-                    uint4 w[4];
                     __nv_bfloat16* o = P.dgu + row * 2 * P.N;
                     const int64_t ldb = int64_t(P.N) * 4;
-                    if (P.interleaved) {
-                        float f[32];
-                        weave(g, v, 0, f);
-                        pack_row(f, w);
-                        store_rows(sm, lane, w, o + 2 * col, ldb, rows, 2 * bytes);
-                        weave(g, v, 16, f);
-                        pack_row(f, w);
-                        store_rows(sm, lane, w, o + 2 * col + 32, ldb, rows, 2 * bytes - 64);
+                    auto put = [&](const uint32_t (&r)[16], void* at, int64_t ld, int n) {
+                        const uint4 w[4] = {make_uint4(r[0], r[1], r[2], r[3]), make_uint4(r[4], r[5], r[6], r[7]),
+                                            make_uint4(r[8], r[9], r[10], r[11]), make_uint4(r[12], r[13], r[14], r[15])};
+                        store_rows(sm, lane, w, at, ld, rows, n);
+                    };
+                    if constexpr (S::IL) {
+                        put(o0, o + 2 * col, ldb, 2 * bytes);
+                        put(o1, o + 2 * col + 32, ldb, 2 * bytes - 64);
                     } else {
-                        pack_row(g, w);
-                        store_rows(sm, lane, w, o + col, ldb, rows, bytes);
-                        pack_row(v, w);
-                        store_rows(sm, lane, w, o + P.N + col, ldb, rows, bytes);
+                        put(o0, o + col, ldb, bytes);
+                        put(o1, o + P.N + col, ldb, bytes);
                     }
-                    pack_row(hh, w);
-                    store_rows(sm, lane, w, P.hw + row * P.N + col, int64_t(P.N) * 2, rows, bytes);
+                    put(oh, P.hw + row * P.N + col, int64_t(P.N) * 2, bytes);
                 }
                 if (P.partial && valid) P.partial[(row + lane) * P.parts + (t.n0 / kCols) * 2 + ch] = dw;
-            } else {
-                char* ob;
-                if constexpr (KIND == kTN)
-                    ob = static_cast<char*>(t.half ? P.out1 : P.out) + (t.e * P.so + row * P.ldo) * 2;
-                else
-                    ob = static_cast<char*>(P.out) + row * P.ldo * (P.out_f32 ? 4 : 2);
-                const int orows = KIND == kTN ? rows : vrows;
-#pragma unroll 1
+            } else if constexpr (KIND == kTN) {
+                // everything out of TMEM first: the next products need not wait for the stores
+                uint4 w[4][4];
+#pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const int col = t.n0 + 128 * ch + 32 * c;
                     float f[32];
                     if (t.nk > 0) {
                         uint32_t dr[32];
                         tmem_load(tacc + 128 * ch + 32 * c, dr);
                         tmem_wait(dr);
-                        if (c == 3) release();
 #pragma unroll
                         for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(dr[j]);
                     } else {  // an expert without rows: its gradient is zero
 #pragma unroll
                         for (int j = 0; j < 32; ++j) f[j] = 0.0f;
                     }
+                    pack_row(f, w[c]);
+                }
+                if (t.nk > 0) release();
+                if (rows <= 0) continue;
+                __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(t.half ? P.out1 : P.out) + t.e * P.so + row * P.ldo;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int col = t.n0 + 128 * ch + 32 * c;
+                    store_rows(sm, lane, w[c], ob + col, P.ldo * 2, rows, (P.N - col) * 2);
+                }
+            } else {
+                char* ob = static_cast<char*>(P.out) + row * P.ldo * (P.out_f32 ? 4 : 2);
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    const int col = t.n0 + 128 * ch + 32 * c;
+                    uint32_t dr[32];
+                    tmem_load(tacc + 128 * ch + 32 * c, dr);
+                    tmem_wait(dr);
+                    if (c == 3) release();
+                    float f[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(dr[j]);
                     const int bytes = (P.N - col) * 2;
-                    if (bytes <= 0 || orows <= 0) continue;
+                    if (bytes <= 0 || vrows <= 0) continue;
                     uint4 w[4];
-                    if constexpr (KIND != kTN) {
-                        if (P.bias0) add_bias(P.bias0 + t.e * P.sbias, col, P.N, f);
-                        if (P.pre) {
-                            pack_row(f, w);
-                            store_rows(sm, lane, w, P.pre + row * P.ldp + col, P.ldp * 2, orows, bytes);
-                        }
-                        if (P.act != MOE_LINEAR_NONE) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) f[j] = linear_act<true>(P.act, f[j]);
-                        }
-                        if (P.row_scale) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) f[j] *= rs;
-                        }
-                        if (P.residual) {
-                            float z[32];
-                            load_rows(sm, lane, w, P.residual + row * P.ldr + col, P.ldr * 2, orows, bytes);
-                            unpack_row(w, z);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) f[j] += z[j];
-                        }
-                        if (P.out_f32) {
-#pragma unroll
-                            for (int b = 0; b < 2; ++b) {
-#pragma unroll
-                                for (int p = 0; p < 4; ++p)
-                                    w[p] = make_uint4(__float_as_uint(f[16 * b + 4 * p]), __float_as_uint(f[16 * b + 4 * p + 1]),
-                                                      __float_as_uint(f[16 * b + 4 * p + 2]), __float_as_uint(f[16 * b + 4 * p + 3]));
-                                store_rows(sm, lane, w, ob + (col + 16 * b) * 4, P.ldo * 4, orows, 2 * bytes - 64 * b);
-                            }
-                            continue;
-                        }
+                    if (P.bias0) add_bias(P.bias0 + t.e * P.sbias, col, P.N, f);
+                    if (P.pre) {
+                        pack_row(f, w);
+                        store_rows(sm, lane, w, P.pre + row * P.ldp + col, P.ldp * 2, vrows, bytes);
                     }
-                    pack_row(f, w);
-                    store_rows(sm, lane, w, ob + col * 2, P.ldo * 2, orows, bytes);
+                    if (P.act != MOE_LINEAR_NONE) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) f[j] = linear_act<true>(P.act, f[j]);
+                    }
+                    if (P.row_scale) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) f[j] *= rs;
+                    }
+                    if (P.residual) {
+                        float z[32];
+                        fetch_rows(lane, w, P.residual + row * P.ldr + col, P.ldr * 2, vrows, bytes);
+                        turn_rows(sm, lane, w);
+                        unpack_row(w, z);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) f[j] += z[j];
+                    }
+                    if (P.out_f32) {
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                            for (int p = 0; p < 4; ++p)
+                                w[p] = make_uint4(__float_as_uint(f[16 * b + 4 * p]), __float_as_uint(f[16 * b + 4 * p + 1]),
+                                                  __float_as_uint(f[16 * b + 4 * p + 2]), __float_as_uint(f[16 * b + 4 * p + 3]));
+                            store_rows(sm, lane, w, ob + (col + 16 * b) * 4, P.ldo * 4, vrows, 2 * bytes - 64 * b);
+                        }
+                    } else {
+                        pack_row(f, w);
+                        store_rows(sm, lane, w, ob + col * 2, P.ldo * 2, vrows, bytes);
+                    }
                 }
             }
         }
@@ -955,7 +1000,6 @@ cudaError_t launch_tc_gateup(const GemmArgs& g, const GatedArgs& ga, cudaStream_
     const int64_t tiles = row_grid(P, g.plan, pair);
     const int64_t rows = grouped ? g.plan.max_rows : g.plan.T, E = grouped ? g.plan.E : 1;
     P.nk = P.nk_half = int(blocks_of(g.R, kBR));
-    P.interleaved = ga.interleaved;
     P.bias0 = static_cast<const __nv_bfloat16*>(g.bias);
     P.bias1 = static_cast<const __nv_bfloat16*>(g.bias1);
     P.sbias = g.sbias;
@@ -969,6 +1013,7 @@ cudaError_t launch_tc_gateup(const GemmArgs& g, const GatedArgs& ga, cudaStream_
     if (!map_a(&P.a, g.a, rows, g.lda, g.R, 1, false) || !map_b_k(&P.b0, g.b, E, ga.I, ga.interleaved ? 2 : 1, g.R))
         return cudaErrorInvalidValue;
     if (!ga.interleaved && !map_b_k(&P.b1, g.b1, E, ga.I, 1, g.R)) return cudaErrorInvalidValue;
+    if (ga.interleaved) return pair ? launch_t<kNT, kGateUpI, true>(P, tiles, s) : launch_t<kNT, kGateUpI, false>(P, tiles, s);
     return pair ? launch_t<kNT, kGateUp, true>(P, tiles, s) : launch_t<kNT, kGateUp, false>(P, tiles, s);
 }
 
@@ -983,7 +1028,6 @@ cudaError_t launch_tc_dgated(const GemmArgs& g, const GatedArgs& ga, float* part
     const int64_t tiles = row_grid(P, g.plan, pair);
     const int64_t rows = grouped ? g.plan.max_rows : g.plan.T, E = grouped ? g.plan.E : 1;
     P.nk = P.nk_half = int(blocks_of(g.R, kBR));
-    P.interleaved = ga.interleaved;
     P.act = ga.act;
     P.limit = ga.limit;
     P.alpha = ga.alpha;
@@ -996,6 +1040,7 @@ cudaError_t launch_tc_dgated(const GemmArgs& g, const GatedArgs& ga, float* part
     P.parts = dgated_parts(ga.I);
     if (!map_a(&P.a, g.a, rows, g.lda, g.R, 1, false) || !map_b_n(&P.b0, g.b, E, g.R, ga.I, g.ldb, g.sb))
         return cudaErrorInvalidValue;
+    if (ga.interleaved) return pair ? launch_t<kNN, kDGatedI, true>(P, tiles, s) : launch_t<kNN, kDGatedI, false>(P, tiles, s);
     return pair ? launch_t<kNN, kDGated, true>(P, tiles, s) : launch_t<kNN, kDGated, false>(P, tiles, s);
 }
 
