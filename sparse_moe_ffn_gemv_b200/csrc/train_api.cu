@@ -151,6 +151,18 @@ struct FfnWs {
     size_t parts;     // [rows, dgated_parts] partial sums of dtopk_w (bf16, routed)
     size_t total;
 };
+// The plan's sizes; offsets only says routed or dense here.
+RowPlan shape_plan(const FfnShape& f) {
+    static const int32_t routed = 0;
+    RowPlan p;
+    p.T = f.T;
+    p.S = f.S;
+    p.E = f.E;
+    p.k = f.k;
+    p.max_rows = f.rows;
+    p.offsets = f.dense ? nullptr : &routed;
+    return p;
+}
 FfnWs ffn_ws(const FfnShape& f, bool backward) {
     FfnWs L{};
     Carver c;
@@ -164,7 +176,7 @@ FfnWs ffn_ws(const FfnShape& f, bool backward) {
         L.up = c.take(f.rows * f.K * f.es);
         if (backward) L.dyp = c.take(f.rows * f.K * f.es);
         L.rows_out = c.take(f.rows * f.K * 4);
-        if (backward && !f32) L.parts = c.take(f.rows * dgated_parts(f.I) * 4);
+        if (backward && !f32) L.parts = c.take(f.rows * dgated_parts(shape_plan(f), f.I, f.K) * 4);
     }
     if (backward) {
         if (f32) L.dh = c.take(f.rows * f.I * 4);
@@ -183,12 +195,7 @@ FfnWs ffn_ws(const FfnShape& f, bool backward) {
 
 RowPlan row_plan(const FfnShape& f, const int32_t* offsets, const int32_t* sorted_slot, void* ws, const FfnWs& L,
                  int32_t* status) {
-    RowPlan p;
-    p.T = f.T;
-    p.S = f.S;
-    p.E = f.E;
-    p.k = f.k;
-    p.max_rows = f.rows;
+    RowPlan p = shape_plan(f);
     p.status = status;
     if (!f.dense) {
         p.offsets = offsets;
@@ -519,7 +526,7 @@ moe_status moe_ffn_backward(const moe_config* cfg, const moe_weights* w, const v
     } else {
         float* parts = dtopk_w ? at<float>(ws, L.parts) : nullptr;
         MOE_CUDA(launch_tc_dgated(g, ga, parts, s));
-        if (dtopk_w) MOE_CUDA(launch_dtopk(ga, parts, dgated_parts(f.I), s));
+        if (dtopk_w) MOE_CUDA(launch_dtopk(ga, parts, dgated_parts(p, f.I, f.K), s));
     }
     // du = dg Wg + dv Wu
     if (du) {

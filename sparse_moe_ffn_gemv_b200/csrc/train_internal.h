@@ -120,10 +120,10 @@ struct GatedArgs {
 cudaError_t launch_gated_forward(const GatedArgs& a, cudaStream_t s);
 cudaError_t launch_gated_backward(const GatedArgs& a, cudaStream_t s);
 // bf16: in the epilogue of the product g = (gate/up forward; dy Wd backward), which writes
-// pre and h, or dgu, hw and per row dgated_parts(I) partial sums of dh . h.
+// pre and h, or dgu, hw and per row dgated_parts(plan, I, R) partial sums of dh . h.
 cudaError_t launch_tc_gateup(const GemmArgs& g, const GatedArgs& ga, cudaStream_t s);
 cudaError_t launch_tc_dgated(const GemmArgs& g, const GatedArgs& ga, float* partial, cudaStream_t s);
-int dgated_parts(int I);
+int dgated_parts(const RowPlan& p, int I, int64_t R);
 // dtopk_w[slot] = the row's partial sums (+ dyp . down_b), from GatedArgs' plan, dtopk_w, dyp, down_b, K.
 cudaError_t launch_dtopk(const GatedArgs& a, const float* partial, int parts, cudaStream_t s);
 

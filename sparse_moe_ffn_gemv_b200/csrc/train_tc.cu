@@ -26,6 +26,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 #include "ptx.cuh"
@@ -46,8 +47,28 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 // kGateUpI, kDGatedI: alternating gate / up columns.
 enum Epi { kStore = 0, kGateUp = 1, kGateUpI = 2, kDGated = 3, kDGatedI = 4 };
 
+// Division by a launch constant: n / d = umulhi(n, m) >> s for 0 <= n < 2^31 (m = ceil(2^(32+s) / d)
+// with 2^s < d <= 2^(s+1)), two instructions in place of a divide in every role's tile walk.
+struct FastDiv {
+    uint32_t d, m, s;
+    __device__ __forceinline__ int operator()(int n) const {
+        return d == 1 ? n : int(__umulhi(uint32_t(n), m) >> s);
+    }
+};
+FastDiv fast_div(int64_t d) {
+    FastDiv f{uint32_t(d), 0, 0};
+    if (d <= 1) return f;
+    uint32_t lg = 0;  // ceil(log2 d)
+    while ((int64_t(1) << lg) < d) ++lg;
+    f.s = lg - 1;
+    f.m = uint32_t(((uint64_t(1) << (32 + f.s)) + d - 1) / d);
+    return f;
+}
+
 struct TcTrain {
     CUtensorMap a, b0, b1;
+    FastDiv d_tile, d_m, d_band, d_width, d_tail;  // see tile_of
+    int splits;             // CTAs of a cluster that share a tile's reduction (SPLIT)
     // rows
     const int32_t *offsets, *poff, *uoff, *row_slot;  // grouped (offsets != null)
     int E;
@@ -278,22 +299,20 @@ __device__ __forceinline__ Tile tile_of(const TcTrain& P, const Tables& tb, int 
     t.e = 0;
     t.r0 = t.pos0 = 0;
     if constexpr (KIND == kTN) {
-        // expert by expert; within one, the row blocks of a column block in turn
-        const int per = P.m_blocks * P.halves * P.n_blocks;
-        t.e = idx / per;
-        int l = idx - t.e * per;
+        // expert by expert; within one (dense: within a band of column blocks), the row blocks
+        // of a column block in turn
+        t.e = P.d_tile(idx);
+        const int l = idx - t.e * int(P.d_tile.d);
         int mb, nb;
-        if (P.band > 0) {  // dense: bands of column blocks, every row block in turn
-            const int mt = P.m_blocks * P.halves;
-            const int b = l / (P.band * mt), w = l - b * P.band * mt;
-            const int width = min(P.band, P.n_blocks - b * P.band);
-            mb = w / width;
-            nb = b * P.band + (w - mb * width);
+        const int b = P.d_band(l), w = l - b * int(P.d_band.d), c0 = b * P.band;
+        if (P.n_blocks - c0 >= P.band) {
+            mb = P.d_width(w);
+            nb = c0 + w - mb * P.band;
         } else {
-            nb = l / (P.m_blocks * P.halves);
-            mb = l - nb * P.m_blocks * P.halves;
+            mb = P.d_tail(w);
+            nb = c0 + w - mb * int(P.d_tail.d);
         }
-        t.half = mb / P.m_blocks;
+        t.half = P.d_m(mb);
         t.row0 = int64_t(mb - t.half * P.m_blocks) * S::BM;
         t.limit = int(min(int64_t(S::BM), P.mrows - t.row0));
         t.nvalid = t.limit;
@@ -308,11 +327,16 @@ __device__ __forceinline__ Tile tile_of(const TcTrain& P, const Tables& tb, int 
     }
     t.nk = P.nk;
     if (!P.offsets) {  // bands of row tiles, every column block in turn
-        const int per = P.band * P.n_blocks;
-        const int b = idx / per, w = idx - b * per;
-        const int width = min(P.band, P.m_blocks - b * P.band);
-        const int nb = w / width;
-        t.row0 = (int64_t(b) * P.band + (w - nb * width)) * S::BM;
+        const int b = P.d_band(idx), w = idx - b * int(P.d_band.d), r0 = b * P.band;
+        int nb, mt;
+        if (P.m_blocks - r0 >= P.band) {
+            nb = P.d_width(w);
+            mt = r0 + w - nb * P.band;
+        } else {
+            nb = P.d_tail(w);
+            mt = r0 + w - nb * int(P.d_tail.d);
+        }
+        t.row0 = int64_t(mt) * S::BM;
         t.n0 = nb * S::UNITS;
         t.limit = int(min(int64_t(S::BM), P.rows - t.row0));
         t.nvalid = t.limit;
@@ -327,7 +351,7 @@ __device__ __forceinline__ Tile tile_of(const TcTrain& P, const Tables& tb, int 
     }
     const int nt = tb.ts[lo + 1] - tb.ts[lo];
     const int l = idx - tb.ts[lo] * P.n_blocks;
-    const int nb = l / nt, mt = l - nb * nt;
+    const int nb = nt == 1 ? l : l / nt, mt = l - nb * nt;
     t.e = lo;
     t.row0 = tb.poff[lo] + int64_t(mt) * S::BM;
     t.n0 = nb * S::UNITS;
@@ -351,8 +375,12 @@ __device__ __forceinline__ void load4(void* dst, const CUtensorMap* m, uint64_t*
     else tma_4d(dst, m, bar, c0, c1, c2, c3, pol);
 }
 
-template <int KIND, int EPI, bool PAIR>
+// SPLIT: the CTAs of a cluster share one tile, each a part of its reduction; their accumulators
+// meet in shared memory, where each CTA adds up a part of the columns (in rank order) and runs
+// the epilogue on it. For problems of fewer tiles than SMs.
+template <int KIND, int EPI, bool PAIR, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_constant__ TcTrain P) {
+    static_assert(!(PAIR && SPLIT), "one or the other");
     using S = Shape<KIND, EPI, PAIR>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -367,8 +395,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t crank = PAIR ? cluster_rank() : 0u;
-    const int tile0 = PAIR ? int(blockIdx.x >> 1) : int(blockIdx.x);
-    const int tstep = PAIR ? int(gridDim.x >> 1) : int(gridDim.x);
+    const int srank = SPLIT ? int(cluster_rank()) : 0, splits = SPLIT ? P.splits : 1;
+    const int tile0 = PAIR ? int(blockIdx.x >> 1) : SPLIT ? int(blockIdx.x) / splits : int(blockIdx.x);
+    const int tstep = PAIR ? int(gridDim.x >> 1) : SPLIT ? 1 << 30 : int(gridDim.x);
+    // this CTA's reduction blocks of a tile
+    auto kb_begin = [&](const Tile& t) { return SPLIT ? t.nk * srank / splits : 0; };
+    auto kb_end = [&](const Tile& t) { return SPLIT ? t.nk * (srank + 1) / splits : t.nk; };
     if (warp == 0) {
         if constexpr (PAIR) {
             asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(tmem_slot)));
@@ -438,7 +470,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
             for (int idx = tile0; idx < total && !gave_up; idx += tstep) {
                 const Tile t = tile_of<KIND, EPI, PAIR>(P, tb, idx);
                 const int arow = int(t.row0) + 128 * int(crank);
-                for (int kb = 0; kb < t.nk; ++kb) {
+                const int kend = kb_end(t);
+                for (int kb = kb_begin(t); kb < kend; ++kb) {
                     if (!wait_bar(&empty[stage], phase ^ 1u)) {
                         gave_up = true;
                         break;
@@ -502,7 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
             uint32_t stage = 0, phase = 0, it = 0;
             for (int idx = tile0; idx < total && !gave_up; idx += tstep) {
                 const Tile t = tile_of<KIND, EPI, PAIR>(P, tb, idx);
-                if (t.nk == 0) continue;
+                const int kbeg = kb_begin(t), kend = kb_end(t);
+                if (kbeg == kend) continue;
                 const uint32_t ab = it & 1u, ph = (it >> 1) & 1u;
                 ++it;
                 if (!wait_bar(&acc_empty[ab], ph ^ 1u)) {
@@ -512,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                 fence_after();
                 const uint32_t d0 = tmem + ab * kCols;
                 constexpr uint32_t desc = idesc(S::AMN, S::BMN, S::BM, kCols);
-                for (int kb = 0; kb < t.nk; ++kb) {
+                for (int kb = kbeg; kb < kend; ++kb) {
                     if (!wait_bar(&full[stage], phase)) {
                         gave_up = true;
                         break;
@@ -522,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
 #pragma unroll
                     for (int k = 0; k < kBR / 16; ++k)
                         mma<PAIR>(d0, operand<S::AMN>(sa + k * kStep<S::AMN>), operand<S::BMN>(sb + k * kStep<S::BMN>),
-                                  desc, kb > 0 || k > 0 ? 1u : 0u);
+                                  desc, kb > kbeg || k > 0 ? 1u : 0u);
                     commit<PAIR>(&empty[stage]);
                     if (++stage == S::STAGES) {
                         stage = 0;
@@ -537,16 +571,58 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
             if (gave_up) set_status(P.status, MOE_ERR_DEVICE_TIMEOUT);
         }
         __syncwarp();
-    } else {
-        // ------------------------------------------------------------ epilogue
+    }
+    // ---------------------------------------------------------------- epilogue
+    if constexpr (SPLIT) {
+        // this CTA's part of the sums into shared memory (the ring: its products are done), 16
+        // bytes of four columns per row, rows adjacent
+        if (warp >= 2 && tile0 < total) {
+            const Tile t = tile_of<KIND, EPI, PAIR>(P, tb, tile0);
+            const bool any = kb_begin(t) < kb_end(t);
+            bool ok = true;
+            if (any) {
+                ok = wait_bar_sleep(&acc_full[0], 0);
+                if (!ok) set_status(P.status, MOE_ERR_DEVICE_TIMEOUT);
+                fence_after();
+            }
+            const int q = warp & 3, ch = (warp - 2) >> 2;
+#pragma unroll 1
+            for (int c = 4 * ch; ok && c < 4 * ch + 4; ++c) {
+                uint32_t r[32];
+                if (any) {
+                    tmem_load(tmem + (uint32_t(q * 32) << 16) + 32 * c, r);
+                    tmem_wait(r);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[j] = 0;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<uint4*>(smem + ((c * 8 + j) * 128 + q * 32 + lane) * 16) =
+                        make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+            }
+        }
+        __syncwarp();
+        cluster_sync();
+    }
+    if (warp >= 2) {
         const int q = warp & 3;                    // TMEM lane quarter of this warp
         const int ch = (warp - 2) >> 2;            // column half
         uint8_t* sm = stg + (warp - 2) * 2048;
         const int wrow = int(crank) * 128 + q * 32;  // first tile row of the warp
+        uint32_t it = 0;
+        // the warp's 32-column chunks of a tile (kGateUp: of its 128 units)
+        constexpr int kChunks = S::GATEUP ? 4 : 8;
+        int c0 = ch * (kChunks / 2), c1 = c0 + kChunks / 2;
+        if constexpr (SPLIT) {
+            const int n = kChunks / splits, half = (n + 1) / 2;
+            c0 = srank * n + ch * half;
+            c1 = min(c0 + half, (srank + 1) * n);
+        }
         // kDGated: pre-activations of the next 32 columns (gate, up), one chunk ahead
         uint4 x0[4], x1[4];
         auto fetch_pre = [&](const Tile& t, int c, int vrows) {
-            const int col = t.n0 + 128 * ch + 32 * c;
+            const int col = t.n0 + 32 * c;
             const int bytes = (P.N - col) * 2;
             const __nv_bfloat16* pr = P.pre + (t.pos0 + wrow) * P.ldp;
             if constexpr (S::IL) {
@@ -557,8 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                 fetch_rows(lane, x1, pr + P.N + col, P.ldp * 2, vrows, bytes);
             }
         };
-        uint32_t it = 0;
-        for (int idx = tile0; idx < total; idx += tstep) {
+        auto epilogue = [&](int idx) -> bool {
             const Tile t = tile_of<KIND, EPI, PAIR>(P, tb, idx);
             const int rows = min(32, t.limit - wrow);     // may be negative
             const int vrows = min(32, t.nvalid - wrow);
@@ -569,17 +644,44 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                 const int slot = P.row_slot[row + lane];
                 rs = slot < 0 ? 0.0f : P.row_scale[slot];
             }
-            if constexpr (S::DGATED) fetch_pre(t, 0, vrows);
-            if (t.nk > 0) {
+            if constexpr (S::DGATED)
+                if (c0 < c1) fetch_pre(t, c0, vrows);
+            if (!SPLIT && t.nk > 0) {
                 ++it;
                 if (!wait_bar_sleep(&acc_full[ab], ph)) {
                     set_status(P.status, MOE_ERR_DEVICE_TIMEOUT);
-                    break;
+                    return false;
                 }
                 fence_after();
             }
             const uint32_t tacc = tmem + (uint32_t(q * 32) << 16) + ab * kCols;
+            // accumulator columns 32 c .. 32 c + 31 of this lane's row
+            auto acc = [&](int c, uint32_t (&r)[32]) {
+                if constexpr (SPLIT) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[j] = 0;
+                    for (int p = 0; p < splits; ++p) {
+                        const uint32_t at = mapa_shared(smem + (c * 8 * 128 + q * 32 + lane) * 16, uint32_t(p));
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            float4 v;
+                            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                         : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                                         : "r"(at + j * 2048)
+                                         : "memory");
+                            r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) + v.x);
+                            r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) + v.y);
+                            r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) + v.z);
+                            r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) + v.w);
+                        }
+                    }
+                } else {
+                    tmem_load(tacc + 32 * c, r);
+                    tmem_wait(r);
+                }
+            };
             auto release = [&]() {  // this warp has read its part of the accumulators
+                if constexpr (SPLIT) return;
                 fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -588,17 +690,14 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                 }
             };
             if constexpr (S::GATEUP) {
-                // units n0 + 64 ch .. + 63: gate in columns 0..127, up in 128..255
+                // gate of the tile's 128 units in columns 0..127, up in 128..255
 #pragma unroll 1
-                for (int c = 0; c < 2; ++c) {
-                    const int cu = 64 * ch + 32 * c;
+                for (int c = c0; c < c1; ++c) {
                     uint32_t gr[32], vr[32];
-                    tmem_load(tacc + cu, gr);
-                    tmem_load(tacc + 128 + cu, vr);
-                    tmem_wait(gr);
-                    tmem_wait(vr);
-                    if (c == 1) release();
-                    const int u0 = t.n0 + cu;
+                    acc(c, gr);
+                    acc(4 + c, vr);
+                    if (c == c1 - 1) release();
+                    const int u0 = t.n0 + 32 * c;
                     if (u0 >= P.N || vrows <= 0) continue;
                     float g[32], v[32];
 #pragma unroll
@@ -654,8 +753,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                 float dw = 0.0f;
                 const bool valid = lane < vrows;
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    const int col = t.n0 + 128 * ch + 32 * c;
+                for (int c = c0; c < c1; ++c) {
+                    const int col = t.n0 + 32 * c;
                     const int bytes = (P.N - col) * 2;
                     turn_rows(sm, lane, x0);
                     turn_rows(sm, lane, x1);
@@ -663,11 +762,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                                              x0[2].x, x0[2].y, x0[2].z, x0[2].w, x0[3].x, x0[3].y, x0[3].z, x0[3].w};
                     const uint32_t a1[16] = {x1[0].x, x1[0].y, x1[0].z, x1[0].w, x1[1].x, x1[1].y, x1[1].z, x1[1].w,
                                              x1[2].x, x1[2].y, x1[2].z, x1[2].w, x1[3].x, x1[3].y, x1[3].z, x1[3].w};
-                    if (c < 3) fetch_pre(t, c + 1, vrows);
+                    if (c + 1 < c1) fetch_pre(t, c + 1, vrows);
                     uint32_t dr[32];
-                    tmem_load(tacc + 128 * ch + 32 * c, dr);
-                    tmem_wait(dr);
-                    if (c == 3) release();
+                    acc(c, dr);
+                    if (c == c1 - 1) release();
                     if (bytes <= 0 || rows <= 0) continue;
                     uint32_t o0[16], o1[16], oh[16];  // dg and dv (or alternating), w h
 #pragma unroll
@@ -719,8 +817,23 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                     }
                     put(oh, P.hw + row * P.N + col, int64_t(P.N) * 2, bytes);
                 }
-                if (P.partial && valid) P.partial[(row + lane) * P.parts + (t.n0 / kCols) * 2 + ch] = dw;
+                if (P.partial && valid) P.partial[(row + lane) * P.parts + ((t.n0 / kCols) * splits + srank) * 2 + ch] = dw;
             } else if constexpr (KIND == kTN) {
+                __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(t.half ? P.out1 : P.out) + t.e * P.so + row * P.ldo;
+                if constexpr (SPLIT) {
+#pragma unroll 1
+                    for (int c = c0; c < c1; ++c) {
+                        uint32_t dr[32];
+                        acc(c, dr);
+                        float f[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(dr[j]);
+                        uint4 w[4];
+                        pack_row(f, w);
+                        const int col = t.n0 + 32 * c;
+                        store_rows(sm, lane, w, ob + col, P.ldo * 2, rows, (P.N - col) * 2);
+                    }
+                } else {
                 // everything out of TMEM first: the next products need not wait for the stores
                 uint4 w[4][4];
 #pragma unroll
@@ -728,8 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                     float f[32];
                     if (t.nk > 0) {
                         uint32_t dr[32];
-                        tmem_load(tacc + 128 * ch + 32 * c, dr);
-                        tmem_wait(dr);
+                        acc(4 * ch + c, dr);
 #pragma unroll
                         for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(dr[j]);
                     } else {  // an expert without rows: its gradient is zero
@@ -739,22 +851,21 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                     pack_row(f, w[c]);
                 }
                 if (t.nk > 0) release();
-                if (rows <= 0) continue;
-                __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(t.half ? P.out1 : P.out) + t.e * P.so + row * P.ldo;
+                if (rows <= 0) return true;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int col = t.n0 + 128 * ch + 32 * c;
                     store_rows(sm, lane, w[c], ob + col, P.ldo * 2, rows, (P.N - col) * 2);
                 }
+                }
             } else {
                 char* ob = static_cast<char*>(P.out) + row * P.ldo * (P.out_f32 ? 4 : 2);
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    const int col = t.n0 + 128 * ch + 32 * c;
+                for (int c = c0; c < c1; ++c) {
+                    const int col = t.n0 + 32 * c;
                     uint32_t dr[32];
-                    tmem_load(tacc + 128 * ch + 32 * c, dr);
-                    tmem_wait(dr);
-                    if (c == 3) release();
+                    acc(c, dr);
+                    if (c == c1 - 1) release();
                     float f[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(dr[j]);
@@ -797,11 +908,19 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                     }
                 }
             }
+            return true;
+        };
+        if constexpr (SPLIT) {
+            if (tile0 < total) epilogue(tile0);
+        } else {
+            for (int idx = tile0; idx < total; idx += tstep)
+                if (!epilogue(idx)) break;
         }
+        __syncwarp();
     }
     fence_before();
     __syncthreads();
-    if constexpr (PAIR) cluster_sync();
+    if constexpr (PAIR || SPLIT) cluster_sync();  // no CTA leaves while another reads its shared memory
     if (warp == 0) {
         fence_after();
         if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
@@ -843,17 +962,35 @@ bool encode(CUtensorMap* m, const void* base, int rank, const int64_t* dims, con
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// SMs of a B200 (the library's only target), asked once.
 int sms() {
-    int dev = 0, n = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    static const int n = [] {
+        int dev = 0, v = 148;
+        if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
+        return v;
+    }();
     return n;
 }
 
-template <int KIND, int EPI, bool PAIR>
+// Allows a kernel its shared memory, once per device.
+template <typename K>
+cudaError_t allow_smem(K kern, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess) return err;
+    done.fetch_or(bit, std::memory_order_release);
+    return cudaSuccess;
+}
+
+template <int KIND, int EPI, bool PAIR, bool SPLIT>
 cudaError_t launch_t(const TcTrain& P, int64_t max_tiles, cudaStream_t s) {
     using S = Shape<KIND, EPI, PAIR>;
-    auto kern = tc_train_kernel<KIND, EPI, PAIR>;
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    auto kern = tc_train_kernel<KIND, EPI, PAIR, SPLIT>;
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t err = allow_smem(kern, S::SMEM, allowed);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
@@ -861,16 +998,25 @@ cudaError_t launch_t(const TcTrain& P, int64_t max_tiles, cudaStream_t s) {
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = PAIR ? 2 : 1;
+    attr[0].val.clusterDim.x = PAIR ? 2 : SPLIT ? P.splits : 1;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = PAIR ? 1 : 0;
+    cfg.numAttrs = PAIR || SPLIT ? 1 : 0;
+    if (SPLIT) {
+        cfg.gridDim = dim3(unsigned(max_tiles) * P.splits);
+        if ((err = cudaLaunchKernelEx(&cfg, kern, P)) != cudaSuccess) return err;
+        return cudaGetLastError();
+    }
     int most = sms();
     if (PAIR) {  // pairs that can be resident at once (an odd SM of a GPC stays out)
-        cfg.gridDim = dim3(2 * (most / 2));
-        int resident = 0;
-        if ((err = cudaOccupancyMaxActiveClusters(&resident, kern, &cfg)) != cudaSuccess) return err;
-        if (resident <= 0) return cudaErrorInvalidConfiguration;
+        static std::atomic<int> fits{0};
+        int resident = fits.load();
+        if (resident == 0) {
+            cfg.gridDim = dim3(2 * (most / 2));
+            if ((err = cudaOccupancyMaxActiveClusters(&resident, kern, &cfg)) != cudaSuccess) return err;
+            if (resident <= 0) return cudaErrorInvalidConfiguration;
+            fits.store(resident);
+        }
         most = std::min(resident, most / 2);
     }
     const int n = int(std::min<int64_t>(max_tiles, most));
@@ -878,6 +1024,13 @@ cudaError_t launch_t(const TcTrain& P, int64_t max_tiles, cudaStream_t s) {
     cfg.gridDim = dim3(PAIR ? 2 * n : n);
     if ((err = cudaLaunchKernelEx(&cfg, kern, P)) != cudaSuccess) return err;
     return cudaGetLastError();
+}
+
+// The three forms of a product: split, pairs, or one CTA per tile.
+template <int KIND, int EPI>
+cudaError_t launch(const TcTrain& P, bool pair, int64_t max_tiles, cudaStream_t s) {
+    if (P.splits > 1) return launch_t<KIND, EPI, false, true>(P, max_tiles, s);
+    return pair ? launch_t<KIND, EPI, true, false>(P, max_tiles, s) : launch_t<KIND, EPI, false, false>(P, max_tiles, s);
 }
 
 int64_t blocks_of(int64_t n, int64_t b) { return (n + b - 1) / b; }
@@ -893,6 +1046,7 @@ TcTrain base_of(const RowPlan& p) {
     P.rows = p.T;
     P.halves = 1;
     P.status = p.status;
+    P.splits = 1;
     return P;
 }
 
@@ -921,6 +1075,21 @@ bool use_pair(const RowPlan& p, int64_t rows, int64_t n_blocks) {
     return blocks_of(rows, 256) * n_blocks >= sms() / 2;
 }
 
+// CTAs per tile: as many (2, 4, 8; at most `most`, what the columns divide into) as the SMs
+// hold at once, each with two reduction blocks or more.
+int splits_of(int64_t tiles, int64_t nk, int most) {
+    int s = 1;
+    while (2 * s <= most && tiles * 2 * s <= sms() && nk >= 4 * s) s *= 2;
+    return s;
+}
+
+// Bands of P.band of `n` blocks, with `other` blocks of the other kind in turn in each.
+void set_bands(TcTrain& P, int n, int other) {
+    P.d_band = fast_div(int64_t(P.band) * other);
+    P.d_width = fast_div(P.band);
+    P.d_tail = fast_div(std::max(1, n % P.band));
+}
+
 // Row tiles at most, and the dense problem's bands (as many row tiles as, with every column
 // block, fill the GPU: the tiles running together share both operands in L2).
 int64_t row_grid(TcTrain& P, const RowPlan& p, bool pair) {
@@ -929,6 +1098,7 @@ int64_t row_grid(TcTrain& P, const RowPlan& p, bool pair) {
                                : blocks_of(p.T, BM));
     const int conc = pair ? sms() / 2 : sms();
     P.band = std::max(1, std::min(P.m_blocks, conc / std::max(1, P.n_blocks)));
+    set_bands(P, P.m_blocks, P.n_blocks);
     return int64_t(P.m_blocks) * P.n_blocks;
 }
 
@@ -952,12 +1122,17 @@ cudaError_t launch_tc_gemm_train(const GemmArgs& a, cudaStream_t s) {
         const int64_t tiles256 = blocks_of(P.mrows, 256) * P.halves * P.n_blocks * P.E;
         const bool pair = tiles256 >= sms() / 2;
         P.m_blocks = int(blocks_of(P.mrows, pair ? 256 : 128));
-        P.band = grouped ? 0 : std::max(1, std::min(P.n_blocks, (pair ? sms() / 2 : sms()) / (P.m_blocks * P.halves)));
+        // an expert's tiles: one column block at a time; dense: as many as fill the GPU with every row block
+        P.band = grouped ? 1 : std::max(1, std::min(P.n_blocks, (pair ? sms() / 2 : sms()) / (P.m_blocks * P.halves)));
+        set_bands(P, P.n_blocks, P.m_blocks * P.halves);
+        P.d_tile = fast_div(int64_t(P.m_blocks) * P.halves * P.n_blocks);
+        P.d_m = fast_div(P.m_blocks);
         if (!map_a(&P.a, a.a, rows, a.lda, P.mrows, P.halves, true) ||
             !map_b_n(&P.b0, a.b, 1, rows, a.N, a.ldb, rows * a.ldb))
             return cudaErrorInvalidValue;
         const int64_t tiles = int64_t(P.E) * P.m_blocks * P.halves * P.n_blocks;
-        return pair ? launch_t<kTN, kStore, true>(P, tiles, s) : launch_t<kTN, kStore, false>(P, tiles, s);
+        if (!pair && !grouped) P.splits = splits_of(tiles, blocks_of(a.R, kBR), 8);
+        return launch<kTN, kStore>(P, pair, tiles, s);
     }
     const bool pair = use_pair(a.plan, a.M, P.n_blocks);
     const int64_t rows = grouped ? a.plan.max_rows : a.M;
@@ -977,18 +1152,20 @@ cudaError_t launch_tc_gemm_train(const GemmArgs& a, cudaStream_t s) {
     const int64_t E = grouped ? a.plan.E : 1;
     if (a.kind == kNT) {
         P.nk = P.nk_half = int(blocks_of(a.R, kBR));
+        if (!pair) P.splits = splits_of(tiles, P.nk, 8);
         if (!map_a(&P.a, a.a, rows, a.lda, a.R, 1, false) || !map_b_k(&P.b0, a.b, E, a.N, 1, a.R)) return cudaErrorInvalidValue;
-        return pair ? launch_t<kNT, kStore, true>(P, tiles, s) : launch_t<kNT, kStore, false>(P, tiles, s);
+        return launch<kNT, kStore>(P, pair, tiles, s);
     }
     const int halves = a.split ? 2 : 1;
     const int64_t R = a.R / halves;
     P.nk_half = int(blocks_of(R, kBR));
     P.nk = P.nk_half * halves;
+    if (!pair) P.splits = splits_of(tiles, P.nk, 8);
     P.b_split = halves > 1;
     if (!map_a(&P.a, a.a, rows, a.lda, R, halves, false) || !map_b_n(&P.b0, a.b, E, R, a.N, a.ldb, R * a.ldb))
         return cudaErrorInvalidValue;
     if (halves > 1 && !map_b_n(&P.b1, a.b1, E, R, a.N, a.ldb, R * a.ldb)) return cudaErrorInvalidValue;
-    return pair ? launch_t<kNN, kStore, true>(P, tiles, s) : launch_t<kNN, kStore, false>(P, tiles, s);
+    return launch<kNN, kStore>(P, pair, tiles, s);
 }
 
 cudaError_t launch_tc_gateup(const GemmArgs& g, const GatedArgs& ga, cudaStream_t s) {
@@ -1000,6 +1177,7 @@ cudaError_t launch_tc_gateup(const GemmArgs& g, const GatedArgs& ga, cudaStream_
     const int64_t tiles = row_grid(P, g.plan, pair);
     const int64_t rows = grouped ? g.plan.max_rows : g.plan.T, E = grouped ? g.plan.E : 1;
     P.nk = P.nk_half = int(blocks_of(g.R, kBR));
+    if (!pair) P.splits = splits_of(tiles, P.nk, 4);
     P.bias0 = static_cast<const __nv_bfloat16*>(g.bias);
     P.bias1 = static_cast<const __nv_bfloat16*>(g.bias1);
     P.sbias = g.sbias;
@@ -1013,11 +1191,17 @@ cudaError_t launch_tc_gateup(const GemmArgs& g, const GatedArgs& ga, cudaStream_
     if (!map_a(&P.a, g.a, rows, g.lda, g.R, 1, false) || !map_b_k(&P.b0, g.b, E, ga.I, ga.interleaved ? 2 : 1, g.R))
         return cudaErrorInvalidValue;
     if (!ga.interleaved && !map_b_k(&P.b1, g.b1, E, ga.I, 1, g.R)) return cudaErrorInvalidValue;
-    if (ga.interleaved) return pair ? launch_t<kNT, kGateUpI, true>(P, tiles, s) : launch_t<kNT, kGateUpI, false>(P, tiles, s);
-    return pair ? launch_t<kNT, kGateUp, true>(P, tiles, s) : launch_t<kNT, kGateUp, false>(P, tiles, s);
+    if (ga.interleaved) return launch<kNT, kGateUpI>(P, pair, tiles, s);
+    return launch<kNT, kGateUp>(P, pair, tiles, s);
 }
 
-int dgated_parts(int I) { return 2 * int(blocks_of(I, kCols)); }
+int dgated_parts(const RowPlan& p, int I, int64_t R) {
+    TcTrain P = base_of(p);
+    P.n_blocks = int(blocks_of(I, kCols));
+    const bool pair = use_pair(p, p.T, P.n_blocks);
+    const int64_t tiles = row_grid(P, p, pair);
+    return 2 * P.n_blocks * (pair ? 1 : splits_of(tiles, blocks_of(R, kBR), 8));
+}
 
 cudaError_t launch_tc_dgated(const GemmArgs& g, const GatedArgs& ga, float* partial, cudaStream_t s) {
     TcTrain P = base_of(g.plan);
@@ -1028,6 +1212,7 @@ cudaError_t launch_tc_dgated(const GemmArgs& g, const GatedArgs& ga, float* part
     const int64_t tiles = row_grid(P, g.plan, pair);
     const int64_t rows = grouped ? g.plan.max_rows : g.plan.T, E = grouped ? g.plan.E : 1;
     P.nk = P.nk_half = int(blocks_of(g.R, kBR));
+    if (!pair) P.splits = splits_of(tiles, P.nk, 8);
     P.act = ga.act;
     P.limit = ga.limit;
     P.alpha = ga.alpha;
@@ -1037,11 +1222,11 @@ cudaError_t launch_tc_dgated(const GemmArgs& g, const GatedArgs& ga, float* part
     P.dgu = static_cast<__nv_bfloat16*>(ga.dgu);
     P.hw = static_cast<__nv_bfloat16*>(ga.hw);
     P.partial = partial;
-    P.parts = dgated_parts(ga.I);
+    P.parts = dgated_parts(g.plan, ga.I, g.R);
     if (!map_a(&P.a, g.a, rows, g.lda, g.R, 1, false) || !map_b_n(&P.b0, g.b, E, g.R, ga.I, g.ldb, g.sb))
         return cudaErrorInvalidValue;
-    if (ga.interleaved) return pair ? launch_t<kNN, kDGatedI, true>(P, tiles, s) : launch_t<kNN, kDGatedI, false>(P, tiles, s);
-    return pair ? launch_t<kNN, kDGated, true>(P, tiles, s) : launch_t<kNN, kDGated, false>(P, tiles, s);
+    if (ga.interleaved) return launch<kNN, kDGatedI>(P, pair, tiles, s);
+    return launch<kNN, kDGated>(P, pair, tiles, s);
 }
 
 }  // namespace moe
