@@ -183,8 +183,7 @@ FfnWs ffn_ws(const FfnShape& f, bool backward) {
         L.dgu = c.take(f.rows * 2 * f.I * f.es);
         L.hw = c.take(f.rows * f.I * f.es);
         if (f.bias)
-            L.partial = c.take(std::max(int64_t(colsum_splits(f.rows, f.E, 2 * f.I)) * f.E * 2 * f.I,
-                                        int64_t(colsum_splits(f.rows, f.E, f.K)) * f.E * f.K) * 4);
+            L.partial = c.take(round_rows(f.rows) / kRowTile * std::max(2 * int64_t(f.I), int64_t(f.K)) * 4);
     } else {
         if (f32) L.gp = c.take(f.rows * 2 * f.I * 4);
         L.h = c.take(f.rows * f.I * f.es);
@@ -247,6 +246,16 @@ moe_status moe_linear_forward(const moe_linear_desc* d, const void* x, int64_t l
     MOE_CHECK(stride(ldy, N, d->dtype));
     if (residual) MOE_CHECK(stride(ldr, N, d->dtype));
     MOE_CHECK(check_ws(ws, ws_bytes, linear_ws(d, T, false).total));
+    if (T <= kSmallT) {
+        SmallArgs a;
+        a.T = int(T); a.K = K; a.N = N; a.dtype = d->dtype; a.act = d->activation;
+        a.x = x; a.ldx = ldx; a.w = w; a.bias = bias;
+        a.residual = residual; a.ldr = ldr;
+        a.pre = pre;
+        a.y = y; a.ldy = ldy;
+        MOE_CUDA(launch_small(a, (cudaStream_t)stream));
+        return MOE_OK;
+    }
     GemmArgs g;
     g.plan.status = device_status;
     g.kind = kNT;
@@ -366,6 +375,30 @@ moe_status moe_ffn_forward(const moe_config* cfg, const moe_weights* w, const vo
     MOE_CHECK(check_ws(ws, ws_bytes, L.total));
     cudaStream_t s = (cudaStream_t)stream;
     const RowPlan p = row_plan(f, expert_offsets, sorted_slot, ws, L, device_status);
+    if (dense && T <= kSmallT) {
+        SmallArgs a;
+        a.T = int(T); a.K = f.K; a.N = f.I; a.dtype = f.dtype;
+        a.gated = true; a.interleaved = f.il; a.act = cfg->activation; a.limit = cfg->swiglu_limit;
+        a.alpha = cfg->swiglu_alpha;
+        a.x = u; a.ldx = ldu;
+        a.w = f.il ? w->gate_up_w : w->gate_w; a.w1 = w->up_w;
+        if (f.bias) {
+            a.bias = f.il ? w->gate_up_b : w->gate_b;
+            a.bias1 = w->up_b;
+        }
+        a.pre = pre;
+        a.y = at<void>(ws, L.h); a.ldy = f.I;
+        MOE_CUDA(launch_small(a, s));
+        SmallArgs o;
+        o.T = int(T); o.K = f.I; o.N = f.K; o.dtype = f.dtype;
+        o.x = a.y; o.ldx = f.I; o.w = w->down_w;
+        o.bias = f.bias ? w->down_b : nullptr;
+        o.residual = residual; o.ldr = ldr;
+        o.y = y; o.ldy = ldy;
+        o.wait_input = true;
+        MOE_CUDA(launch_small(o, s));
+        return MOE_OK;
+    }
     if (!dense) {
         GatherArgs ga;
         ga.plan = p;

@@ -14,14 +14,17 @@ template <> struct Vec<float> { static constexpr int N = 4; };
 template <> struct Vec<__nv_bfloat16> { static constexpr int N = 8; };
 
 template <typename T>
-__device__ __forceinline__ void load_vec(const T* p, float (&f)[Vec<T>::N]) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void unpack_vec(const uint4 v, float (&f)[Vec<T>::N]) {
     if constexpr (Vec<T>::N == 8) {
         unpack8(v, f);
     } else {
         f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
         f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
     }
+}
+template <typename T>
+__device__ __forceinline__ void load_vec(const T* p, float (&f)[Vec<T>::N]) {
+    unpack_vec<T>(*reinterpret_cast<const uint4*>(p), f);
 }
 template <typename T>
 __device__ __forceinline__ uint4 pack_vec(const float (&f)[Vec<T>::N]) {
@@ -52,12 +55,34 @@ __device__ __forceinline__ float logistic(float z) {
     else return 1.0f / (1.0f + expf(-z));
 }
 
+// Phi(z) and the normal density for results that are rounded to bf16 next: Phi(-|z|) =
+// erfc(|z| / sqrt 2) / 2 by Abramowitz and Stegun 7.1.26, t (a1 + ... + a5 t^4) e^(-z^2 / 2) with
+// t = 1 / (1 + p |z| / sqrt 2), absolute error below 1.5e-7; the exponential is the density's.
+// 23.8 -> 10 us against erfcf in the derivative pass of 4097 x 2048 (the erfcf made it
+// compute bound).
+__device__ __forceinline__ void normal_fast(float z, float& Phi, float& phi) {
+    const float e = __expf(-0.5f * z * z);
+    const float t = __fdividef(1.0f, fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.0f));
+    const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+                             0.254829592f);
+    const float tail = 0.5f * p * e;
+    Phi = z > 0.0f ? 1.0f - tail : tail;
+    phi = 0.39894228f * e;
+}
+
 // Activation of a linear layer and its derivative.
 template <bool FAST>
 __device__ __forceinline__ float linear_act(int act, float z) {
     if (act == MOE_LINEAR_SILU) return z * logistic<FAST>(z);
     // z Phi(z) with Phi(z) = erfc(-z / sqrt 2) / 2, which keeps its relative precision for z << 0
-    if (act == MOE_LINEAR_GELU) return z * 0.5f * erfcf(-z * 0.70710678f);
+    if (act == MOE_LINEAR_GELU) {
+        if constexpr (FAST) {
+            float Phi, phi;
+            normal_fast(z, Phi, phi);
+            return z * Phi;
+        }
+        return z * 0.5f * erfcf(-z * 0.70710678f);
+    }
     return z;
 }
 template <bool FAST>
@@ -67,8 +92,12 @@ __device__ __forceinline__ float linear_dact(int act, float z) {
         return p * (1.0f + z * (1.0f - p));
     }
     if (act == MOE_LINEAR_GELU) {
-        const float e = FAST ? __expf(-0.5f * z * z) : expf(-0.5f * z * z);
-        return 0.5f * erfcf(-z * 0.70710678f) + z * e * 0.39894228f;
+        if constexpr (FAST) {
+            float Phi, phi;
+            normal_fast(z, Phi, phi);
+            return Phi + z * phi;
+        }
+        return 0.5f * erfcf(-z * 0.70710678f) + z * expf(-0.5f * z * z) * 0.39894228f;
     }
     return 1.0f;
 }

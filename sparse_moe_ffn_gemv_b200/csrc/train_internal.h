@@ -94,6 +94,27 @@ struct GemmArgs {
 cudaError_t launch_simt_gemm(const GemmArgs& a, cudaStream_t s);     // f32
 cudaError_t launch_tc_gemm_train(const GemmArgs& a, cudaStream_t s);  // bf16, any kind
 
+// The forward products for at most kSmallT tokens, both types.
+constexpr int kSmallT = 8;
+struct SmallArgs {
+    int T = 0, K = 0, N = 0;  // N: outputs (gated: units)
+    int dtype = MOE_DTYPE_BF16;
+    bool gated = false;
+    int interleaved = 0, act = 0;  // act: enum moe_linear_activation, gated: enum moe_activation
+    float limit = 0.f, alpha = 0.f;
+    const void* x = nullptr; int64_t ldx = 0;
+    const void *w = nullptr, *w1 = nullptr;  // w1: the up plane
+    const void *bias = nullptr, *bias1 = nullptr;
+    const void* residual = nullptr; int64_t ldr = 0;
+    void* pre = nullptr;                     // [T, N] (gated: [T, 2N])
+    void* y = nullptr; int64_t ldy = 0;
+    // x is written by the launch just before (a launch of this kernel): this one may start
+    // early and waits for it
+    bool wait_input = false;
+    int ks = 1;  // set by the launcher
+};
+cudaError_t launch_small(const SmallArgs& a, cudaStream_t s);
+
 // ------------------------------------------------------------------ element-wise passes
 // The gated activation of every row and its derivative.
 struct GatedArgs {
@@ -134,10 +155,9 @@ struct ColsumArgs {
     const float* row_scale = nullptr;
     void* out = nullptr; int64_t so = 0;
     void* out1 = nullptr; int split = 0;  // columns from split on go to out1
-    float* partial = nullptr;             // [colsum_splits, E, cols]
+    float* partial = nullptr;             // [rows / kRowTile rounded up, cols]
     int dtype = MOE_DTYPE_BF16;
 };
-int colsum_splits(int64_t rows, int E, int cols);
 cudaError_t launch_colsum(const ColsumArgs& a, cudaStream_t s);
 
 // dz = dy * act'(pre), rounded to the activation dtype; partial column sums of the unrounded

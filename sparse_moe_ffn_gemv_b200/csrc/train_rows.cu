@@ -230,35 +230,47 @@ __global__ void __launch_bounds__(256) dtopk_kernel(const GatedArgs a, const flo
     }
 }
 
-// Column sums, first pass: block (x: 64 16-byte column vectors' worth, y: expert, z: split of
-// the expert's rows). Each thread owns one vector of columns and every 4th row of the split.
-constexpr int kColVecs = 64, kColRows = 4;
+// Column sums, first pass: a block sums kRowTile rows (which belong to one expert) of 64
+// 16-byte column vectors; each thread one vector and every 4th row, 8 rows' loads in flight.
+constexpr int kColVecs = 64, kColRows = 4, kColDeep = 8;
 template <typename T>
-__global__ void __launch_bounds__(kColVecs * kColRows) colsum_kernel(const ColsumArgs a, int splits) {
+__global__ void __launch_bounds__(kColVecs * kColRows) colsum_kernel(const ColsumArgs a) {
     constexpr int V = Vec<T>::N;
-    const int e = blockIdx.y, z = blockIdx.z;
-    int64_t r0 = 0, r1 = a.plan.T;
-    if (a.plan.offsets) {
-        r0 = a.plan.poff[e];
-        r1 = r0 + (a.plan.uoff[e + 1] - a.plan.uoff[e]);
+    const RowPlan& p = a.plan;
+    const int64_t b = int64_t(blockIdx.x) * kRowTile;
+    int64_t end = p.T;
+    if (p.offsets) {
+        if (b >= p.poff[p.E]) return;
+        const int e = expert_of_row(p.poff, p.E, int(b));
+        end = p.poff[e] + (p.uoff[e + 1] - p.uoff[e]);
     }
-    const int64_t per = (r1 - r0 + splits - 1) / splits;
-    const int64_t b = r0 + z * per, end = min(r1, b + per);
-    const int c = (blockIdx.x * kColVecs + threadIdx.x % kColVecs) * V;
+    end = min(end, b + kRowTile);
+    const int c = (blockIdx.y * kColVecs + threadIdx.x % kColVecs) * V;
     const int ry = threadIdx.x / kColVecs;
     float acc[V] = {};
     if (c < a.cols) {
-        for (int64_t r = b + ry; r < end; r += kColRows) {
-            float f[V];
-            load_vec(static_cast<const T*>(a.x) + r * a.ldx + c, f);
-            float sc = 1.0f;
-            if (a.row_scale) {
-                const int slot = a.plan.row_slot[r];
-                if (slot < 0) continue;
-                sc = a.row_scale[slot];
+        for (int64_t r = b + ry; r < end; r += kColDeep * kColRows) {
+            uint4 f[kColDeep];
+            float sc[kColDeep];
+#pragma unroll
+            for (int u = 0; u < kColDeep; ++u) {
+                const int64_t ru = r + u * kColRows;
+                f[u] = make_uint4(0, 0, 0, 0);
+                sc[u] = 1.0f;
+                if (ru >= end) continue;
+                f[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + ru * a.ldx + c);
+                if (a.row_scale) {
+                    const int slot = p.row_slot[ru];
+                    sc[u] = slot < 0 ? 0.0f : a.row_scale[slot];
+                }
             }
 #pragma unroll
-            for (int q = 0; q < V; ++q) acc[q] += f[q] * sc;
+            for (int u = 0; u < kColDeep; ++u) {
+                float v[V];
+                unpack_vec<T>(f[u], v);
+#pragma unroll
+                for (int q = 0; q < V; ++q) acc[q] = fmaf(v[q], sc[u], acc[q]);
+            }
         }
     }
     __shared__ float sm[kColRows][kColVecs][V + 1];
@@ -266,7 +278,7 @@ __global__ void __launch_bounds__(kColVecs * kColRows) colsum_kernel(const Colsu
     for (int q = 0; q < V; ++q) sm[ry][threadIdx.x % kColVecs][q] = acc[q];
     __syncthreads();
     if (ry == 0 && c < a.cols) {
-        float* o = a.partial + (int64_t(z) * a.plan.E + e) * a.cols + c;
+        float* o = a.partial + int64_t(blockIdx.x) * a.cols + c;
 #pragma unroll
         for (int q = 0; q < V; ++q) {
             float s = 0.f;
@@ -277,19 +289,33 @@ __global__ void __launch_bounds__(kColVecs * kColRows) colsum_kernel(const Colsu
     }
 }
 
-// Second pass: the splits' partial sums added in order and rounded once.
+// Second pass, 32 columns of one expert per block: 8 threads per column each add every 8th
+// partial row of the expert, then those 8 in order; rounded once. Without a plan (dense): the
+// `parts` rows of one matrix.
 template <typename T>
-__global__ void __launch_bounds__(256) colsum_finish_kernel(const ColsumArgs a, int splits) {
-    const int64_t n = int64_t(a.plan.E) * a.cols;
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
-        float s = 0.f;
-        for (int z = 0; z < splits; ++z) s += a.partial[z * n + i];
-        const int64_t e = i / a.cols;
-        const int c = int(i - e * a.cols);
-        T* o = a.split && c >= a.split ? static_cast<T*>(a.out1) + e * a.so + (c - a.split)
-                                       : static_cast<T*>(a.out) + e * a.so + c;
-        *o = from_f<T>(s);
+__global__ void __launch_bounds__(256) colsum_finish_kernel(const ColsumArgs a, int parts) {
+    __shared__ float sm[8][33];
+    const int e = blockIdx.y;
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + x;
+    int64_t p0 = 0, p1 = parts;
+    if (a.plan.offsets) {
+        p0 = a.plan.poff[e] / kRowTile;
+        p1 = a.plan.poff[e + 1] / kRowTile;
     }
+    float s = 0.f;
+    if (c < a.cols)
+#pragma unroll 4
+        for (int64_t z = p0 + y; z < p1; z += 8) s += a.partial[z * a.cols + c];
+    sm[y][x] = s;
+    __syncthreads();
+    if (y != 0 || c >= a.cols) return;
+    s = sm[0][x];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) s += sm[j][x];
+    T* o = a.split && c >= a.split ? static_cast<T*>(a.out1) + e * a.so + (c - a.split)
+                                   : static_cast<T*>(a.out) + e * a.so + c;
+    *o = from_f<T>(s);
 }
 
 template <typename T>
@@ -302,18 +328,32 @@ __global__ void __launch_bounds__(kColVecs * kColRows) dact_kernel(const DactArg
     const int ry = threadIdx.x / kColVecs;
     float acc[V] = {};
     if (c < a.N) {
-        for (int64_t r = b + ry; r < end; r += kColRows) {
-            float f[V];
-            load_vec(static_cast<const T*>(a.dy) + r * a.lddy + c, f);
-            if (a.act != MOE_LINEAR_NONE) {
-                float z[V];
-                load_vec(static_cast<const T*>(a.pre) + r * a.N + c, z);
+        for (int64_t r = b + ry; r < end; r += 4 * kColRows) {
+            uint4 dv[4], zv[4];
 #pragma unroll
-                for (int q = 0; q < V; ++q) f[q] *= linear_dact<FAST>(a.act, z[q]);
-                store_vec(static_cast<T*>(a.dz) + r * a.N + c, f);
+            for (int u = 0; u < 4; ++u) {
+                const int64_t ru = r + u * kColRows;
+                dv[u] = zv[u] = make_uint4(0, 0, 0, 0);
+                if (ru >= end) continue;
+                dv[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.dy) + ru * a.lddy + c);
+                if (a.act != MOE_LINEAR_NONE)
+                    zv[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.pre) + ru * a.N + c);
             }
 #pragma unroll
-            for (int q = 0; q < V; ++q) acc[q] += f[q];
+            for (int u = 0; u < 4; ++u) {
+                const int64_t ru = r + u * kColRows;
+                float f[V];
+                unpack_vec<T>(dv[u], f);
+                if (a.act != MOE_LINEAR_NONE && ru < end) {
+                    float z[V];
+                    unpack_vec<T>(zv[u], z);
+#pragma unroll
+                    for (int q = 0; q < V; ++q) f[q] *= linear_dact<FAST>(a.act, z[q]);
+                    store_vec(static_cast<T*>(a.dz) + ru * a.N + c, f);
+                }
+#pragma unroll
+                for (int q = 0; q < V; ++q) acc[q] += f[q];
+            }
         }
     }
     if (!a.partial) return;
@@ -370,24 +410,17 @@ cudaError_t launch_dtopk(const GatedArgs& a, const float* partial, int parts, cu
     return cudaGetLastError();
 }
 
-// Enough blocks to fill the GPU, at least 64 rows each.
-int colsum_splits(int64_t rows, int E, int cols) {
-    const int64_t cb = (cols + 511) / 512;
-    const int64_t want = std::max<int64_t>(1, 592 / (cb * E));
-    return int(std::max<int64_t>(1, std::min<int64_t>(want, rows / E / 64)));
-}
-
 cudaError_t launch_colsum(const ColsumArgs& a, cudaStream_t s) {
     const int V = a.dtype == MOE_DTYPE_F32 ? 4 : 8;
-    const int splits = colsum_splits(a.plan.max_rows, a.plan.E, a.cols);
-    const dim3 grid((a.cols / V + kColVecs - 1) / kColVecs, a.plan.E, splits);
-    const unsigned fin = grid_for(int64_t(a.plan.E) * a.cols, 256, 148 * 8);
+    const int64_t tiles = (a.plan.max_rows + kRowTile - 1) / kRowTile;
+    const dim3 grid(unsigned(tiles), (a.cols / V + kColVecs - 1) / kColVecs);
+    const dim3 fin((a.cols + 31) / 32, a.plan.E);
     if (a.dtype == MOE_DTYPE_F32) {
-        colsum_kernel<float><<<grid, kColVecs * kColRows, 0, s>>>(a, splits);
-        colsum_finish_kernel<float><<<fin, 256, 0, s>>>(a, splits);
+        colsum_kernel<float><<<grid, kColVecs * kColRows, 0, s>>>(a);
+        colsum_finish_kernel<float><<<fin, 256, 0, s>>>(a, int(tiles));
     } else {
-        colsum_kernel<__nv_bfloat16><<<grid, kColVecs * kColRows, 0, s>>>(a, splits);
-        colsum_finish_kernel<__nv_bfloat16><<<fin, 256, 0, s>>>(a, splits);
+        colsum_kernel<__nv_bfloat16><<<grid, kColVecs * kColRows, 0, s>>>(a);
+        colsum_finish_kernel<__nv_bfloat16><<<fin, 256, 0, s>>>(a, int(tiles));
     }
     return cudaGetLastError();
 }
@@ -408,7 +441,7 @@ cudaError_t launch_dact(const DactArgs& a, cudaStream_t s) {
         c.cols = a.N;
         c.out = a.db;
         c.partial = a.partial;
-        const unsigned fin = grid_for(a.N, 256, 148 * 8);
+        const unsigned fin = (a.N + 31) / 32;
         if (a.dtype == MOE_DTYPE_F32) colsum_finish_kernel<float><<<fin, 256, 0, s>>>(c, splits);
         else colsum_finish_kernel<__nv_bfloat16><<<fin, 256, 0, s>>>(c, splits);
     }

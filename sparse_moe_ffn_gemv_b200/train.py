@@ -80,7 +80,10 @@ def _p(t: Optional[torch.Tensor]):
 
 
 class _Operator:
-    """What the handles share: device, dtype, status word, checks, workspace, stream."""
+    """What the handles share: device, dtype, status word, checks, workspace, stream.
+
+    A call of a few microseconds on the GPU is soon bound by its Python side, so the checks
+    below read each tensor attribute once and the handle keeps what does not change."""
 
     def __init__(self, dtype: str, device):
         if dtype not in _DTYPE:
@@ -91,58 +94,62 @@ class _Operator:
             raise ValueError(f"device {device!r}: the operators run on CUDA devices")
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
+        self._index = self.device.index
         self.lib = lib()
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._status_p = self.status.data_ptr()
         self._ws_bytes: Dict[Tuple[int, int], int] = {}
 
     def device_status(self) -> int:
         """The status device-side checks left since the last call (0: none). Synchronises."""
+        torch.cuda.synchronize(self.device)
         v = int(self.status.item())
         self.status.zero_()
         return v
+
+    def _elsewhere(self, stream) -> bool:
+        """Whether the call names a stream, or another device is current."""
+        return stream is not None or torch.cuda.current_device() != self._index
 
     @contextlib.contextmanager
     def _on(self, stream):
         """The handle's device and the call's stream made current: what is allocated in the
         call belongs to the stream that uses it."""
         if stream is not None:
+            if stream.device != self.device:
+                raise ValueError(f"stream of {stream.device}, handle of {self.device}")
             with torch.cuda.stream(stream):
                 yield
         else:
             with torch.cuda.device(self.device):
                 yield
 
-    def _guard(self, stream):
-        if stream is None and torch.cuda.current_device() == self.device.index:
-            return contextlib.nullcontext()
-        if stream is not None and stream.device != self.device:
-            raise ValueError(f"stream of {stream.device}, handle of {self.device}")
-        return self._on(stream)
-
     def _flat(self, name: str, t: torch.Tensor, numel: int, dtype=None) -> int:
         """A contiguous tensor of a given size: its address."""
-        if t.dtype != (dtype or self.dtype) or t.device != self.device:
-            raise ValueError(f"{name}: {t.dtype} on {t.device}, wanted {dtype or self.dtype} on {self.device}")
+        dtype = dtype or self.dtype
+        if t.dtype is not dtype or t.get_device() != self._index:
+            raise ValueError(f"{name}: {t.dtype} on {t.device}, wanted {dtype} on {self.device}")
         if t.numel() != numel or not t.is_contiguous():
             raise ValueError(f"{name}: shape {tuple(t.shape)}, strides {t.stride()}; wanted {numel} contiguous values")
         return t.data_ptr()
 
     def _rows(self, name: str, t: torch.Tensor, width: int, rows: Optional[int] = None) -> Tuple[int, int]:
         """A [rows, width] tensor with unit column stride: its address and row stride."""
-        if t.dtype != self.dtype or t.device != self.device:
+        if t.dtype is not self.dtype or t.get_device() != self._index:
             raise ValueError(f"{name}: {t.dtype} on {t.device}, wanted {self.dtype} on {self.device}")
-        if t.dim() != 2 or t.shape[1] != width or (rows is not None and t.shape[0] != rows):
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted [{'rows' if rows is None else rows}, {width}]")
-        n, st = t.shape[0], t.stride()
-        if n and width > 1 and st[1] != 1:
-            raise ValueError(f"{name}: strides {st}: the columns of a row must be contiguous")
-        return t.data_ptr(), st[0] if n > 1 else width
+        shape = t.shape
+        if len(shape) != 2 or shape[1] != width or (rows is not None and shape[0] != rows):
+            raise ValueError(f"{name}: shape {tuple(shape)}, wanted [{'rows' if rows is None else rows}, {width}]")
+        n, (ld, unit) = shape[0], t.stride()
+        if n and width > 1 and unit != 1:
+            raise ValueError(f"{name}: strides {(ld, unit)}: the columns of a row must be contiguous")
+        return t.data_ptr(), ld if n > 1 else width
 
-    def _workspace(self, size_fn, desc, T: int, backward: int):
+    def _workspace(self, size_fn, desc_ref, T: int, backward: int):
         n = self._ws_bytes.get((T, backward))
         if n is None:
             out = ctypes.c_size_t(0)
-            M._check(size_fn(ctypes.byref(desc), T, backward, ctypes.byref(out)), size_fn.__name__)
+            M._check(size_fn(desc_ref, T, backward, ctypes.byref(out)), size_fn.__name__)
             if len(self._ws_bytes) >= 1024:
                 self._ws_bytes.clear()
             n = self._ws_bytes[(T, backward)] = out.value
@@ -152,7 +159,7 @@ class _Operator:
         return torch.empty(shape, dtype=dtype or self.dtype, device=self.device)
 
     def _stream(self):
-        return torch.cuda.current_stream(self.device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self._index)
 
 
 class Linear(_Operator):
@@ -165,41 +172,46 @@ class Linear(_Operator):
         super().__init__(dtype, device)
         self.n_in, self.n_out, self.activation = in_features, out_features, activation
         self.desc = MoeLinearDesc(in_features, out_features, LINEAR_ACTIVATION[activation], inputs.DTYPE[dtype])
-        self._workspace(self.lib.moe_linear_workspace_size, self.desc, 0, 0)  # checks the shape
+        self._desc = ctypes.byref(self.desc)
+        self._workspace(self.lib.moe_linear_workspace_size, self._desc, 0, 0)  # checks the shape
 
     def forward(self, x, w, bias=None, residual=None, keep: bool = False, out=None, stream=None):
         """y, or (y, pre) with keep: pre = x W^T + b is what backward needs of an activation."""
-        with self._guard(stream):
-            T, K, N = x.shape[0], self.n_in, self.n_out
-            xp, ldx = self._rows("x", x, K)
-            wp = self._flat("w", w, N * K)
-            bp = None if bias is None else self._flat("bias", bias, N)
-            rp, ldr = (None, 0) if residual is None else self._rows("residual", residual, N, T)
-            y = self._empty(T, N) if out is None else out
-            yp, ldy = self._rows("out", y, N, T)
-            pre = self._empty(T, N) if keep else None
-            ws, n = self._workspace(self.lib.moe_linear_workspace_size, self.desc, T, 0)
-            M._check(self.lib.moe_linear_forward(ctypes.byref(self.desc), xp, ldx, wp, bp, rp, ldr, T, yp, ldy,
-                                                 _p(pre), _p(ws), n, self.status.data_ptr(), self._stream()),
-                     "moe_linear_forward")
+        if self._elsewhere(stream):
+            with self._on(stream):
+                return self.forward(x, w, bias, residual, keep, out)
+        T, K, N = x.shape[0], self.n_in, self.n_out
+        xp, ldx = self._rows("x", x, K)
+        wp = self._flat("w", w, N * K)
+        bp = None if bias is None else self._flat("bias", bias, N)
+        rp, ldr = (None, 0) if residual is None else self._rows("residual", residual, N, T)
+        y = self._empty(T, N) if out is None else out
+        yp, ldy = self._rows("out", y, N, T)
+        pre = self._empty(T, N) if keep else None
+        ws, n = self._workspace(self.lib.moe_linear_workspace_size, self._desc, T, 0)
+        M._check(self.lib.moe_linear_forward(self._desc, xp, ldx, wp, bp, rp, ldr, T, yp, ldy,
+                                             _p(pre), _p(ws), n, self._status_p, self._stream()),
+                 "moe_linear_forward")
         return (y, pre) if keep else y
 
     def backward(self, dy, x, w, pre=None, bias_grad: bool = True, input_grad: bool = True,
                  weight_grad: bool = True, stream=None):
         """(dx, dw, db); None for a gradient not asked for. A residual's gradient is dy."""
-        with self._guard(stream):
-            T, K, N = x.shape[0], self.n_in, self.n_out
-            gp, ldg = self._rows("dy", dy, N, T)
-            xp, ldx = self._rows("x", x, K)
-            wp = self._flat("w", w, N * K)
-            pp = None if pre is None else self._flat("pre", pre, T * N)
-            dx = self._empty(T, K) if input_grad else None
-            dw = self._empty(N, K) if weight_grad else None
-            db = self._empty(N) if bias_grad else None
-            ws, n = self._workspace(self.lib.moe_linear_workspace_size, self.desc, T, 1)
-            M._check(self.lib.moe_linear_backward(ctypes.byref(self.desc), gp, ldg, xp, ldx, wp, pp, T, _p(dx), K,
-                                                  _p(dw), _p(db), _p(ws), n, self.status.data_ptr(),
-                                                  self._stream()), "moe_linear_backward")
+        if self._elsewhere(stream):
+            with self._on(stream):
+                return self.backward(dy, x, w, pre, bias_grad, input_grad, weight_grad)
+        T, K, N = x.shape[0], self.n_in, self.n_out
+        gp, ldg = self._rows("dy", dy, N, T)
+        xp, ldx = self._rows("x", x, K)
+        wp = self._flat("w", w, N * K)
+        pp = None if pre is None else self._flat("pre", pre, T * N)
+        dx = self._empty(T, K) if input_grad else None
+        dw = self._empty(N, K) if weight_grad else None
+        db = self._empty(N) if bias_grad else None
+        ws, n = self._workspace(self.lib.moe_linear_workspace_size, self._desc, T, 1)
+        M._check(self.lib.moe_linear_backward(self._desc, gp, ldg, xp, ldx, wp, pp, T, _p(dx), K,
+                                              _p(dw), _p(db), _p(ws), n, self._status_p,
+                                              self._stream()), "moe_linear_backward")
         return dx, dw, db
 
 
@@ -215,10 +227,11 @@ class GatedFfn(_Operator):
         super().__init__(spec.act_dtype, device)
         self.spec = spec
         self.cfg = M.config_from_spec(spec)
+        self._cfg = ctypes.byref(self.cfg)
         M._check(M.moe_config_validate(self.cfg), "moe_config_validate")
         E, I, K = spec.num_experts, spec.intermediate, spec.expert_in
         self.E, self.k, self.I, self.K = E, spec.top_k, I, K
-        self._workspace(self.lib.moe_ffn_workspace_size, self.cfg, 0, 0)  # checks the weight format
+        self._workspace(self.lib.moe_ffn_workspace_size, self._cfg, 0, 0)  # checks the weight format
         shapes = {"gate_up_w": (E, 2 * I, K)} if spec.gate_up_interleaved else {"gate_w": (E, I, K), "up_w": (E, I, K)}
         shapes["down_w"] = (E, K, I)
         if spec.has_expert_bias:
@@ -249,41 +262,45 @@ class GatedFfn(_Operator):
                 out=None, stream=None):
         """(y, pre): y [T, K], and the pre-activations [T*k, 2I] in sorted order that backward
         takes (None without keep)."""
-        with self._guard(stream):
-            T = u.shape[0]
-            up, ldu = self._rows("u", u, self.K)
-            w = self._planes(M.MoeWeights(), weights, "weights")
-            off, slots, wts = self._routing(routing, T)
-            rp, ldr = (None, 0) if residual is None else self._rows("residual", residual, self.K, T)
-            y = self._empty(T, self.K) if out is None else out
-            yp, ldy = self._rows("out", y, self.K, T)
-            pre = self._empty(T * self.k, 2 * self.I) if keep else None
-            ws, n = self._workspace(self.lib.moe_ffn_workspace_size, self.cfg, T, 0)
-            M._check(self.lib.moe_ffn_forward(ctypes.byref(self.cfg), ctypes.byref(w), up, ldu, T, off, slots, wts, rp,
-                                              ldr, yp, ldy, _p(pre), _p(ws), n, self.status.data_ptr(),
-                                              self._stream()), "moe_ffn_forward")
+        if self._elsewhere(stream):
+            with self._on(stream):
+                return self.forward(u, weights, routing, residual, keep, out)
+        T = u.shape[0]
+        up, ldu = self._rows("u", u, self.K)
+        w = self._planes(M.MoeWeights(), weights, "weights")
+        off, slots, wts = self._routing(routing, T)
+        rp, ldr = (None, 0) if residual is None else self._rows("residual", residual, self.K, T)
+        y = self._empty(T, self.K) if out is None else out
+        yp, ldy = self._rows("out", y, self.K, T)
+        pre = self._empty(T * self.k, 2 * self.I) if keep else None
+        ws, n = self._workspace(self.lib.moe_ffn_workspace_size, self._cfg, T, 0)
+        M._check(self.lib.moe_ffn_forward(self._cfg, ctypes.byref(w), up, ldu, T, off, slots, wts, rp,
+                                          ldr, yp, ldy, _p(pre), _p(ws), n, self._status_p,
+                                          self._stream()), "moe_ffn_forward")
         return y, pre
 
     def backward(self, dy, u, weights: Dict[str, torch.Tensor], pre, routing=None, input_grad: bool = True,
                  stream=None) -> Dict[str, torch.Tensor]:
         """Gradients by name: "x" (of u), "topk_w" (routed), and those of the weight planes."""
-        with self._guard(stream):
-            T = u.shape[0]
-            gp, ldg = self._rows("dy", dy, self.K, T)
-            up, ldu = self._rows("u", u, self.K)
-            w = self._planes(M.MoeWeights(), weights, "weights")
-            off, slots, wts = self._routing(routing, T)
-            pp = self._flat("pre", pre, T * self.k * 2 * self.I)
-            grads = {f: self._empty(*s) for f, s in self.shapes.items()}
-            g = MoeFfnGrads()
-            for f, t in grads.items():
-                setattr(g, f, t.data_ptr())
-            dwt = None if off is None else self._empty(T, self.k, dtype=torch.float32)
-            du = self._empty(T, self.K) if input_grad else None
-            ws, n = self._workspace(self.lib.moe_ffn_workspace_size, self.cfg, T, 1)
-            M._check(self.lib.moe_ffn_backward(ctypes.byref(self.cfg), ctypes.byref(w), up, ldu, T, off, slots, wts, pp,
-                                               gp, ldg, _p(du), self.K, _p(dwt), ctypes.byref(g), _p(ws), n,
-                                               self.status.data_ptr(), self._stream()), "moe_ffn_backward")
+        if self._elsewhere(stream):
+            with self._on(stream):
+                return self.backward(dy, u, weights, pre, routing, input_grad)
+        T = u.shape[0]
+        gp, ldg = self._rows("dy", dy, self.K, T)
+        up, ldu = self._rows("u", u, self.K)
+        w = self._planes(M.MoeWeights(), weights, "weights")
+        off, slots, wts = self._routing(routing, T)
+        pp = self._flat("pre", pre, T * self.k * 2 * self.I)
+        grads = {f: self._empty(*s) for f, s in self.shapes.items()}
+        g = MoeFfnGrads()
+        for f, t in grads.items():
+            setattr(g, f, t.data_ptr())
+        dwt = None if off is None else self._empty(T, self.k, dtype=torch.float32)
+        du = self._empty(T, self.K) if input_grad else None
+        ws, n = self._workspace(self.lib.moe_ffn_workspace_size, self._cfg, T, 1)
+        M._check(self.lib.moe_ffn_backward(self._cfg, ctypes.byref(w), up, ldu, T, off, slots, wts, pp,
+                                           gp, ldg, _p(du), self.K, _p(dwt), ctypes.byref(g), _p(ws), n,
+                                           self._status_p, self._stream()), "moe_ffn_backward")
         if du is not None:
             grads["x"] = du
         if dwt is not None:
@@ -300,39 +317,44 @@ class Norm(_Operator):
         super().__init__(dtype, device)
         self.width, self.kind = width, kind
         self.desc = MoeNormDesc(width, NORM_KIND[kind], inputs.DTYPE[dtype], eps)
-        self._workspace(self.lib.moe_norm_workspace_size, self.desc, 0, 0)  # checks the shape
+        self._desc = ctypes.byref(self.desc)
+        self._workspace(self.lib.moe_norm_workspace_size, self._desc, 0, 0)  # checks the shape
 
     def forward(self, x, w, bias=None, out=None, stream=None):
         """(y, stats): stats [T, 2] f32 (mean, 1 / sqrt(var + eps)) is what backward takes."""
-        with self._guard(stream):
-            T, H = x.shape[0], self.width
-            xp, ldx = self._rows("x", x, H)
-            wp = self._flat("w", w, H)
-            bp = None if bias is None else self._flat("bias", bias, H)
-            y = self._empty(T, H) if out is None else out
-            yp, ldy = self._rows("out", y, H, T)
-            stats = self._empty(T, 2, dtype=torch.float32)
-            M._check(self.lib.moe_norm_forward(ctypes.byref(self.desc), xp, ldx, wp, bp, T, yp, ldy, stats.data_ptr(),
-                                               self._stream()), "moe_norm_forward")
+        if self._elsewhere(stream):
+            with self._on(stream):
+                return self.forward(x, w, bias, out)
+        T, H = x.shape[0], self.width
+        xp, ldx = self._rows("x", x, H)
+        wp = self._flat("w", w, H)
+        bp = None if bias is None else self._flat("bias", bias, H)
+        y = self._empty(T, H) if out is None else out
+        yp, ldy = self._rows("out", y, H, T)
+        stats = self._empty(T, 2, dtype=torch.float32)
+        M._check(self.lib.moe_norm_forward(self._desc, xp, ldx, wp, bp, T, yp, ldy, stats.data_ptr(),
+                                           self._stream()), "moe_norm_forward")
         return y, stats
 
     def backward(self, dy, x, w, stats, bias_grad: Optional[bool] = None, input_grad: bool = True,
                  stream=None):
         """(dx, dw, db); db is None for RMS norm or with bias_grad False."""
-        with self._guard(stream):
-            T, H = x.shape[0], self.width
-            if bias_grad and self.kind == "rms":
-                raise ValueError("RMS norm has no bias")
-            if bias_grad is None:
-                bias_grad = self.kind == "layer"
-            gp, ldg = self._rows("dy", dy, H, T)
-            xp, ldx = self._rows("x", x, H)
-            wp = self._flat("w", w, H)
-            sp = self._flat("stats", stats, 2 * T, torch.float32)
-            dx = self._empty(T, H) if input_grad else None
-            dw = self._empty(H)
-            db = self._empty(H) if bias_grad else None
-            ws, n = self._workspace(self.lib.moe_norm_workspace_size, self.desc, T, 1)
-            M._check(self.lib.moe_norm_backward(ctypes.byref(self.desc), gp, ldg, xp, ldx, wp, sp, T, _p(dx), H,
-                                                _p(dw), _p(db), _p(ws), n, self._stream()), "moe_norm_backward")
+        if self._elsewhere(stream):
+            with self._on(stream):
+                return self.backward(dy, x, w, stats, bias_grad, input_grad)
+        T, H = x.shape[0], self.width
+        if bias_grad and self.kind == "rms":
+            raise ValueError("RMS norm has no bias")
+        if bias_grad is None:
+            bias_grad = self.kind == "layer"
+        gp, ldg = self._rows("dy", dy, H, T)
+        xp, ldx = self._rows("x", x, H)
+        wp = self._flat("w", w, H)
+        sp = self._flat("stats", stats, 2 * T, torch.float32)
+        dx = self._empty(T, H) if input_grad else None
+        dw = self._empty(H)
+        db = self._empty(H) if bias_grad else None
+        ws, n = self._workspace(self.lib.moe_norm_workspace_size, self._desc, T, 1)
+        M._check(self.lib.moe_norm_backward(self._desc, gp, ldg, xp, ldx, wp, sp, T, _p(dx), H,
+                                            _p(dw), _p(db), _p(ws), n, self._stream()), "moe_norm_backward")
         return dx, dw, db
