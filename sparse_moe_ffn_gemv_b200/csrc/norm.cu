@@ -6,7 +6,9 @@
 // Statistics and sums in f32; the variance is taken about the mean in a second pass over the
 // row, not as a difference of two large sums.
 #include <algorithm>
+#include <atomic>
 
+#include "ptx.cuh"
 #include "train_dev.cuh"
 
 namespace moe {
@@ -26,6 +28,80 @@ __device__ __forceinline__ float block_sum(float v, float* sm) {
     return s;
 }
 
+// Sums of two values over the tpr threads of a row group (a multiple of 32), through red[warp].
+// One block barrier; calls in a row alternate between two arrays.
+__device__ __forceinline__ void group_sum2(float& x, float& y, int tpr, float2* red) {
+    x = warp_sum(x);
+    y = warp_sum(y);
+    const int warp = threadIdx.x >> 5, nw = tpr >> 5;
+    if ((threadIdx.x & 31) == 0) red[warp] = make_float2(x, y);
+    __syncthreads();
+    const float2* g = red + warp / nw * nw;
+    x = y = 0.f;
+    for (int i = 0; i < nw; ++i) {
+        x += g[i].x;
+        y += g[i].y;
+    }
+}
+
+// Rows of up to 4 vectors per thread, kept in registers: one read, one write. A group of tpr
+// threads per row, 256 / tpr rows per block.
+constexpr int kVpt = 4;
+template <typename T, bool LAYER>
+__global__ void __launch_bounds__(kNormThreads) norm_forward_rows_kernel(const NormArgs a, int tpr) {
+    constexpr int V = Vec<T>::N;
+    __shared__ float2 red[2][kNormThreads / 32];
+    const int n = a.H / V, g = threadIdx.x / tpr, c0 = threadIdx.x % tpr;
+    const int64_t t = int64_t(blockIdx.x) * (kNormThreads / tpr) + g;
+    const bool live = t < a.T;
+    const T* x = static_cast<const T*>(a.x) + (live ? t : 0) * a.ldx;
+    uint4 xv[kVpt];
+#pragma unroll
+    for (int i = 0; i < kVpt; ++i) {
+        const int c = c0 + i * tpr;
+        xv[i] = live && c < n ? ld_stream16(x + c * V) : make_uint4(0, 0, 0, 0);
+    }
+    float mean = 0.f, s = 0.f, unused = 0.f;
+    if constexpr (LAYER) {
+#pragma unroll
+        for (int i = 0; i < kVpt; ++i) {
+            float f[V];
+            unpack_vec<T>(xv[i], f);
+#pragma unroll
+            for (int q = 0; q < V; ++q) s += f[q];
+        }
+        group_sum2(s, unused, tpr, red[0]);
+        mean = s / float(a.H);
+        s = unused = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kVpt; ++i) {
+        if (c0 + i * tpr >= n) break;
+        float f[V];
+        unpack_vec<T>(xv[i], f);
+#pragma unroll
+        for (int q = 0; q < V; ++q) s = fmaf(f[q] - mean, f[q] - mean, s);
+    }
+    group_sum2(s, unused, tpr, red[1]);
+    if (!live) return;
+    const float rstd = 1.0f / sqrtf(s / float(a.H) + a.eps);
+    T* y = static_cast<T*>(a.y) + t * a.ldy;
+#pragma unroll
+    for (int i = 0; i < kVpt; ++i) {
+        const int c = c0 + i * tpr;
+        if (c >= n) break;
+        float f[V], w[V], b[V] = {};
+        unpack_vec<T>(xv[i], f);
+        load_vec(static_cast<const T*>(a.w) + c * V, w);
+        if (LAYER && a.b) load_vec(static_cast<const T*>(a.b) + c * V, b);
+#pragma unroll
+        for (int q = 0; q < V; ++q) f[q] = (f[q] - mean) * rstd * w[q] + b[q];
+        store_vec(y + c * V, f);
+    }
+    if (a.stats && c0 == 0) *reinterpret_cast<float2*>(a.stats + 2 * t) = make_float2(mean, rstd);
+}
+
+// Wider rows: read again (from L2) for each pass.
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) norm_forward_kernel(const NormArgs a) {
     constexpr int V = Vec<T>::N;
@@ -69,6 +145,131 @@ __global__ void __launch_bounds__(kNormThreads) norm_forward_kernel(const NormAr
     }
 }
 
+// Backward for rows of up to 4 vectors per thread: one read of x and dy serves dx, dw and db.
+// Two blocks per SM walk the rows; x and dy of the next rows are brought to shared memory by
+// bulk copies meanwhile (registers hold the running column sums, so they cannot hold loads in
+// flight as well). Each thread keeps its columns' sums over all of the block's rows; the
+// block's rows groups add up in order at the end, then norm_finish_kernel adds the blocks.
+constexpr int kNormStages = 8;
+template <typename T, bool LAYER>
+__global__ void __launch_bounds__(kNormThreads, 2) norm_backward_rows_kernel(const NormArgs a, int tpr, int stages) {
+    constexpr int V = Vec<T>::N;
+    extern __shared__ __align__(128) uint8_t sm[];
+    __shared__ float2 red[2][kNormThreads / 32];
+    __shared__ uint64_t full[kNormStages];
+    const int n = a.H / V, G = kNormThreads / tpr, g = threadIdx.x / tpr, c0 = threadIdx.x % tpr;
+    const uint32_t row_bytes = uint32_t(a.H) * sizeof(T);
+    const uint4* sw = reinterpret_cast<const uint4*>(sm);
+    uint8_t* ring = sm + (row_bytes + 127) / 128 * 128;
+    const uint32_t stage_bytes = 2 * G * row_bytes;
+    const int64_t groups = (a.T + G - 1) / G;
+    for (int c = threadIdx.x; c < n; c += kNormThreads)
+        reinterpret_cast<uint4*>(sm)[c] = reinterpret_cast<const uint4*>(a.w)[c];
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    const uint64_t pol = policy_evict_first();
+    auto fill = [&](int64_t grp, int st) {  // one thread
+        const int64_t t0 = grp * G;
+        const int rows = int(min(int64_t(G), a.T - t0));
+        mbar_expect_tx(&full[st], 2 * rows * row_bytes);
+        for (int r = 0; r < rows; ++r) {
+            uint8_t* d = ring + st * stage_bytes + r * 2 * row_bytes;
+            bulk_g2s(d, static_cast<const T*>(a.x) + (t0 + r) * a.ldx, row_bytes, &full[st], pol);
+            bulk_g2s(d + row_bytes, static_cast<const T*>(a.dy) + (t0 + r) * a.lddy, row_bytes, &full[st], pol);
+        }
+    };
+    if (threadIdx.x == 0)
+        for (int i = 0; i < stages; ++i)
+            if (blockIdx.x + int64_t(i) * gridDim.x < groups) fill(blockIdx.x + int64_t(i) * gridDim.x, i);
+    float aw[kVpt][V] = {}, ab[kVpt][V] = {};
+    int st = 0, it = 0;
+    uint32_t phase = 0;
+    for (int64_t grp = blockIdx.x; grp < groups; grp += gridDim.x, ++it) {
+        if (!mbar_wait(&full[st], phase, gtimer() + 2000000000ull)) break;
+        const int64_t t = grp * G + g;
+        const bool live = t < a.T;
+        float mean = 0.f, rstd = 0.f;
+        if (live) {
+            const float2 ms = __ldg(reinterpret_cast<const float2*>(a.cstats + 2 * t));
+            mean = ms.x;
+            rstd = ms.y;
+        }
+        const uint4* sx = reinterpret_cast<const uint4*>(ring + st * stage_bytes + g * 2 * row_bytes);
+        const uint4* sd = reinterpret_cast<const uint4*>(ring + st * stage_bytes + g * 2 * row_bytes + row_bytes);
+        uint4 xv[kVpt], dv[kVpt];
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < kVpt; ++i) {
+            const int c = c0 + i * tpr;
+            if (!live || c >= n) break;
+            xv[i] = sx[c];
+            dv[i] = sd[c];
+            float f[V], d[V], w[V];
+            unpack_vec<T>(xv[i], f);
+            unpack_vec<T>(dv[i], d);
+            unpack_vec<T>(sw[c], w);
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const float xh = (f[q] - mean) * rstd;
+                aw[i][q] = fmaf(d[q], xh, aw[i][q]);
+                if (LAYER) ab[i][q] += d[q];
+                const float dw = d[q] * w[q];
+                if (LAYER) s1 += dw;
+                s2 = fmaf(dw, xh, s2);
+            }
+        }
+        group_sum2(s1, s2, tpr, red[it & 1]);
+        // every thread has read the stage: bring its next rows
+        if (threadIdx.x == 0 && grp + int64_t(stages) * gridDim.x < groups) fill(grp + int64_t(stages) * gridDim.x, st);
+        if (++st == stages) {
+            st = 0;
+            phase ^= 1u;
+        }
+        if (!live || !a.dx) continue;
+        s1 /= float(a.H);
+        s2 /= float(a.H);
+        T* dx = static_cast<T*>(a.dx) + t * a.lddx;
+#pragma unroll
+        for (int i = 0; i < kVpt; ++i) {
+            const int c = c0 + i * tpr;
+            if (c >= n) break;
+            float f[V], d[V], w[V];
+            unpack_vec<T>(xv[i], f);
+            unpack_vec<T>(dv[i], d);
+            unpack_vec<T>(sw[c], w);
+#pragma unroll
+            for (int q = 0; q < V; ++q) f[q] = rstd * (d[q] * w[q] - s1 - (f[q] - mean) * rstd * s2);
+            store_vec(dx + c * V, f);
+        }
+    }
+    if (!a.partial) return;
+    // the row groups' sums, one group after the other (the ring is free: every copy was waited for)
+    __syncthreads();
+    float* acc = reinterpret_cast<float*>(ring);
+    for (int j = 0; j < G; ++j) {
+        if (g == j) {
+#pragma unroll
+            for (int i = 0; i < kVpt; ++i) {
+                const int c = c0 + i * tpr;
+                if (c >= n) break;
+#pragma unroll
+                for (int q = 0; q < V; ++q) {
+                    float *pw = acc + c * V + q, *pb = acc + a.H + c * V + q;
+                    *pw = j ? *pw + aw[i][q] : aw[i][q];
+                    if (LAYER) *pb = j ? *pb + ab[i][q] : ab[i][q];
+                }
+            }
+        }
+        __syncthreads();
+    }
+    float* o = a.partial + int64_t(blockIdx.x) * 2 * a.H;
+    for (int c = threadIdx.x; c < (LAYER ? 2 : 1) * a.H; c += kNormThreads) o[c] = acc[c];
+}
+
+// Wider rows.
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) norm_dx_kernel(const NormArgs a) {
     constexpr int V = Vec<T>::N;
@@ -147,43 +348,115 @@ __global__ void __launch_bounds__(kColVecs * kColRows) norm_dw_kernel(const Norm
     }
 }
 
+// The blocks' partial sums: 32 columns per block, 8 threads per column each adding every 8th
+// part, then those 8 in order; rounded once.
 template <typename T>
 __global__ void __launch_bounds__(256) norm_finish_kernel(const NormArgs a, int parts) {
-    const int i = blockIdx.x * 256 + threadIdx.x;
-    if (i >= 2 * a.H) return;
-    const int which = i / a.H, c = i - which * a.H;
-    T* o = static_cast<T*>(which ? a.db : a.dw);
+    __shared__ float sm[8][33];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + x;
+    T* o = static_cast<T*>(blockIdx.y ? a.db : a.dw);
     if (!o) return;
     float s = 0.f;
-    for (int p = 0; p < parts; ++p) s += a.partial[(int64_t(p) * 2 + which) * a.H + c];
+    if (c < a.H)
+#pragma unroll 8
+        for (int p = y; p < parts; p += 8) s += a.partial[(int64_t(p) * 2 + blockIdx.y) * a.H + c];
+    sm[y][x] = s;
+    __syncthreads();
+    if (y != 0 || c >= a.H) return;
+    s = sm[0][x];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) s += sm[j][x];
     o[c] = from_f<T>(s);
 }
 
-template <typename T>
-cudaError_t backward_t(const NormArgs& a, cudaStream_t s) {
-    constexpr int V = Vec<T>::N;
-    if (a.dx) norm_dx_kernel<T><<<unsigned(std::min<int64_t>(a.T, 148 * 8)), kNormThreads, 0, s>>>(a);
-    if (a.dw || a.db) {
-        const int parts = norm_blocks(a.T, a.H);
-        const dim3 grid((a.H / V + kColVecs - 1) / kColVecs, parts);
-        norm_dw_kernel<T><<<grid, kColVecs * kColRows, 0, s>>>(a);
-        norm_finish_kernel<T><<<(2 * a.H + 255) / 256, 256, 0, s>>>(a, parts);
+// Threads per row that hold it in registers, or 0 for wider rows.
+int threads_per_row(int H, int V) {
+    for (int tpr = 32; tpr <= kNormThreads; tpr *= 2)
+        if (H / V <= tpr * kVpt) return tpr;
+    return 0;
+}
+
+// Shared memory of the backward kernel: w, then as many stages as fit about 100 KB (two blocks
+// per SM), which the final sums (2 H floats) reuse.
+struct NormRing {
+    int stages, bytes;
+};
+NormRing norm_ring(int H, int es, int tpr) {
+    const int row = H * es, w = (row + 127) / 128 * 128, stage = 2 * (kNormThreads / tpr) * row;
+    NormRing r;
+    r.stages = std::max(2, std::min(kNormStages, (100 * 1024 - w) / stage));
+    r.bytes = w + std::max(r.stages * stage, 2 * H * 4);
+    return r;
+}
+
+int backward_parts(int64_t T, int H, int V, bool* rows) {
+    const int tpr = threads_per_row(H, V);
+    *rows = tpr > 0;
+    if (tpr) return int(std::min<int64_t>((T + kNormThreads / tpr - 1) / (kNormThreads / tpr), 2 * 148));
+    const int64_t cb = (H + 511) / 512;
+    return int(std::max<int64_t>(1, std::min<int64_t>(std::max<int64_t>(1, 592 / cb), T / 16)));
+}
+
+template <typename T, bool LAYER>
+cudaError_t backward_rows(const NormArgs& a, int parts, cudaStream_t s) {
+    static std::atomic<uint64_t> allowed{0};
+    const int tpr = threads_per_row(a.H, Vec<T>::N);
+    const NormRing ring = norm_ring(a.H, sizeof(T), tpr);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (!(allowed.load() & bit)) {
+        e = cudaFuncSetAttribute(norm_backward_rows_kernel<T, LAYER>, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024);
+        if (e != cudaSuccess) return e;
+        allowed.fetch_or(bit);
     }
+    norm_backward_rows_kernel<T, LAYER><<<parts, kNormThreads, ring.bytes, s>>>(a, tpr, ring.stages);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t backward_t(NormArgs a, cudaStream_t s) {
+    constexpr int V = Vec<T>::N;
+    bool rows;
+    const int parts = backward_parts(a.T, a.H, V, &rows);
+    const bool sums = a.dw || a.db;
+    if (!sums) a.partial = nullptr;
+    if (!sums && !a.dx) return cudaSuccess;
+    if (rows) {
+        const cudaError_t e = a.kind == MOE_NORM_LAYER ? backward_rows<T, true>(a, parts, s) : backward_rows<T, false>(a, parts, s);
+        if (e != cudaSuccess) return e;
+    } else {
+        if (a.dx) norm_dx_kernel<T><<<unsigned(std::min<int64_t>(a.T, 148 * 8)), kNormThreads, 0, s>>>(a);
+        if (sums) norm_dw_kernel<T><<<dim3((a.H / V + kColVecs - 1) / kColVecs, parts), kColVecs * kColRows, 0, s>>>(a);
+    }
+    if (sums) norm_finish_kernel<T><<<dim3((a.H + 31) / 32, a.db ? 2 : 1), 256, 0, s>>>(a, parts);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t forward_t(const NormArgs& a, cudaStream_t s) {
+    const int tpr = threads_per_row(a.H, Vec<T>::N);
+    if (!tpr) {
+        norm_forward_kernel<T><<<unsigned(std::min<int64_t>(a.T, 148 * 8)), kNormThreads, 0, s>>>(a);
+        return cudaGetLastError();
+    }
+    const unsigned grid = unsigned((a.T + kNormThreads / tpr - 1) / (kNormThreads / tpr));
+    if (a.kind == MOE_NORM_LAYER) norm_forward_rows_kernel<T, true><<<grid, kNormThreads, 0, s>>>(a, tpr);
+    else norm_forward_rows_kernel<T, false><<<grid, kNormThreads, 0, s>>>(a, tpr);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-int norm_blocks(int64_t T, int H) {
-    const int64_t cb = (H + 511) / 512;
-    return int(std::max<int64_t>(1, std::min<int64_t>(std::max<int64_t>(1, 592 / cb), T / 16)));
+int norm_blocks(int64_t T, int H, int dtype) {
+    bool rows;
+    return backward_parts(T, H, dtype == MOE_DTYPE_F32 ? 4 : 8, &rows);
 }
 
 cudaError_t launch_norm_forward(const NormArgs& a, cudaStream_t s) {
-    const unsigned grid = unsigned(std::min<int64_t>(a.T, 148 * 8));
-    if (a.dtype == MOE_DTYPE_F32) norm_forward_kernel<float><<<grid, kNormThreads, 0, s>>>(a);
-    else norm_forward_kernel<__nv_bfloat16><<<grid, kNormThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return a.dtype == MOE_DTYPE_F32 ? forward_t<float>(a, s) : forward_t<__nv_bfloat16>(a, s);
 }
 
 cudaError_t launch_norm_backward(const NormArgs& a, cudaStream_t s) {

@@ -67,7 +67,17 @@ moe_status check_linear(const moe_linear_desc* d, int64_t T) {
 }
 
 cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t s) {
-    return g.dtype == MOE_DTYPE_F32 ? launch_simt_gemm(g, s) : launch_tc_gemm_train(g, s);
+    return g.dtype == MOE_DTYPE_F32 ? launch_simt_gemm(&g, 1, s) : launch_tc_gemm_train(g, s);
+}
+
+// Independent products: one launch in f32, one each in bf16.
+cudaError_t launch_gemms(const GemmArgs* g, int n, cudaStream_t s) {
+    if (n > 0 && g[0].dtype == MOE_DTYPE_F32) return launch_simt_gemm(g, n, s);
+    for (int i = 0; i < n; ++i) {
+        const cudaError_t e = launch_tc_gemm_train(g[i], s);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 struct LinearWs {
@@ -320,25 +330,29 @@ moe_status moe_linear_backward(const moe_linear_desc* d, const void* dy, int64_t
         }
         MOE_CUDA(launch_dact(a, s));
     }
-    GemmArgs g;
-    g.plan.status = device_status;
-    g.dtype = d->dtype;
+    GemmArgs g[2];
+    int n = 0;
     if (dx) {
-        g.kind = kNN;
-        g.a = dz; g.lda = lddz;
-        g.b = w; g.ldb = K;
-        g.M = T; g.N = K; g.R = N;
-        g.out = dx; g.ldo = lddx;
-        MOE_CUDA(launch_gemm(g, s));
+        GemmArgs& p = g[n++];
+        p.kind = kNN;
+        p.a = dz; p.lda = lddz;
+        p.b = w; p.ldb = K;
+        p.M = T; p.N = K; p.R = N;
+        p.out = dx; p.ldo = lddx;
     }
     if (dw) {
-        g.kind = kTN;
-        g.a = dz; g.lda = lddz;
-        g.b = x; g.ldb = ldx;
-        g.M = N; g.N = K; g.R = T;
-        g.out = dw; g.ldo = K;
-        MOE_CUDA(launch_gemm(g, s));
+        GemmArgs& p = g[n++];
+        p.kind = kTN;
+        p.a = dz; p.lda = lddz;
+        p.b = x; p.ldb = ldx;
+        p.M = N; p.N = K; p.R = T;
+        p.out = dw; p.ldo = K;
     }
+    for (int i = 0; i < n; ++i) {
+        g[i].plan.status = device_status;
+        g[i].dtype = d->dtype;
+    }
+    MOE_CUDA(launch_gemms(g, n, s));
     return MOE_OK;
 }
 
@@ -433,7 +447,7 @@ moe_status moe_ffn_forward(const moe_config* cfg, const moe_weights* w, const vo
     if (f.dtype == MOE_DTYPE_F32) {
         g.out = at<void>(ws, L.gp); g.ldo = 2 * f.I;
         ga.gp = at<float>(ws, L.gp);
-        MOE_CUDA(launch_simt_gemm(g, s));
+        MOE_CUDA(launch_simt_gemm(&g, 1, s));
         MOE_CUDA(launch_gated_forward(ga, s));
     } else {
         MOE_CUDA(launch_tc_gateup(g, ga, s));
@@ -527,8 +541,6 @@ moe_status moe_ffn_backward(const moe_config* cfg, const moe_weights* w, const v
         up = ga.dst[0];
         dyp = ga.dst[1];
         ldup = lddyp = f.K;
-        // slots without a row (dropped) have no gradient
-        if (dtopk_w) MOE_CUDA(cudaMemsetAsync(dtopk_w, 0, size_t(f.S) * 4, s));
     }
     // dh = dy Wd
     GemmArgs g;
@@ -554,19 +566,18 @@ moe_status moe_ffn_backward(const moe_config* cfg, const moe_weights* w, const v
     if (f.dtype == MOE_DTYPE_F32) {
         g.out = at<void>(ws, L.dh); g.ldo = f.I;
         ga.dh = at<float>(ws, L.dh);
-        MOE_CUDA(launch_simt_gemm(g, s));
+        MOE_CUDA(launch_simt_gemm(&g, 1, s));
         MOE_CUDA(launch_gated_backward(ga, s));
     } else {
         float* parts = dtopk_w ? at<float>(ws, L.parts) : nullptr;
         MOE_CUDA(launch_tc_dgated(g, ga, parts, s));
         if (dtopk_w) MOE_CUDA(launch_dtopk(ga, parts, dgated_parts(p, f.I, f.K), s));
     }
-    // du = dg Wg + dv Wu
-    if (du) {
-        GemmArgs x;
+    GemmArgs gm[3];
+    int n = 0;
+    if (du) {  // du = dg Wg + dv Wu
+        GemmArgs& x = gm[n++];
         x.kind = kNN;
-        x.plan = p;
-        x.dtype = f.dtype;
         x.a = ga.dgu; x.lda = 2 * f.I;
         x.b = f.il ? w->gate_up_w : w->gate_w; x.ldb = f.K; x.sb = int64_t(f.I) * f.K * (f.il ? 2 : 1);
         if (!f.il) {
@@ -575,36 +586,44 @@ moe_status moe_ffn_backward(const moe_config* cfg, const moe_weights* w, const v
         }
         x.M = f.T; x.N = f.K; x.R = 2 * f.I;
         x.out = dense ? du : at<void>(ws, L.rows_out); x.ldo = dense ? lddu : f.K; x.out_f32 = !dense;
-        MOE_CUDA(launch_gemm(x, s));
-        if (!dense) {
-            SumSlotsArgs sa;
-            sa.plan = p;
-            sa.rows = at<float>(ws, L.rows_out);
-            sa.out = du; sa.ldo = lddu;
-            sa.K = f.K;
-            sa.dtype = f.dtype;
-            MOE_CUDA(launch_sum_slots(sa, s));
+    }
+    {  // dWd = dy^T (w h)
+        GemmArgs& t = gm[n++];
+        t.kind = kTN;
+        t.a = dyp; t.lda = lddyp;
+        t.b = ga.hw; t.ldb = f.I;
+        t.M = f.K; t.N = f.I; t.R = f.T;
+        t.out = gr->down_w; t.ldo = f.I; t.so = int64_t(f.K) * f.I;
+    }
+    {  // [dWg; dWu] = [dg dv]^T u
+        GemmArgs& t = gm[n++];
+        t.kind = kTN;
+        t.a = ga.dgu; t.lda = 2 * f.I;
+        t.b = up; t.ldb = ldup;
+        t.M = 2 * f.I; t.N = f.K; t.R = f.T;
+        t.out = f.il ? gr->gate_up_w : gr->gate_w; t.ldo = f.K; t.so = int64_t(f.I) * f.K * (f.il ? 2 : 1);
+        if (!f.il) {
+            t.out1 = gr->up_w;
+            t.split = f.I;
         }
     }
-    // dWd = dy^T (w h),  [dWg; dWu] = [dg dv]^T u
-    GemmArgs t;
-    t.kind = kTN;
-    t.plan = p;
-    t.dtype = f.dtype;
-    t.a = dyp; t.lda = lddyp;
-    t.b = ga.hw; t.ldb = f.I;
-    t.M = f.K; t.N = f.I; t.R = f.T;
-    t.out = gr->down_w; t.ldo = f.I; t.so = int64_t(f.K) * f.I;
-    MOE_CUDA(launch_gemm(t, s));
-    t.a = ga.dgu; t.lda = 2 * f.I;
-    t.b = up; t.ldb = ldup;
-    t.M = 2 * f.I; t.N = f.K;
-    t.out = f.il ? gr->gate_up_w : gr->gate_w; t.ldo = f.K; t.so = int64_t(f.I) * f.K * (f.il ? 2 : 1);
-    if (!f.il) {
-        t.out1 = gr->up_w;
-        t.split = f.I;
+    for (int i = 0; i < n; ++i) {
+        gm[i].plan = p;
+        gm[i].dtype = f.dtype;
     }
-    MOE_CUDA(launch_gemm(t, s));
+    // f32: all in one launch; bf16: du first, whose rows the sum then finds in L2
+    const int first = f.dtype == MOE_DTYPE_F32 ? n : (du ? 1 : 0);
+    MOE_CUDA(launch_gemms(gm, first, s));
+    if (du && !dense) {
+        SumSlotsArgs sa;
+        sa.plan = p;
+        sa.rows = at<float>(ws, L.rows_out);
+        sa.out = du; sa.ldo = lddu;
+        sa.K = f.K;
+        sa.dtype = f.dtype;
+        MOE_CUDA(launch_sum_slots(sa, s));
+    }
+    MOE_CUDA(launch_gemms(gm + first, n - first, s));
     if (f.bias) {
         ColsumArgs c;
         c.plan = p;
@@ -641,7 +660,7 @@ moe_status check_norm(const moe_norm_desc* d, int64_t T) {
     return MOE_OK;
 }
 size_t norm_ws(const moe_norm_desc* d, int64_t T, bool backward) {
-    return backward && T > 0 ? align256(size_t(norm_blocks(T, d->width)) * 2 * d->width * 4) : 0;
+    return backward && T > 0 ? align256(size_t(norm_blocks(T, d->width, d->dtype)) * 2 * d->width * 4) : 0;
 }
 }  // namespace
 

@@ -30,7 +30,7 @@ struct RowPlan {
     int32_t* poff = nullptr;      // [E + 1] first padded row of each expert
     int32_t* uoff = nullptr;      // [E + 1] first sorted position of each expert (checked copy)
     int32_t* row_slot = nullptr;  // [padded rows] slot, or -1 (padding, dropped)
-    int32_t* slot_row = nullptr;  // [S] padded row, or -1 (dropped)
+    int32_t* slot_row = nullptr;  // [S] padded row; anything for a slot without one
     int64_t max_rows = 0;         // dense: T
     int* status = nullptr;
 };
@@ -91,7 +91,9 @@ struct GemmArgs {
     int dtype = MOE_DTYPE_BF16;        // a, b, bias, residual, pre
     int out_f32 = 0;                   // out is f32 instead
 };
-cudaError_t launch_simt_gemm(const GemmArgs& a, cudaStream_t s);     // f32
+// f32: n independent products (at most kMaxSimt) in one launch.
+constexpr int kMaxSimt = 3;
+cudaError_t launch_simt_gemm(const GemmArgs* a, int n, cudaStream_t s);
 cudaError_t launch_tc_gemm_train(const GemmArgs& a, cudaStream_t s);  // bf16, any kind
 
 // The forward products for at most kSmallT tokens, both types.
@@ -186,7 +188,7 @@ struct NormArgs {
     const float* cstats = nullptr;
     float* partial = nullptr;  // [norm_blocks, 2, H]
 };
-int norm_blocks(int64_t T, int H);
+int norm_blocks(int64_t T, int H, int dtype);
 cudaError_t launch_norm_forward(const NormArgs& a, cudaStream_t s);
 cudaError_t launch_norm_backward(const NormArgs& a, cudaStream_t s);
 

@@ -88,7 +88,14 @@ __global__ void __launch_bounds__(kGatherThreads) gather_padded_kernel(const Gat
     }
 }
 
-// One block row per token: its slots' rows added in slot order in f32.
+// Padded row of a slot, or -1 for one without (dropped): slot_row is written for slots that
+// have a row only and never cleared, so what it says is checked against the row's own slot.
+__device__ __forceinline__ int row_of_slot(const RowPlan& p, int slot) {
+    const int r = p.slot_row[slot];
+    return r >= 0 && r < p.poff[p.E] && p.row_slot[r] == slot ? r : -1;
+}
+
+// Each token's slots' rows added in slot order in f32.
 template <typename T>
 __global__ void __launch_bounds__(256) sum_slots_kernel(const SumSlotsArgs a) {
     constexpr int V = Vec<T>::N;
@@ -98,9 +105,8 @@ __global__ void __launch_bounds__(256) sum_slots_kernel(const SumSlotsArgs a) {
         const int64_t t = i / vpr;
         const int c = int(i - t * vpr) * V;
         float acc[V] = {};
-        const int32_t* sr = a.plan.slot_row + t * a.plan.k;
         for (int j = 0; j < a.plan.k; ++j) {
-            const int r = sr[j];
+            const int r = row_of_slot(a.plan, int(t) * a.plan.k + j);
             if (r < 0) continue;
             float f[V];
 #pragma unroll
@@ -194,7 +200,7 @@ __global__ void __launch_bounds__(256) gated_backward_kernel(const GatedArgs a) 
             dgu[cv] = from_f<T>(dv);
             hw[i] = from_f<T>(hh);
         }
-        if (!a.dtopk_w || o.slot < 0) continue;
+        if (!a.dtopk_w || o.slot < 0 || !a.plan.offsets) continue;
         if (a.down_b)
             for (int c = lane; c < a.K; c += 32)
                 dw += to_f<T>(static_cast<const T*>(a.dyp)[r * a.K + c]) *
@@ -202,15 +208,21 @@ __global__ void __launch_bounds__(256) gated_backward_kernel(const GatedArgs a) 
         dw = warp_sum(dw);
         if (lane == 0) a.dtopk_w[o.slot] = dw;
     }
+    if (a.dtopk_w && a.plan.offsets)  // slots without a row
+        for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < a.plan.S; i += int64_t(gridDim.x) * 256)
+            if (row_of_slot(a.plan, int(i)) < 0) a.dtopk_w[i] = 0.0f;
 }
 
-// One warp per row: its partial sums in order, and with a down bias the row's dy . down_b.
+// One warp per slot: its row's partial sums in order, and with a down bias the row's dy . down_b.
 __global__ void __launch_bounds__(256) dtopk_kernel(const GatedArgs a, const float* partial, int parts) {
     const int lane = threadIdx.x & 31;
-    const int64_t rows = plan_rows(a.plan), warps = int64_t(gridDim.x) * 8;
-    for (int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); r < rows; r += warps) {
-        const int slot = a.plan.row_slot[r];
-        if (slot < 0) continue;
+    const int64_t warps = int64_t(gridDim.x) * 8;
+    for (int64_t slot = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); slot < a.plan.S; slot += warps) {
+        const int64_t r = row_of_slot(a.plan, int(slot));
+        if (r < 0) {
+            if (lane == 0) a.dtopk_w[slot] = 0.0f;
+            continue;
+        }
         float dw = 0.0f;
         for (int i = lane; i < parts; i += 32) dw += partial[r * parts + i];
         if (a.down_b) {
@@ -380,8 +392,6 @@ unsigned grid_for(int64_t items, int64_t per_block, int64_t most) {
 }  // namespace
 
 cudaError_t launch_gather_padded(const GatherArgs& a, cudaStream_t s) {
-    const cudaError_t e = cudaMemsetAsync(a.plan.slot_row, 0xFF, size_t(a.plan.S) * 4, s);
-    if (e != cudaSuccess) return e;
     const unsigned grid = grid_for(a.plan.max_rows, kGatherThreads / 32, 148 * 4);
     gather_padded_kernel<<<grid, kGatherThreads, 0, s>>>(a);
     return cudaGetLastError();
@@ -406,7 +416,7 @@ cudaError_t launch_gated_backward(const GatedArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_dtopk(const GatedArgs& a, const float* partial, int parts, cudaStream_t s) {
-    dtopk_kernel<<<grid_for(a.plan.max_rows, 8, 148 * 8), 256, 0, s>>>(a, partial, parts);
+    dtopk_kernel<<<grid_for(a.plan.S, 8, 148 * 8), 256, 0, s>>>(a, partial, parts);
     return cudaGetLastError();
 }
 

@@ -38,18 +38,22 @@ __device__ __forceinline__ void stash(float (&sm)[kBR][64 + 4], const float (&v)
     }
 }
 
+struct Shared {
+    float a[kBR][kBM + 4], b[kBR][kBN + 4];
+};
+
 template <int KIND>
-__global__ void __launch_bounds__(kThreads) simt_gemm_kernel(const GemmArgs a) {
+__device__ void simt_tile(const GemmArgs& a, int64_t m0, int64_t n0, int z, Shared& sh) {
     using T = float;
     constexpr bool AR = KIND == kTN, BR = KIND != kNT;  // operand rows are reduction indices
-    __shared__ float sa[kBR][kBM + 4], sb[kBR][kBN + 4];
+    auto& sa = sh.a;
+    auto& sb = sh.b;
     const RowPlan& p = a.plan;
     const bool grouped = p.offsets != nullptr;
-    const int64_t m0 = int64_t(blockIdx.x) * kBM, n0 = int64_t(blockIdx.y) * kBN;
     int e = 0;
     int64_t M = a.M, r0 = 0, R = a.R;
     if (KIND == kTN) {
-        e = blockIdx.z;
+        e = z;
         if (grouped) {
             r0 = p.poff[e];
             R = r0 + (p.uoff[e + 1] - p.uoff[e]);
@@ -142,16 +146,45 @@ __global__ void __launch_bounds__(kThreads) simt_gemm_kernel(const GemmArgs a) {
     }
 }
 
+struct Simt {
+    GemmArgs p[kMaxSimt];
+    int64_t end[kMaxSimt];  // first tile after problem i
+    int tx[kMaxSimt], ty[kMaxSimt];
+    int n;
+};
+
+__global__ void __launch_bounds__(kThreads) simt_gemm_kernel(const __grid_constant__ Simt S) {
+    __shared__ Shared sh;
+    int64_t t = blockIdx.x;
+    int i = 0;
+    while (i < S.n - 1 && t >= S.end[i]) ++i;
+    if (i > 0) t -= S.end[i - 1];
+    // row tiles fastest: neighbouring blocks share operand B
+    const int64_t mt = t % S.tx[i], r = t / S.tx[i];
+    const int nt = int(r % S.ty[i]), z = int(r / S.ty[i]);
+    const GemmArgs& a = S.p[i];
+    if (a.kind == kNT) simt_tile<kNT>(a, mt * kBM, int64_t(nt) * kBN, z, sh);
+    else if (a.kind == kNN) simt_tile<kNN>(a, mt * kBM, int64_t(nt) * kBN, z, sh);
+    else simt_tile<kTN>(a, mt * kBM, int64_t(nt) * kBN, z, sh);
+}
+
 }  // namespace
 
-cudaError_t launch_simt_gemm(const GemmArgs& a, cudaStream_t s) {
-    const bool grouped = a.plan.offsets != nullptr;
-    const int64_t rows = a.kind == kTN ? a.M : grouped ? a.plan.max_rows : a.M;
-    const dim3 grid(unsigned((rows + kBM - 1) / kBM), unsigned((a.N + kBN - 1) / kBN),
-                    a.kind == kTN && grouped ? unsigned(a.plan.E) : 1u);
-    if (a.kind == kNT) simt_gemm_kernel<kNT><<<grid, kThreads, 0, s>>>(a);
-    else if (a.kind == kNN) simt_gemm_kernel<kNN><<<grid, kThreads, 0, s>>>(a);
-    else simt_gemm_kernel<kTN><<<grid, kThreads, 0, s>>>(a);
+cudaError_t launch_simt_gemm(const GemmArgs* a, int n, cudaStream_t s) {
+    Simt S;
+    S.n = n;
+    int64_t tiles = 0;
+    for (int i = 0; i < n; ++i) {
+        const bool grouped = a[i].plan.offsets != nullptr;
+        const int64_t rows = a[i].kind == kTN ? a[i].M : grouped ? a[i].plan.max_rows : a[i].M;
+        S.p[i] = a[i];
+        S.tx[i] = int((rows + kBM - 1) / kBM);
+        S.ty[i] = (a[i].N + kBN - 1) / kBN;
+        tiles += int64_t(S.tx[i]) * S.ty[i] * (a[i].kind == kTN && grouped ? a[i].plan.E : 1);
+        S.end[i] = tiles;
+    }
+    if (tiles >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    simt_gemm_kernel<<<unsigned(tiles), kThreads, 0, s>>>(S);
     return cudaGetLastError();
 }
 

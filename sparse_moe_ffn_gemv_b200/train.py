@@ -158,6 +158,13 @@ class _Operator:
     def _empty(self, *shape, dtype=None):
         return torch.empty(shape, dtype=dtype or self.dtype, device=self.device)
 
+    def _like(self, t, *shape):
+        """An uninitialised tensor of the handle's dtype; like t where t has that shape
+        (a microsecond less than torch.empty)."""
+        if t.shape == shape and t.is_contiguous():
+            return torch.empty_like(t)
+        return t.new_empty(shape)
+
     def _stream(self):
         return torch._C._cuda_getCurrentRawStream(self._index)
 
@@ -185,7 +192,7 @@ class Linear(_Operator):
         wp = self._flat("w", w, N * K)
         bp = None if bias is None else self._flat("bias", bias, N)
         rp, ldr = (None, 0) if residual is None else self._rows("residual", residual, N, T)
-        y = self._empty(T, N) if out is None else out
+        y = (x.new_empty((T, N)) if residual is None else self._like(residual, T, N)) if out is None else out
         yp, ldy = self._rows("out", y, N, T)
         pre = self._empty(T, N) if keep else None
         ws, n = self._workspace(self.lib.moe_linear_workspace_size, self._desc, T, 0)
@@ -205,8 +212,8 @@ class Linear(_Operator):
         xp, ldx = self._rows("x", x, K)
         wp = self._flat("w", w, N * K)
         pp = None if pre is None else self._flat("pre", pre, T * N)
-        dx = self._empty(T, K) if input_grad else None
-        dw = self._empty(N, K) if weight_grad else None
+        dx = self._like(x, T, K) if input_grad else None
+        dw = self._like(w, N, K) if weight_grad else None
         db = self._empty(N) if bias_grad else None
         ws, n = self._workspace(self.lib.moe_linear_workspace_size, self._desc, T, 1)
         M._check(self.lib.moe_linear_backward(self._desc, gp, ldg, xp, ldx, wp, pp, T, _p(dx), K,
@@ -238,15 +245,18 @@ class GatedFfn(_Operator):
             shapes.update({"gate_up_b": (E, 2 * I)} if spec.gate_up_interleaved else {"gate_b": (E, I), "up_b": (E, I)})
             shapes["down_b"] = (E, K)
         self.shapes = shapes
-        self._numel = {f: functools.reduce(int.__mul__, s) for f, s in shapes.items()}
+        self._planes_numel = [(f, functools.reduce(int.__mul__, s)) for f, s in shapes.items()]
 
-    def _planes(self, struct, tensors, what: str):
-        for f, n in self._numel.items():
+    def _planes(self, tensors):
+        w, dtype, index = M.MoeWeights(), self.dtype, self._index
+        for f, n in self._planes_numel:
             t = tensors.get(f)
             if t is None:
-                raise M.MoeError(M.STATUS_CODE["MOE_ERR_MISSING_TENSOR"], f"{what} {f}")
-            setattr(struct, f, self._flat(f, t, n))
-        return struct
+                raise M.MoeError(M.STATUS_CODE["MOE_ERR_MISSING_TENSOR"], f"weights {f}")
+            if t.dtype is not dtype or t.get_device() != index or t.numel() != n or not t.is_contiguous():
+                self._flat(f, t, n)  # says what is wrong
+            setattr(w, f, t.data_ptr())
+        return w
 
     def _routing(self, routing, T: int):
         if routing is None:
@@ -267,10 +277,10 @@ class GatedFfn(_Operator):
                 return self.forward(u, weights, routing, residual, keep, out)
         T = u.shape[0]
         up, ldu = self._rows("u", u, self.K)
-        w = self._planes(M.MoeWeights(), weights, "weights")
+        w = self._planes(weights)
         off, slots, wts = self._routing(routing, T)
         rp, ldr = (None, 0) if residual is None else self._rows("residual", residual, self.K, T)
-        y = self._empty(T, self.K) if out is None else out
+        y = self._like(u, T, self.K) if out is None else out
         yp, ldy = self._rows("out", y, self.K, T)
         pre = self._empty(T * self.k, 2 * self.I) if keep else None
         ws, n = self._workspace(self.lib.moe_ffn_workspace_size, self._cfg, T, 0)
@@ -288,15 +298,15 @@ class GatedFfn(_Operator):
         T = u.shape[0]
         gp, ldg = self._rows("dy", dy, self.K, T)
         up, ldu = self._rows("u", u, self.K)
-        w = self._planes(M.MoeWeights(), weights, "weights")
+        w = self._planes(weights)
         off, slots, wts = self._routing(routing, T)
         pp = self._flat("pre", pre, T * self.k * 2 * self.I)
-        grads = {f: self._empty(*s) for f, s in self.shapes.items()}
+        grads = {f: self._like(weights[f], *s) for f, s in self.shapes.items()}
         g = MoeFfnGrads()
         for f, t in grads.items():
             setattr(g, f, t.data_ptr())
         dwt = None if off is None else self._empty(T, self.k, dtype=torch.float32)
-        du = self._empty(T, self.K) if input_grad else None
+        du = self._like(u, T, self.K) if input_grad else None
         ws, n = self._workspace(self.lib.moe_ffn_workspace_size, self._cfg, T, 1)
         M._check(self.lib.moe_ffn_backward(self._cfg, ctypes.byref(w), up, ldu, T, off, slots, wts, pp,
                                            gp, ldg, _p(du), self.K, _p(dwt), ctypes.byref(g), _p(ws), n,
@@ -329,7 +339,7 @@ class Norm(_Operator):
         xp, ldx = self._rows("x", x, H)
         wp = self._flat("w", w, H)
         bp = None if bias is None else self._flat("bias", bias, H)
-        y = self._empty(T, H) if out is None else out
+        y = self._like(x, T, H) if out is None else out
         yp, ldy = self._rows("out", y, H, T)
         stats = self._empty(T, 2, dtype=torch.float32)
         M._check(self.lib.moe_norm_forward(self._desc, xp, ldx, wp, bp, T, yp, ldy, stats.data_ptr(),
@@ -351,9 +361,9 @@ class Norm(_Operator):
         xp, ldx = self._rows("x", x, H)
         wp = self._flat("w", w, H)
         sp = self._flat("stats", stats, 2 * T, torch.float32)
-        dx = self._empty(T, H) if input_grad else None
-        dw = self._empty(H)
-        db = self._empty(H) if bias_grad else None
+        dx = self._like(x, T, H) if input_grad else None
+        dw = self._like(w, H)
+        db = self._like(w, H) if bias_grad else None
         ws, n = self._workspace(self.lib.moe_norm_workspace_size, self._desc, T, 1)
         M._check(self.lib.moe_norm_backward(self._desc, gp, ldg, xp, ldx, wp, sp, T, _p(dx), H,
                                             _p(dw), _p(db), _p(ws), n, self._stream()), "moe_norm_backward")
