@@ -28,6 +28,34 @@ __device__ __forceinline__ float block_sum(float v, float* sm) {
     return s;
 }
 
+// Two f32 operations per instruction (sm_100): the backward pass is bound by issue slots as
+// much as by HBM.
+__device__ __forceinline__ uint64_t bits2(float2 a) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+    return r;
+}
+__device__ __forceinline__ float2 pair2(uint64_t a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return pair2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return pair2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return pair2(r);
+}
+
 // Sums of two values over the tpr threads of a row group (a multiple of 32), through red[warp].
 // One block barrier; calls in a row alternate between two arrays.
 __device__ __forceinline__ void group_sum2(float& x, float& y, int tpr, float2* red) {
@@ -184,7 +212,11 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_backward_rows_kernel(con
     if (threadIdx.x == 0)
         for (int i = 0; i < stages; ++i)
             if (blockIdx.x + int64_t(i) * gridDim.x < groups) fill(blockIdx.x + int64_t(i) * gridDim.x, i);
-    float aw[kVpt][V] = {}, ab[kVpt][V] = {};
+    float2 aw[kVpt][V / 2], ab[kVpt][V / 2];
+#pragma unroll
+    for (int i = 0; i < kVpt; ++i)
+#pragma unroll
+        for (int q = 0; q < V / 2; ++q) aw[i][q] = ab[i][q] = make_float2(0.f, 0.f);
     int st = 0, it = 0;
     uint32_t phase = 0;
     for (int64_t grp = blockIdx.x; grp < groups; grp += gridDim.x, ++it) {
@@ -200,7 +232,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_backward_rows_kernel(con
         const uint4* sx = reinterpret_cast<const uint4*>(ring + st * stage_bytes + g * 2 * row_bytes);
         const uint4* sd = reinterpret_cast<const uint4*>(ring + st * stage_bytes + g * 2 * row_bytes + row_bytes);
         uint4 xv[kVpt], dv[kVpt];
-        float s1 = 0.f, s2 = 0.f;
+        float2 t1 = make_float2(0.f, 0.f), t2 = t1;  // sums of dy w and dy w (x - mean)
 #pragma unroll
         for (int i = 0; i < kVpt; ++i) {
             const int c = c0 + i * tpr;
@@ -212,15 +244,19 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_backward_rows_kernel(con
             unpack_vec<T>(dv[i], d);
             unpack_vec<T>(sw[c], w);
 #pragma unroll
-            for (int q = 0; q < V; ++q) {
-                const float xh = (f[q] - mean) * rstd;
-                aw[i][q] = fmaf(d[q], xh, aw[i][q]);
-                if (LAYER) ab[i][q] += d[q];
-                const float dw = d[q] * w[q];
-                if (LAYER) s1 += dw;
-                s2 = fmaf(dw, xh, s2);
+            for (int q = 0; q < V; q += 2) {
+                const float2 x2 = add2(make_float2(f[q], f[q + 1]), make_float2(-mean, -mean));
+                const float2 d2 = make_float2(d[q], d[q + 1]);
+                const float2 g2 = mul2(d2, make_float2(w[q], w[q + 1]));
+                aw[i][q / 2] = fma2(mul2(d2, make_float2(rstd, rstd)), x2, aw[i][q / 2]);
+                if (LAYER) {
+                    ab[i][q / 2] = add2(ab[i][q / 2], d2);
+                    t1 = add2(t1, g2);
+                }
+                t2 = fma2(g2, x2, t2);
             }
         }
+        float s1 = t1.x + t1.y, s2 = (t2.x + t2.y) * rstd;
         group_sum2(s1, s2, tpr, red[it & 1]);
         // every thread has read the stage: bring its next rows
         if (threadIdx.x == 0 && grp + int64_t(stages) * gridDim.x < groups) fill(grp + int64_t(stages) * gridDim.x, st);
@@ -229,8 +265,8 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_backward_rows_kernel(con
             phase ^= 1u;
         }
         if (!live || !a.dx) continue;
-        s1 /= float(a.H);
-        s2 /= float(a.H);
+        // dx = rstd g - rstd mean(g) - (x - mean) rstd^2 mean(g xh)
+        const float k1 = -rstd * (s1 / float(a.H)), k2 = -rstd * rstd * (s2 / float(a.H));
         T* dx = static_cast<T*>(a.dx) + t * a.lddx;
 #pragma unroll
         for (int i = 0; i < kVpt; ++i) {
@@ -241,7 +277,13 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_backward_rows_kernel(con
             unpack_vec<T>(dv[i], d);
             unpack_vec<T>(sw[c], w);
 #pragma unroll
-            for (int q = 0; q < V; ++q) f[q] = rstd * (d[q] * w[q] - s1 - (f[q] - mean) * rstd * s2);
+            for (int q = 0; q < V; q += 2) {
+                const float2 x2 = add2(make_float2(f[q], f[q + 1]), make_float2(-mean, -mean));
+                const float2 g2 = mul2(make_float2(d[q], d[q + 1]), make_float2(w[q], w[q + 1]));
+                const float2 o = fma2(x2, make_float2(k2, k2), fma2(g2, make_float2(rstd, rstd), make_float2(k1, k1)));
+                f[q] = o.x;
+                f[q + 1] = o.y;
+            }
             store_vec(dx + c * V, f);
         }
     }
@@ -256,10 +298,11 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_backward_rows_kernel(con
                 const int c = c0 + i * tpr;
                 if (c >= n) break;
 #pragma unroll
-                for (int q = 0; q < V; ++q) {
-                    float *pw = acc + c * V + q, *pb = acc + a.H + c * V + q;
-                    *pw = j ? *pw + aw[i][q] : aw[i][q];
-                    if (LAYER) *pb = j ? *pb + ab[i][q] : ab[i][q];
+                for (int q = 0; q < V / 2; ++q) {
+                    float2* pw = reinterpret_cast<float2*>(acc + c * V + 2 * q);
+                    float2* pb = reinterpret_cast<float2*>(acc + a.H + c * V + 2 * q);
+                    *pw = j ? add2(*pw, aw[i][q]) : aw[i][q];
+                    if (LAYER) *pb = j ? add2(*pb, ab[i][q]) : ab[i][q];
                 }
             }
         }

@@ -1,9 +1,9 @@
 // train_simt.cu -- matrix products on the CUDA cores, for f32 operands (the tensor cores have
 // no 32-bit product) in every operand order the training operators need.
 //
-// 64 x 64 outputs per block, 16 reduction steps per shared-memory stage, a 4 x 4 register tile
-// per thread; the next stage's operands are loaded into registers while the current one is
-// multiplied. The tile is small because f32 blocks are small (a launch of few tiles leaves
+// 64 x 64 outputs per block, 32 reduction steps per shared-memory stage, a 4 x 4 register tile
+// per thread; the next stage's operands are loaded into registers (16-byte vectors) while the
+// current one is multiplied. The tile is small because f32 blocks are small (a launch of few tiles leaves
 // SMs idle sooner than it meets the FMA rate).
 #include <algorithm>
 
@@ -13,41 +13,45 @@ namespace moe {
 
 namespace {
 
-constexpr int kBM = 64, kBN = 64, kBR = 16, kThreads = 256;
-
-// One operand tile [64 rows (m or n)][16 r] as 4 values per thread. RMAJOR: memory rows are
-// reduction indices (element (i, r) at p[r * ld + i]), else (i, r) at p[i * ld + r].
-template <typename T, bool RMAJOR>
-__device__ __forceinline__ void fetch(float (&v)[4], const T* p, int64_t ld, int64_t i0, int64_t ni, int64_t r0,
-                                      int64_t r1) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int idx = threadIdx.x + q * kThreads;
-        const int i = RMAJOR ? idx % 64 : idx / kBR, r = RMAJOR ? idx / 64 : idx % kBR;
-        const int64_t gi = i0 + i, gr = r0 + r;
-        v[q] = gi < ni && gr < r1 ? to_f<T>(p[RMAJOR ? gr * ld + gi : gi * ld + gr]) : 0.0f;
-    }
-}
-template <bool RMAJOR>
-__device__ __forceinline__ void stash(float (&sm)[kBR][64 + 4], const float (&v)[4]) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int idx = threadIdx.x + q * kThreads;
-        const int i = RMAJOR ? idx % 64 : idx / kBR, r = RMAJOR ? idx / 64 : idx % kBR;
-        sm[r][i] = v[q];
-    }
-}
+constexpr int kBM = 64, kBN = 64, kBR = 32, kThreads = 256;
 
 struct Shared {
     float a[kBR][kBM + 4], b[kBR][kBN + 4];
 };
 
+// One operand tile [64 i][32 r], two 16-byte vectors per thread. RMAJOR: memory rows are
+// reduction indices (vectors along i), else vectors along r. at(i, r) gives a vector's address,
+// or null outside the operand (row lengths are multiples of 4, so a vector is in or out whole).
+template <bool RMAJOR, typename At>
+__device__ __forceinline__ void fetch(float4 (&v)[2], At at) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int idx = threadIdx.x + q * kThreads;
+        const int i = RMAJOR ? idx % 16 * 4 : idx / 8, r = RMAJOR ? idx / 16 : idx % 8 * 4;
+        const float* p = at(i, r);
+        v[q] = p ? *reinterpret_cast<const float4*>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+}
+template <bool RMAJOR>
+__device__ __forceinline__ void stash(float (&sm)[kBR][64 + 4], const float4 (&v)[2]) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int idx = threadIdx.x + q * kThreads;
+        if (RMAJOR) {
+            *reinterpret_cast<float4*>(&sm[idx / 16][idx % 16 * 4]) = v[q];
+        } else {
+            const int i = idx / 8, r = idx % 8 * 4;
+            sm[r][i] = v[q].x;
+            sm[r + 1][i] = v[q].y;
+            sm[r + 2][i] = v[q].z;
+            sm[r + 3][i] = v[q].w;
+        }
+    }
+}
+
 template <int KIND>
-__device__ void simt_tile(const GemmArgs& a, int64_t m0, int64_t n0, int z, Shared& sh) {
-    using T = float;
+__device__ __forceinline__ void simt_tile(const GemmArgs& a, int64_t m0, int64_t n0, int z, Shared& sh) {
     constexpr bool AR = KIND == kTN, BR = KIND != kNT;  // operand rows are reduction indices
-    auto& sa = sh.a;
-    auto& sb = sh.b;
     const RowPlan& p = a.plan;
     const bool grouped = p.offsets != nullptr;
     int e = 0;
@@ -63,50 +67,35 @@ __device__ void simt_tile(const GemmArgs& a, int64_t m0, int64_t n0, int z, Shar
         if (m0 >= M) return;
         e = expert_of_row(p.poff, p.E, int(m0));
     }
-    const T* A = static_cast<const T*>(a.a);
-    const T* B = static_cast<const T*>(a.b) + int64_t(e) * (KIND == kTN ? 0 : a.sb);
-    const T* B1 = a.b1 ? static_cast<const T*>(a.b1) + int64_t(e) * a.sb : nullptr;
-    // operand B's pointer and index shift for reduction step r (kNN split) / column n (kNT split):
-    // splits are multiples of the tile only by chance, so the choice is made per element
-    float va[4], vb[4], acc[4][4] = {};
-    auto fetch_b = [&](int64_t r) {
-        if (KIND == kNN && a.split) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int idx = threadIdx.x + q * kThreads;
-                const int64_t gi = n0 + idx % 64, gr = r + idx / 64;
-                vb[q] = 0.f;
-                if (gi < a.N && gr < R) vb[q] = to_f<T>(gr < a.split ? B[gr * a.ldb + gi] : B1[(gr - a.split) * a.ldb + gi]);
-            }
-        } else if (KIND == kNT && a.split) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int idx = threadIdx.x + q * kThreads;
-                const int64_t gi = n0 + idx / kBR, gr = r + idx % kBR;
-                vb[q] = 0.f;
-                if (gi < a.N && gr < R) vb[q] = to_f<T>(gi < a.split ? B[gi * a.ldb + gr] : B1[(gi - a.split) * a.ldb + gr]);
-            }
-        } else {
-            fetch<T, BR>(vb, B, a.ldb, n0, a.N, r, R);
-        }
+    const float* A = static_cast<const float*>(a.a);
+    const float* B = static_cast<const float*>(a.b) + int64_t(e) * (KIND == kTN ? 0 : a.sb);
+    const float* B1 = a.b1 ? static_cast<const float*>(a.b1) + int64_t(e) * a.sb : nullptr;
+    float4 va[2], vb[2];
+    auto fetch_ab = [&](int64_t rb) {
+        fetch<AR>(va, [&](int i, int r) -> const float* {
+            const int64_t gi = m0 + i, gr = rb + r;
+            return gi < M && gr < R ? A + (AR ? gr * a.lda + gi : gi * a.lda + gr) : nullptr;
+        });
+        fetch<BR>(vb, [&](int i, int r) -> const float* {
+            const int64_t gi = n0 + i, gr = rb + r;
+            if (gi >= a.N || gr >= R) return nullptr;
+            if (KIND == kNN && a.split && gr >= a.split) return B1 + (gr - a.split) * a.ldb + gi;
+            if (KIND == kNT && a.split && gi >= a.split) return B1 + (gi - a.split) * a.ldb + gr;
+            return B + (BR ? gr * a.ldb + gi : gi * a.ldb + gr);
+        });
     };
+    float acc[4][4] = {};
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    if (r0 < R) {
-        fetch<T, AR>(va, A, a.lda, m0, M, r0, R);
-        fetch_b(r0);
-    }
+    if (r0 < R) fetch_ab(r0);
     for (int64_t r = r0; r < R; r += kBR) {
-        stash<AR>(sa, va);
-        stash<BR>(sb, vb);
+        stash<AR>(sh.a, va);
+        stash<BR>(sh.b, vb);
         __syncthreads();
-        if (r + kBR < R) {
-            fetch<T, AR>(va, A, a.lda, m0, M, r + kBR, R);
-            fetch_b(r + kBR);
-        }
-#pragma unroll
+        if (r + kBR < R) fetch_ab(r + kBR);
+#pragma unroll 8
         for (int q = 0; q < kBR; ++q) {
-            const float4 x = *reinterpret_cast<const float4*>(&sa[q][ty * 4]);
-            const float4 y = *reinterpret_cast<const float4*>(&sb[q][tx * 4]);
+            const float4 x = *reinterpret_cast<const float4*>(&sh.a[q][ty * 4]);
+            const float4 y = *reinterpret_cast<const float4*>(&sh.b[q][tx * 4]);
             const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -115,34 +104,41 @@ __device__ void simt_tile(const GemmArgs& a, int64_t m0, int64_t n0, int z, Shar
         }
         __syncthreads();
     }
+    const int64_t n = n0 + tx * 4;
+    if (n >= a.N) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int64_t m = m0 + ty * 4 + i;
-        if (m >= M) continue;
+        if (m >= M) break;
+        float o[4] = {acc[i][0], acc[i][1], acc[i][2], acc[i][3]};
+        if (KIND == kTN) {
+            float* d = static_cast<float*>(a.split && m >= a.split ? a.out1 : a.out) + int64_t(e) * a.so +
+                       (a.split && m >= a.split ? m - a.split : m) * a.ldo + n;
+            store_vec(d, o);
+            continue;
+        }
+        if (a.bias) {
+            const bool second = a.split && n >= a.split;
+            float b[4];
+            load_vec(static_cast<const float*>(second ? a.bias1 : a.bias) + int64_t(e) * a.sbias + (second ? n - a.split : n), b);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] += b[j];
+        }
+        if (a.pre) store_vec(static_cast<float*>(a.pre) + m * a.ldp + n, o);
         float rs = 1.0f;
-        if (KIND != kTN && a.row_scale) {
+        if (a.row_scale) {
             const int slot = p.row_slot[m];
             rs = slot < 0 ? 0.0f : a.row_scale[slot];
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t n = n0 + tx * 4 + j;
-            if (n >= a.N) continue;
-            float z = acc[i][j];
-            if (KIND == kTN) {
-                T* o = a.split && m >= a.split ? static_cast<T*>(a.out1) + int64_t(e) * a.so + (m - a.split) * a.ldo
-                                               : static_cast<T*>(a.out) + int64_t(e) * a.so + m * a.ldo;
-                o[n] = from_f<T>(z);
-                continue;
-            }
-            if (a.bias)
-                z += a.split && n >= a.split ? to_f<T>(static_cast<const T*>(a.bias1)[int64_t(e) * a.sbias + n - a.split])
-                                             : to_f<T>(static_cast<const T*>(a.bias)[int64_t(e) * a.sbias + n]);
-            if (a.pre) static_cast<T*>(a.pre)[m * a.ldp + n] = from_f<T>(z);
-            z = linear_act<false>(a.act, z) * rs;
-            if (a.residual) z += to_f<T>(static_cast<const T*>(a.residual)[m * a.ldr + n]);
-            static_cast<T*>(a.out)[m * a.ldo + n] = z;
+        for (int j = 0; j < 4; ++j) o[j] = linear_act<false>(a.act, o[j]) * rs;
+        if (a.residual) {
+            float b[4];
+            load_vec(static_cast<const float*>(a.residual) + m * a.ldr + n, b);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] += b[j];
         }
+        store_vec(static_cast<float*>(a.out) + m * a.ldo + n, o);
     }
 }
 
@@ -153,6 +149,9 @@ struct Simt {
     int n;
 };
 
+// FWD: every problem is kNT; else kNN and kTN (one kernel per pass keeps its code small: a tiny
+// launch spends much of its time fetching instructions).
+template <bool FWD>
 __global__ void __launch_bounds__(kThreads) simt_gemm_kernel(const __grid_constant__ Simt S) {
     __shared__ Shared sh;
     int64_t t = blockIdx.x;
@@ -163,7 +162,7 @@ __global__ void __launch_bounds__(kThreads) simt_gemm_kernel(const __grid_consta
     const int64_t mt = t % S.tx[i], r = t / S.tx[i];
     const int nt = int(r % S.ty[i]), z = int(r / S.ty[i]);
     const GemmArgs& a = S.p[i];
-    if (a.kind == kNT) simt_tile<kNT>(a, mt * kBM, int64_t(nt) * kBN, z, sh);
+    if constexpr (FWD) simt_tile<kNT>(a, mt * kBM, int64_t(nt) * kBN, z, sh);
     else if (a.kind == kNN) simt_tile<kNN>(a, mt * kBM, int64_t(nt) * kBN, z, sh);
     else simt_tile<kTN>(a, mt * kBM, int64_t(nt) * kBN, z, sh);
 }
@@ -184,7 +183,8 @@ cudaError_t launch_simt_gemm(const GemmArgs* a, int n, cudaStream_t s) {
         S.end[i] = tiles;
     }
     if (tiles >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-    simt_gemm_kernel<<<unsigned(tiles), kThreads, 0, s>>>(S);
+    if (a[0].kind == kNT) simt_gemm_kernel<true><<<unsigned(tiles), kThreads, 0, s>>>(S);
+    else simt_gemm_kernel<false><<<unsigned(tiles), kThreads, 0, s>>>(S);
     return cudaGetLastError();
 }
 

@@ -205,6 +205,32 @@ __device__ __forceinline__ void store_rows(uint8_t* sm, int lane, const uint4 (&
     }
     __syncwarp();
 }
+// Rows of 128 bytes in the same 2 KB, 16 rows at a time (piece c of row r at c ^ (r % 8)): whole
+// cache lines, half the write requests.
+__device__ __forceinline__ void store_lines(uint8_t* sm, int lane, const uint4 (&lo)[4], const uint4 (&hi)[4], void* base,
+                                            int64_t ld_bytes, int rows, int bytes) {
+    const int c = lane & 7;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if ((lane >> 4) == h) {
+            const int r = lane & 15;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                *reinterpret_cast<uint4*>(sm + r * 128 + ((i ^ (r & 7)) << 4)) = lo[i];
+                *reinterpret_cast<uint4*>(sm + r * 128 + (((4 + i) ^ (r & 7)) << 4)) = hi[i];
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 4 + (lane >> 3);
+            const uint4 x = *reinterpret_cast<const uint4*>(sm + r * 128 + ((c ^ (r & 7)) << 4));
+            if (h * 16 + r < rows && c * 16 < bytes)
+                *reinterpret_cast<uint4*>(static_cast<char*>(base) + (h * 16 + r) * ld_bytes + c * 16) = x;
+        }
+        __syncwarp();
+    }
+}
 // Reading them: fetch issues the loads (rows and bytes past the limits give zeros), turn hands
 // each lane its row.
 __device__ __forceinline__ void fetch_rows(int lane, uint4 (&x)[4], const void* base, int64_t ld_bytes, int rows,
@@ -853,9 +879,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                 if (t.nk > 0) release();
                 if (rows <= 0) return true;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 4; c += 2) {
                     const int col = t.n0 + 128 * ch + 32 * c;
-                    store_rows(sm, lane, w[c], ob + col, P.ldo * 2, rows, (P.N - col) * 2);
+                    store_lines(sm, lane, w[c], w[c + 1], ob + col, P.ldo * 2, rows, (P.N - col) * 2);
                 }
                 }
             } else {
@@ -894,14 +920,15 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                         for (int j = 0; j < 32; ++j) f[j] += z[j];
                     }
                     if (P.out_f32) {
+                        uint4 hi[4];
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-#pragma unroll
-                            for (int p = 0; p < 4; ++p)
-                                w[p] = make_uint4(__float_as_uint(f[16 * b + 4 * p]), __float_as_uint(f[16 * b + 4 * p + 1]),
-                                                  __float_as_uint(f[16 * b + 4 * p + 2]), __float_as_uint(f[16 * b + 4 * p + 3]));
-                            store_rows(sm, lane, w, ob + (col + 16 * b) * 4, P.ldo * 4, vrows, 2 * bytes - 64 * b);
+                        for (int p = 0; p < 4; ++p) {
+                            w[p] = make_uint4(__float_as_uint(f[4 * p]), __float_as_uint(f[4 * p + 1]),
+                                              __float_as_uint(f[4 * p + 2]), __float_as_uint(f[4 * p + 3]));
+                            hi[p] = make_uint4(__float_as_uint(f[16 + 4 * p]), __float_as_uint(f[16 + 4 * p + 1]),
+                                               __float_as_uint(f[16 + 4 * p + 2]), __float_as_uint(f[16 + 4 * p + 3]));
                         }
+                        store_lines(sm, lane, w, hi, ob + col * 4, P.ldo * 4, vrows, 2 * bytes);
                     } else {
                         pack_row(f, w);
                         store_rows(sm, lane, w, ob + col * 2, P.ldo * 2, vrows, bytes);
