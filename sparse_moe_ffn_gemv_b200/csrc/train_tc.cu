@@ -1117,14 +1117,22 @@ void set_bands(TcTrain& P, int n, int other) {
     P.d_tail = fast_div(std::max(1, n % P.band));
 }
 
-// Row tiles at most, and the dense problem's bands (as many row tiles as, with every column
-// block, fill the GPU: the tiles running together share both operands in L2).
+// Blocks of a band: with every block of the other kind they should fill the GPU, and where
+// those are many, the tiles running together should be about square, so that they share both
+// operands in L2.
+int band_of(int n, int other, int conc) {
+    int b = std::max(1, conc / std::max(1, other));
+    while (b * b < conc) ++b;
+    return std::min(n, b);
+}
+
+// Row tiles at most, and the dense problem's bands.
 int64_t row_grid(TcTrain& P, const RowPlan& p, bool pair) {
     const int BM = pair ? 256 : 128;
     P.m_blocks = int(p.offsets ? blocks_of(p.max_rows, BM) + (pair ? std::min<int64_t>(p.E, p.S) : 0)
                                : blocks_of(p.T, BM));
     const int conc = pair ? sms() / 2 : sms();
-    P.band = std::max(1, std::min(P.m_blocks, conc / std::max(1, P.n_blocks)));
+    P.band = band_of(P.m_blocks, P.n_blocks, conc);
     set_bands(P, P.m_blocks, P.n_blocks);
     return int64_t(P.m_blocks) * P.n_blocks;
 }
@@ -1150,7 +1158,7 @@ cudaError_t launch_tc_gemm_train(const GemmArgs& a, cudaStream_t s) {
         const bool pair = tiles256 >= sms() / 2;
         P.m_blocks = int(blocks_of(P.mrows, pair ? 256 : 128));
         // an expert's tiles: one column block at a time; dense: as many as fill the GPU with every row block
-        P.band = grouped ? 1 : std::max(1, std::min(P.n_blocks, (pair ? sms() / 2 : sms()) / (P.m_blocks * P.halves)));
+        P.band = grouped ? 1 : band_of(P.n_blocks, P.m_blocks * P.halves, pair ? sms() / 2 : sms());
         set_bands(P, P.n_blocks, P.m_blocks * P.halves);
         P.d_tile = fast_div(int64_t(P.m_blocks) * P.halves * P.n_blocks);
         P.d_m = fast_div(P.m_blocks);
