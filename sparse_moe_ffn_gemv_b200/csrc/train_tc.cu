@@ -175,12 +175,7 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
 
 // Bounded wait; the clock starts when the wait does, so that a long launch is no timeout.
 __device__ __forceinline__ bool wait_bar(uint64_t* b, uint32_t parity) {
-    for (int i = 0; i < 64; ++i)
-        if (mbar_try(b, parity)) return true;
-    return mbar_wait(b, parity, gtimer() + kWaitNs);
-}
-__device__ __forceinline__ bool wait_bar_sleep(uint64_t* b, uint32_t parity) {
-    if (mbar_try(b, parity)) return true;
+    if (mbar_try(b, parity) || mbar_try(b, parity)) return true;
     return mbar_wait_sleep(b, parity, gtimer() + kWaitNs);
 }
 
@@ -388,17 +383,40 @@ __device__ __forceinline__ Tile tile_of(const TcTrain& P, const Tables& tb, int 
     return t;
 }
 
+// TMA loads, completing on this CTA's barrier or (PAIR) on the leader's at its cluster address.
+// No L2 policy: createpolicy's evict_normal marks lines for demotion once hit, which had the
+// tiles of a band read 1.5 GB from HBM where 0.9 GB do (8192^3).
 template <bool PAIR>
 __device__ __forceinline__ void load3(void* dst, const CUtensorMap* m, uint64_t* bar, uint32_t bar_c, int c0, int c1,
-                                      int c2, uint64_t pol) {
-    if constexpr (PAIR) tma_3d_pair(dst, m, bar_c, c0, c1, c2, pol);
-    else tma_3d(dst, m, bar, c0, c1, c2, pol);
+                                      int c2) {
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(su32(dst)),
+            "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_c), "r"(c0), "r"(c1), "r"(c2)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(su32(dst)),
+            "l"(reinterpret_cast<uint64_t>(m)), "r"(su32(bar)), "r"(c0), "r"(c1), "r"(c2)
+            : "memory");
 }
 template <bool PAIR>
 __device__ __forceinline__ void load4(void* dst, const CUtensorMap* m, uint64_t* bar, uint32_t bar_c, int c0, int c1,
-                                      int c2, int c3, uint64_t pol) {
-    if constexpr (PAIR) tma_4d_pair(dst, m, bar_c, c0, c1, c2, c3, pol);
-    else tma_4d(dst, m, bar, c0, c1, c2, c3, pol);
+                                      int c2, int c3) {
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(su32(dst)),
+            "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_c), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(su32(dst)),
+            "l"(reinterpret_cast<uint64_t>(m)), "r"(su32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+            : "memory");
 }
 
 // SPLIT: the CTAs of a cluster share one tile, each a part of its reduction; their accumulators
@@ -492,7 +510,6 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
         // ------------------------------------------------------------ TMA producer
         if (lane == 0) {
             uint32_t stage = 0, phase = 0, armed = 0, last = 0;
-            const uint64_t pol = policy_evict_normal();
             for (int idx = tile0; idx < total && !gave_up; idx += tstep) {
                 const Tile t = tile_of<KIND, EPI, PAIR>(P, tb, idx);
                 const int arow = int(t.row0) + 128 * int(crank);
@@ -510,35 +527,35 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                     const int kc = (kb - half * P.nk_half) * kBR;
                     if constexpr (KIND == kTN) {
                         const int r = int(t.r0) + kb * kBR;
-                        load3<PAIR>(sa, &P.a, &full[stage], fb, arow, t.half, r, pol);
-                        load3<PAIR>(sa + 8192, &P.a, &full[stage], fb, arow + 64, t.half, r, pol);
+                        load3<PAIR>(sa, &P.a, &full[stage], fb, arow, t.half, r);
+                        load3<PAIR>(sa + 8192, &P.a, &full[stage], fb, arow + 64, t.half, r);
                         const int nb = t.n0 + 128 * int(crank);
 #pragma unroll
                         for (int j = 0; j < S::B_BYTES / 8192; ++j)
-                            load3<PAIR>(sb + j * 8192, &P.b0, &full[stage], fb, nb + 64 * j, r, 0, pol);
+                            load3<PAIR>(sb + j * 8192, &P.b0, &full[stage], fb, nb + 64 * j, r, 0);
                     } else {
-                        load3<PAIR>(sa, &P.a, &full[stage], fb, kc, half, arow, pol);
+                        load3<PAIR>(sa, &P.a, &full[stage], fb, kc, half, arow);
                         if constexpr (KIND == kNN) {
                             const CUtensorMap* mb = half && P.b_split ? &P.b1 : &P.b0;
                             const int nb = t.n0 + 128 * int(crank);
 #pragma unroll
                             for (int j = 0; j < S::B_BYTES / 8192; ++j)
-                                load3<PAIR>(sb + j * 8192, mb, &full[stage], fb, nb + 64 * j, kc, t.e, pol);
+                                load3<PAIR>(sb + j * 8192, mb, &full[stage], fb, nb + 64 * j, kc, t.e);
                         } else if constexpr (S::GATEUP) {
                             // gate rows, then up rows; of a pair, CTA 0 gate and CTA 1 up
                             if constexpr (PAIR) {
-                                if (S::IL) load4<PAIR>(sb, &P.b0, &full[stage], fb, kc, int(crank), t.n0, t.e, pol);
-                                else load4<PAIR>(sb, crank ? &P.b1 : &P.b0, &full[stage], fb, kc, 0, t.n0, t.e, pol);
+                                if (S::IL) load4<PAIR>(sb, &P.b0, &full[stage], fb, kc, int(crank), t.n0, t.e);
+                                else load4<PAIR>(sb, crank ? &P.b1 : &P.b0, &full[stage], fb, kc, 0, t.n0, t.e);
                             } else {
-                                load4<PAIR>(sb, &P.b0, &full[stage], fb, kc, 0, t.n0, t.e, pol);
-                                if (S::IL) load4<PAIR>(sb + kABytes, &P.b0, &full[stage], fb, kc, 1, t.n0, t.e, pol);
-                                else load4<PAIR>(sb + kABytes, &P.b1, &full[stage], fb, kc, 0, t.n0, t.e, pol);
+                                load4<PAIR>(sb, &P.b0, &full[stage], fb, kc, 0, t.n0, t.e);
+                                if (S::IL) load4<PAIR>(sb + kABytes, &P.b0, &full[stage], fb, kc, 1, t.n0, t.e);
+                                else load4<PAIR>(sb + kABytes, &P.b1, &full[stage], fb, kc, 0, t.n0, t.e);
                             }
                         } else {
                             const int nb = t.n0 + 128 * int(crank);
 #pragma unroll
                             for (int j = 0; j < S::B_BYTES / kABytes; ++j)
-                                load4<PAIR>(sb + j * kABytes, &P.b0, &full[stage], fb, kc, 0, nb + 128 * j, t.e, pol);
+                                load4<PAIR>(sb + j * kABytes, &P.b0, &full[stage], fb, kc, 0, nb + 128 * j, t.e);
                         }
                     }
                     armed |= 1u << stage;
@@ -607,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
             const bool any = kb_begin(t) < kb_end(t);
             bool ok = true;
             if (any) {
-                ok = wait_bar_sleep(&acc_full[0], 0);
+                ok = wait_bar(&acc_full[0], 0);
                 if (!ok) set_status(P.status, MOE_ERR_DEVICE_TIMEOUT);
                 fence_after();
             }
@@ -674,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                 if (c0 < c1) fetch_pre(t, c0, vrows);
             if (!SPLIT && t.nk > 0) {
                 ++it;
-                if (!wait_bar_sleep(&acc_full[ab], ph)) {
+                if (!wait_bar(&acc_full[ab], ph)) {
                     set_status(P.status, MOE_ERR_DEVICE_TIMEOUT);
                     return false;
                 }
