@@ -219,29 +219,27 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_backward_rows_kernel(con
         for (int q = 0; q < V / 2; ++q) aw[i][q] = ab[i][q] = make_float2(0.f, 0.f);
     int st = 0, it = 0;
     uint32_t phase = 0;
+    auto stats_of = [&](int64_t grp) {
+        const int64_t t = grp * G + g;
+        return t < a.T ? __ldg(reinterpret_cast<const float2*>(a.cstats + 2 * t)) : make_float2(0.f, 0.f);
+    };
+    float2 ms = stats_of(blockIdx.x);
     for (int64_t grp = blockIdx.x; grp < groups; grp += gridDim.x, ++it) {
-        if (!mbar_wait(&full[st], phase, gtimer() + 2000000000ull)) break;
         const int64_t t = grp * G + g;
         const bool live = t < a.T;
-        float mean = 0.f, rstd = 0.f;
-        if (live) {
-            const float2 ms = __ldg(reinterpret_cast<const float2*>(a.cstats + 2 * t));
-            mean = ms.x;
-            rstd = ms.y;
-        }
+        const float mean = ms.x, rstd = ms.y;
+        ms = stats_of(grp + gridDim.x);  // of the next row, while this one is worked on
+        if (!mbar_try(&full[st], phase) && !mbar_wait(&full[st], phase, gtimer() + 2000000000ull)) break;
         const uint4* sx = reinterpret_cast<const uint4*>(ring + st * stage_bytes + g * 2 * row_bytes);
         const uint4* sd = reinterpret_cast<const uint4*>(ring + st * stage_bytes + g * 2 * row_bytes + row_bytes);
-        uint4 xv[kVpt], dv[kVpt];
         float2 t1 = make_float2(0.f, 0.f), t2 = t1;  // sums of dy w and dy w (x - mean)
 #pragma unroll
         for (int i = 0; i < kVpt; ++i) {
             const int c = c0 + i * tpr;
             if (!live || c >= n) break;
-            xv[i] = sx[c];
-            dv[i] = sd[c];
             float f[V], d[V], w[V];
-            unpack_vec<T>(xv[i], f);
-            unpack_vec<T>(dv[i], d);
+            unpack_vec<T>(sx[c], f);
+            unpack_vec<T>(sd[c], d);
             unpack_vec<T>(sw[c], w);
 #pragma unroll
             for (int q = 0; q < V; q += 2) {
@@ -258,8 +256,9 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_backward_rows_kernel(con
         }
         float s1 = t1.x + t1.y, s2 = (t2.x + t2.y) * rstd;
         group_sum2(s1, s2, tpr, red[it & 1]);
-        // every thread has read the stage: bring its next rows
-        if (threadIdx.x == 0 && grp + int64_t(stages) * gridDim.x < groups) fill(grp + int64_t(stages) * gridDim.x, st);
+        // every thread is done with the rows before these: bring that stage's next rows
+        const int64_t nxt = grp + int64_t(stages - 1) * gridDim.x;
+        if (threadIdx.x == 0 && it > 0 && nxt < groups) fill(nxt, st == 0 ? stages - 1 : st - 1);
         if (++st == stages) {
             st = 0;
             phase ^= 1u;
@@ -273,8 +272,8 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_backward_rows_kernel(con
             const int c = c0 + i * tpr;
             if (c >= n) break;
             float f[V], d[V], w[V];
-            unpack_vec<T>(xv[i], f);
-            unpack_vec<T>(dv[i], d);
+            unpack_vec<T>(sx[c], f);
+            unpack_vec<T>(sd[c], d);
             unpack_vec<T>(sw[c], w);
 #pragma unroll
             for (int q = 0; q < V; q += 2) {

@@ -13,32 +13,34 @@ namespace moe {
 
 namespace {
 
-constexpr int kBM = 64, kBN = 64, kBR = 32, kThreads = 256;
+constexpr int kBR = 32;
 
-struct Shared {
-    float a[kBR][kBM + 4], b[kBR][kBN + 4];
+// TD x TD threads, 4 x 4 outputs each.
+template <int TD> struct Shared {
+    float a[2][kBR][4 * TD + 4], b[2][kBR][4 * TD + 4];
 };
 
-// One operand tile [64 i][32 r], two 16-byte vectors per thread. RMAJOR: memory rows are
+// One operand tile [4 TD i][32 r] as V 16-byte vectors per thread. RMAJOR: memory rows are
 // reduction indices (vectors along i), else vectors along r. at(i, r) gives a vector's address,
 // or null outside the operand (row lengths are multiples of 4, so a vector is in or out whole).
-template <bool RMAJOR, typename At>
-__device__ __forceinline__ void fetch(float4 (&v)[2], At at) {
+template <int TD> constexpr int kVecs = 4 * TD * kBR / 4 / (TD * TD);
+template <int TD, bool RMAJOR, typename At>
+__device__ __forceinline__ void fetch(float4 (&v)[kVecs<TD>], At at) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int idx = threadIdx.x + q * kThreads;
-        const int i = RMAJOR ? idx % 16 * 4 : idx / 8, r = RMAJOR ? idx / 16 : idx % 8 * 4;
+    for (int q = 0; q < kVecs<TD>; ++q) {
+        const int idx = threadIdx.x + q * TD * TD;
+        const int i = RMAJOR ? idx % TD * 4 : idx / 8, r = RMAJOR ? idx / TD : idx % 8 * 4;
         const float* p = at(i, r);
         v[q] = p ? *reinterpret_cast<const float4*>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 }
-template <bool RMAJOR>
-__device__ __forceinline__ void stash(float (&sm)[kBR][64 + 4], const float4 (&v)[2]) {
+template <int TD, bool RMAJOR>
+__device__ __forceinline__ void stash(float (&sm)[kBR][4 * TD + 4], const float4 (&v)[kVecs<TD>]) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int idx = threadIdx.x + q * kThreads;
+    for (int q = 0; q < kVecs<TD>; ++q) {
+        const int idx = threadIdx.x + q * TD * TD;
         if (RMAJOR) {
-            *reinterpret_cast<float4*>(&sm[idx / 16][idx % 16 * 4]) = v[q];
+            *reinterpret_cast<float4*>(&sm[idx / TD][idx % TD * 4]) = v[q];
         } else {
             const int i = idx / 8, r = idx % 8 * 4;
             sm[r][i] = v[q].x;
@@ -49,8 +51,8 @@ __device__ __forceinline__ void stash(float (&sm)[kBR][64 + 4], const float4 (&v
     }
 }
 
-template <int KIND>
-__device__ __forceinline__ void simt_tile(const GemmArgs& a, int64_t m0, int64_t n0, int z, Shared& sh) {
+template <int TD, int KIND>
+__device__ __forceinline__ void simt_tile(const GemmArgs& a, int64_t m0, int64_t n0, int z, Shared<TD>& sh) {
     constexpr bool AR = KIND == kTN, BR = KIND != kNT;  // operand rows are reduction indices
     const RowPlan& p = a.plan;
     const bool grouped = p.offsets != nullptr;
@@ -70,13 +72,14 @@ __device__ __forceinline__ void simt_tile(const GemmArgs& a, int64_t m0, int64_t
     const float* A = static_cast<const float*>(a.a);
     const float* B = static_cast<const float*>(a.b) + int64_t(e) * (KIND == kTN ? 0 : a.sb);
     const float* B1 = a.b1 ? static_cast<const float*>(a.b1) + int64_t(e) * a.sb : nullptr;
-    float4 va[2], vb[2];
-    auto fetch_ab = [&](int64_t rb) {
-        fetch<AR>(va, [&](int i, int r) -> const float* {
+    // two stages of operands in registers ahead of the one in shared memory
+    float4 va[2][kVecs<TD>], vb[2][kVecs<TD>];
+    auto fetch_ab = [&](float4 (&xa)[kVecs<TD>], float4 (&xb)[kVecs<TD>], int64_t rb) {
+        fetch<TD, AR>(xa, [&](int i, int r) -> const float* {
             const int64_t gi = m0 + i, gr = rb + r;
             return gi < M && gr < R ? A + (AR ? gr * a.lda + gi : gi * a.lda + gr) : nullptr;
         });
-        fetch<BR>(vb, [&](int i, int r) -> const float* {
+        fetch<TD, BR>(xb, [&](int i, int r) -> const float* {
             const int64_t gi = n0 + i, gr = rb + r;
             if (gi >= a.N || gr >= R) return nullptr;
             if (KIND == kNN && a.split && gr >= a.split) return B1 + (gr - a.split) * a.ldb + gi;
@@ -85,24 +88,28 @@ __device__ __forceinline__ void simt_tile(const GemmArgs& a, int64_t m0, int64_t
         });
     };
     float acc[4][4] = {};
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    if (r0 < R) fetch_ab(r0);
-    for (int64_t r = r0; r < R; r += kBR) {
-        stash<AR>(sh.a, va);
-        stash<BR>(sh.b, vb);
-        __syncthreads();
-        if (r + kBR < R) fetch_ab(r + kBR);
+    const int ty = threadIdx.x / TD, tx = threadIdx.x % TD;
+    fetch_ab(va[0], vb[0], r0);
+    fetch_ab(va[1], vb[1], r0 + kBR);
+    for (int64_t r = r0; r < R; r += 2 * kBR) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            // one barrier per stage: the other buffer's readers are past the barrier before it
+            stash<TD, AR>(sh.a[h], va[h]);
+            stash<TD, BR>(sh.b[h], vb[h]);
+            __syncthreads();
+            fetch_ab(va[h], vb[h], r + (2 + h) * kBR);
 #pragma unroll 8
-        for (int q = 0; q < kBR; ++q) {
-            const float4 x = *reinterpret_cast<const float4*>(&sh.a[q][ty * 4]);
-            const float4 y = *reinterpret_cast<const float4*>(&sh.b[q][tx * 4]);
-            const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+            for (int q = 0; q < kBR; ++q) {
+                const float4 x = *reinterpret_cast<const float4*>(&sh.a[h][q][ty * 4]);
+                const float4 y = *reinterpret_cast<const float4*>(&sh.b[h][q][tx * 4]);
+                const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xs[i], ys[j], acc[i][j]);
+                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xs[i], ys[j], acc[i][j]);
+            }
         }
-        __syncthreads();
     }
     const int64_t n = n0 + tx * 4;
     if (n >= a.N) return;
@@ -151,9 +158,10 @@ struct Simt {
 
 // FWD: every problem is kNT; else kNN and kTN (one kernel per pass keeps its code small: a tiny
 // launch spends much of its time fetching instructions).
-template <bool FWD>
-__global__ void __launch_bounds__(kThreads) simt_gemm_kernel(const __grid_constant__ Simt S) {
-    __shared__ Shared sh;
+template <int TD, bool FWD>
+__global__ void __launch_bounds__(TD * TD) simt_gemm_kernel(const __grid_constant__ Simt S) {
+    __shared__ Shared<TD> sh;
+    constexpr int kBM = 4 * TD, kBN = 4 * TD;
     int64_t t = blockIdx.x;
     int i = 0;
     while (i < S.n - 1 && t >= S.end[i]) ++i;
@@ -162,9 +170,28 @@ __global__ void __launch_bounds__(kThreads) simt_gemm_kernel(const __grid_consta
     const int64_t mt = t % S.tx[i], r = t / S.tx[i];
     const int nt = int(r % S.ty[i]), z = int(r / S.ty[i]);
     const GemmArgs& a = S.p[i];
-    if constexpr (FWD) simt_tile<kNT>(a, mt * kBM, int64_t(nt) * kBN, z, sh);
-    else if (a.kind == kNN) simt_tile<kNN>(a, mt * kBM, int64_t(nt) * kBN, z, sh);
-    else simt_tile<kTN>(a, mt * kBM, int64_t(nt) * kBN, z, sh);
+    if constexpr (FWD) simt_tile<TD, kNT>(a, mt * kBM, int64_t(nt) * kBN, z, sh);
+    else if (a.kind == kNN) simt_tile<TD, kNN>(a, mt * kBM, int64_t(nt) * kBN, z, sh);
+    else simt_tile<TD, kTN>(a, mt * kBM, int64_t(nt) * kBN, z, sh);
+}
+
+template <int TD>
+cudaError_t launch_td(Simt& S, cudaStream_t s) {
+    constexpr int B = 4 * TD;
+    int64_t tiles = 0;
+    for (int i = 0; i < S.n; ++i) {
+        const GemmArgs& a = S.p[i];
+        const bool grouped = a.plan.offsets != nullptr;
+        const int64_t rows = a.kind == kTN ? a.M : grouped ? a.plan.max_rows : a.M;
+        S.tx[i] = int((rows + B - 1) / B);
+        S.ty[i] = (a.N + B - 1) / B;
+        tiles += int64_t(S.tx[i]) * S.ty[i] * (a.kind == kTN && grouped ? a.plan.E : 1);
+        S.end[i] = tiles;
+    }
+    if (tiles >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    if (S.p[0].kind == kNT) simt_gemm_kernel<TD, true><<<unsigned(tiles), TD * TD, 0, s>>>(S);
+    else simt_gemm_kernel<TD, false><<<unsigned(tiles), TD * TD, 0, s>>>(S);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -172,20 +199,14 @@ __global__ void __launch_bounds__(kThreads) simt_gemm_kernel(const __grid_consta
 cudaError_t launch_simt_gemm(const GemmArgs* a, int n, cudaStream_t s) {
     Simt S;
     S.n = n;
-    int64_t tiles = 0;
+    int64_t tiles = 0;  // of 64 x 64
     for (int i = 0; i < n; ++i) {
-        const bool grouped = a[i].plan.offsets != nullptr;
-        const int64_t rows = a[i].kind == kTN ? a[i].M : grouped ? a[i].plan.max_rows : a[i].M;
         S.p[i] = a[i];
-        S.tx[i] = int((rows + kBM - 1) / kBM);
-        S.ty[i] = (a[i].N + kBN - 1) / kBN;
-        tiles += int64_t(S.tx[i]) * S.ty[i] * (a[i].kind == kTN && grouped ? a[i].plan.E : 1);
-        S.end[i] = tiles;
+        const bool grouped = a[i].plan.offsets != nullptr;
+        const int64_t rows = a[i].kind != kTN && grouped ? a[i].plan.S : a[i].M;
+        tiles += ((rows + 63) / 64) * ((a[i].N + 63) / 64) * (a[i].kind == kTN && grouped ? a[i].plan.E : 1);
     }
-    if (tiles >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-    if (a[0].kind == kNT) simt_gemm_kernel<true><<<unsigned(tiles), kThreads, 0, s>>>(S);
-    else simt_gemm_kernel<false><<<unsigned(tiles), kThreads, 0, s>>>(S);
-    return cudaGetLastError();
+    return tiles >= 2 * 148 ? launch_td<16>(S, s) : launch_td<8>(S, s);
 }
 
 }  // namespace moe
