@@ -159,6 +159,7 @@ struct FfnWs {
     size_t rows_out;  // [rows, K] f32 slot rows of y or du (routed)
     size_t dh, dgu, hw, partial;
     size_t parts;     // [rows, dgated_parts] partial sums of dtopk_w (bf16, routed)
+    size_t bias_dot;  // [S] dy . down_b (bf16, routed, with biases)
     size_t total;
 };
 // The plan's sizes; offsets only says routed or dense here.
@@ -186,6 +187,7 @@ FfnWs ffn_ws(const FfnShape& f, bool backward) {
         L.up = c.take(f.rows * f.K * f.es);
         if (backward) L.dyp = c.take(f.rows * f.K * f.es);
         L.rows_out = c.take(f.rows * f.K * 4);
+        if (backward && !f32 && f.bias) L.bias_dot = c.take(f.S * 4);
         if (backward && !f32) L.parts = c.take(f.rows * dgated_parts(shape_plan(f), f.I, f.K) * 4);
     }
     if (backward) {
@@ -537,6 +539,10 @@ moe_status moe_ffn_backward(const moe_config* cfg, const moe_weights* w, const v
         ga.zero_pad = true;
         ga.src[1] = dy; ga.ld[1] = lddy; ga.dst[1] = at<void>(ws, L.dyp);
         ga.K = f.K; ga.es = f.es;
+        if (dtopk_w && f.bias && f.dtype == MOE_DTYPE_BF16) {
+            ga.down_b = w->down_b;
+            ga.bias_dot = at<float>(ws, L.bias_dot);
+        }
         MOE_CUDA(launch_gather_padded(ga, s));
         up = ga.dst[0];
         dyp = ga.dst[1];
@@ -562,6 +568,7 @@ moe_status moe_ffn_backward(const moe_config* cfg, const moe_weights* w, const v
     ga.dtopk_w = dtopk_w;
     ga.dyp = dyp;
     ga.down_b = f.bias ? w->down_b : nullptr;
+    if (dtopk_w && f.bias) ga.bias_dot = at<float>(ws, L.bias_dot);
     ga.K = f.K;
     if (f.dtype == MOE_DTYPE_F32) {
         g.out = at<void>(ws, L.dh); g.ldo = f.I;

@@ -44,6 +44,9 @@ struct GatherArgs {
     int K = 0;
     int es = 2;  // bytes per element
     bool zero_pad = false;  // the rows are reduced over (weight gradients)
+    // bf16, two sources: bias_dot[slot] = src[1] row . down_b[expert]
+    const void* down_b = nullptr;  // [E, K]
+    float* bias_dot = nullptr;
 };
 cudaError_t launch_gather_padded(const GatherArgs& a, cudaStream_t s);
 
@@ -137,6 +140,7 @@ struct GatedArgs {
     float* dtopk_w = nullptr;       // by slot
     const void* dyp = nullptr;      // [padded rows, K] with down bias
     const void* down_b = nullptr;   // [E, K]
+    const float* bias_dot = nullptr;  // bf16: dy . down_b by slot, in place of dyp and down_b
     int K = 0;
 };
 // f32: on the results of launch_simt_gemm.
@@ -147,7 +151,7 @@ cudaError_t launch_gated_backward(const GatedArgs& a, cudaStream_t s);
 cudaError_t launch_tc_gateup(const GemmArgs& g, const GatedArgs& ga, cudaStream_t s);
 cudaError_t launch_tc_dgated(const GemmArgs& g, const GatedArgs& ga, float* partial, cudaStream_t s);
 int dgated_parts(const RowPlan& p, int I, int64_t R);
-// dtopk_w[slot] = the row's partial sums (+ dyp . down_b), from GatedArgs' plan, dtopk_w, dyp, down_b, K.
+// dtopk_w[slot] = the row's partial sums (+ bias_dot), from GatedArgs' plan, dtopk_w, bias_dot.
 cudaError_t launch_dtopk(const GatedArgs& a, const float* partial, int parts, cudaStream_t s);
 
 // Column sums of each expert's rows: out[e, c] = sum_r x[r, c] (* topk_w[slot of r]).
