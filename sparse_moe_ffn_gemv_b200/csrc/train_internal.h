@@ -9,9 +9,9 @@
 namespace moe {
 
 // Routed rows live in a padded order: expert e's rows start at poff[e], a multiple of
-// kRowTile, so that no row tile holds rows of two experts and a reduction over an expert's
-// rows may run to the next multiple of the reduction block over rows that are zero.
-constexpr int kRowTile = 128;
+// kRowTile, so that no row tile holds rows of two experts. A reduction over an expert's rows
+// runs to the next multiple of kRowPad (the matrix instruction's depth), over rows that are zero.
+constexpr int kRowTile = 128, kRowPad = 16;
 
 inline int64_t round_rows(int64_t n) { return (n + kRowTile - 1) / kRowTile * kRowTile; }
 // Most padded rows of S slots over E experts.

@@ -22,82 +22,115 @@ __device__ __forceinline__ int row_of_slot(const RowPlan& p, int slot) {
     return r >= 0 && r < p.poff[p.E] && p.row_slot[r] == slot ? r : -1;
 }
 
-// Every block derives the padded order from the offsets itself (E <= 512: one scan in shared
-// memory), so that building the plan needs no launch of its own; block 0 writes it down.
+// The padded order, which every block derives from the offsets itself (E <= 512: one scan in
+// shared memory), so that building it needs no launch of its own; block 0 writes it down.
 // Offsets that are not a rising sequence within [0, S] give an empty plan and the status.
-// PLAN: rows with a slot are left to copy_tokens_kernel.
-template <bool PLAN>
-__global__ void __launch_bounds__(kGatherThreads) gather_padded_kernel(const GatherArgs a) {
-    __shared__ int32_t cnt[kPermE], start[kPermE], pad[kPermE + 1];
-    __shared__ int warp_tot[kGatherThreads / 32 + 1];
-    const RowPlan& p = a.plan;
+struct PlanSmem {
+    int32_t cnt[kPermE], start[kPermE], pad[kPermE + 1];
+    int warp_tot[kGatherThreads / 32 + 1];
+};
+__device__ int build_plan(const RowPlan& p, PlanSmem& sm) {
     const int tid = threadIdx.x;
     int bad = 0;
     for (int e = tid; e < p.E; e += kGatherThreads) {
         const int lo = p.offsets[e], hi = p.offsets[e + 1];
         bad |= lo < 0 || hi < lo || hi > p.S;
-        start[e] = lo;
-        cnt[e] = hi - lo;
+        sm.start[e] = lo;
+        sm.cnt[e] = hi - lo;
     }
     bad = __syncthreads_or(bad);
     for (int e = tid; e < p.E; e += kGatherThreads) {
-        if (bad) cnt[e] = start[e] = 0;
-        pad[e] = (cnt[e] + kRowTile - 1) / kRowTile * kRowTile;
+        if (bad) sm.cnt[e] = sm.start[e] = 0;
+        sm.pad[e] = (sm.cnt[e] + kRowTile - 1) / kRowTile * kRowTile;
     }
     __syncthreads();
-    const int total = block_exclusive_scan<kGatherThreads>(pad, p.E, warp_tot);
-    if (tid == 0) pad[p.E] = total;
+    const int total = block_exclusive_scan<kGatherThreads>(sm.pad, p.E, sm.warp_tot);
+    if (tid == 0) sm.pad[p.E] = total;
     if (blockIdx.x == 0) {
         for (int e = tid; e < p.E; e += kGatherThreads) {
-            p.poff[e] = pad[e];
-            p.uoff[e] = start[e];
+            p.poff[e] = sm.pad[e];
+            p.uoff[e] = sm.start[e];
         }
         if (tid == 0) {
             p.poff[p.E] = total;
-            p.uoff[p.E] = p.E ? start[p.E - 1] + cnt[p.E - 1] : 0;
+            p.uoff[p.E] = sm.start[p.E - 1] + sm.cnt[p.E - 1];
             if (bad) set_status(p.status, MOE_ERR_DEVICE_CHECK);
         }
     }
     __syncthreads();
-    const int lane = tid & 31;
+    return total;
+}
+// Slot of padded row r (-1: padding, or a slot id out of range), written down both ways.
+__device__ __forceinline__ int plan_row(const RowPlan& p, const PlanSmem& sm, int r, int e, bool write) {
+    const int i = r - sm.pad[e];
+    int slot = -1;
+    if (i < sm.cnt[e]) {
+        slot = p.sorted_slot[sm.start[e] + i];
+        if (slot < 0 || slot >= p.S) {
+            if (write) set_status(p.status, MOE_ERR_DEVICE_CHECK);
+            slot = -1;
+        }
+    }
+    if (write) {
+        p.row_slot[r] = slot;
+        if (slot >= 0) p.slot_row[slot] = r;
+    }
+    return slot;
+}
+__device__ __forceinline__ void zero_row(const GatherArgs& a, int r, int lane) {
+    const int64_t vpr = int64_t(a.K) * a.es / 16;
+    for (int j = 0; j < 2; ++j)
+        if (a.dst[j])
+            for (int64_t c = lane; c < vpr; c += 32) static_cast<uint4*>(a.dst[j])[int64_t(r) * vpr + c] = make_uint4(0, 0, 0, 0);
+}
+
+// Few rows: the plan and the copies in one launch, a warp per padded row. Padding is zeroed as
+// far as a reduction over the expert's rows reads; rows of dropped slots are zeros too.
+__global__ void __launch_bounds__(kGatherThreads) gather_padded_kernel(const GatherArgs a) {
+    __shared__ PlanSmem sm;
+    const RowPlan& p = a.plan;
+    const int total = build_plan(p, sm);
+    const int lane = threadIdx.x & 31;
     const int64_t vpr = int64_t(a.K) * a.es / 16;
     const int warps = gridDim.x * (kGatherThreads / 32);
-    for (int r = blockIdx.x * (kGatherThreads / 32) + (tid >> 5); r < total; r += warps) {
-        const int e = expert_of_row(pad, p.E, r);
-        const int i = r - pad[e];
-        int slot = -1;
-        if (i < cnt[e]) {
-            slot = p.sorted_slot[start[e] + i];
-            if (slot < 0 || slot >= p.S) {
-                if (lane == 0) set_status(p.status, MOE_ERR_DEVICE_CHECK);
-                slot = -1;
-            }
+    for (int r = blockIdx.x * (kGatherThreads / 32) + (threadIdx.x >> 5); r < total; r += warps) {
+        const int e = expert_of_row(sm.pad, p.E, r);
+        const int slot = plan_row(p, sm, r, e, lane == 0);
+        if (slot < 0) {
+            const int i = r - sm.pad[e];
+            if (i < sm.cnt[e] || (a.zero_pad && i < (sm.cnt[e] + kRowPad - 1) / kRowPad * kRowPad)) zero_row(a, r, lane);
+            continue;
         }
-        if (lane == 0) {
-            p.row_slot[r] = slot;
-            if (slot >= 0) p.slot_row[slot] = r;
-        }
-        // padding: zeros as far as a reduction over the expert's rows reads (the next multiple
-        // of 64); rows of dropped slots are zeros too
-        if (i >= cnt[e] && (!a.zero_pad || i >= (cnt[e] + 63) / 64 * 64)) continue;
-        if (PLAN && slot >= 0) continue;  // copy_tokens_kernel's
-        const int64_t t = slot < 0 ? 0 : slot / p.k;
+        const int64_t t = slot / p.k;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             if (!a.src[j]) continue;
             const uint4* s = reinterpret_cast<const uint4*>(static_cast<const char*>(a.src[j]) + t * a.ld[j] * a.es);
             uint4* d = static_cast<uint4*>(a.dst[j]) + int64_t(r) * vpr;
-            if (slot < 0) {
-                for (int c = lane; c < vpr; c += 32) d[c] = make_uint4(0, 0, 0, 0);
-            } else {
-                int c = lane;
-                for (; c + 96 < vpr; c += 128) {  // four vectors in flight per lane
-                    const uint4 v0 = __ldg(s + c), v1 = __ldg(s + c + 32), v2 = __ldg(s + c + 64), v3 = __ldg(s + c + 96);
-                    d[c] = v0; d[c + 32] = v1; d[c + 64] = v2; d[c + 96] = v3;
-                }
-                for (; c < vpr; c += 32) d[c] = __ldg(s + c);
+            int64_t c = lane;
+            for (; c + 96 < vpr; c += 128) {  // four vectors in flight per lane
+                const uint4 v0 = __ldg(s + c), v1 = __ldg(s + c + 32), v2 = __ldg(s + c + 64), v3 = __ldg(s + c + 96);
+                d[c] = v0; d[c + 32] = v1; d[c + 64] = v2; d[c + 96] = v3;
             }
+            for (; c < vpr; c += 32) d[c] = __ldg(s + c);
         }
+    }
+}
+
+// Many rows: the plan, a thread per padded row, and the zero rows; copy_tokens_kernel does the rest.
+__global__ void __launch_bounds__(kGatherThreads) plan_rows_kernel(const GatherArgs a) {
+    __shared__ PlanSmem sm;
+    const RowPlan& p = a.plan;
+    const int total = build_plan(p, sm);
+    const int lane = threadIdx.x & 31, step = gridDim.x * kGatherThreads;
+    for (int r0 = blockIdx.x * kGatherThreads + threadIdx.x - lane; r0 < total; r0 += step) {
+        const int r = r0 + lane;  // total is a multiple of 32
+        const int e = expert_of_row(sm.pad, p.E, r);
+        const int slot = plan_row(p, sm, r, e, true);
+        const int i = r - sm.pad[e];
+        unsigned zero = __ballot_sync(0xffffffffu, slot < 0 && (i < sm.cnt[e] || (a.zero_pad && i < (sm.cnt[e] + kRowPad - 1) /
+                                                                                                    kRowPad * kRowPad)));
+        for (; zero; zero &= zero - 1) zero_row(a, r0 + __ffs(zero) - 1, lane);
     }
 }
 
@@ -472,10 +505,10 @@ cudaError_t launch_gather_padded(const GatherArgs& a, cudaStream_t s) {
     const unsigned grid = grid_for(a.plan.max_rows, kGatherThreads / 32, 148 * 4);
     // few rows: one launch that copies as it plans; else (and for the bias products) two
     if (!a.down_b && a.plan.S * a.K * a.es < kCopyBytes) {
-        gather_padded_kernel<false><<<grid, kGatherThreads, 0, s>>>(a);
+        gather_padded_kernel<<<grid, kGatherThreads, 0, s>>>(a);
         return cudaGetLastError();
     }
-    gather_padded_kernel<true><<<grid, kGatherThreads, 0, s>>>(a);
+    plan_rows_kernel<<<grid_for(a.plan.max_rows, kGatherThreads, 148 * 2), kGatherThreads, 0, s>>>(a);
     const int64_t row = int64_t(a.K) * a.es;
     const int smem = int(std::min<int64_t>(kPiece, row)) * (a.src[1] ? 2 : 1) * kCopyWarps;
     static std::atomic<uint64_t> allowed{0};

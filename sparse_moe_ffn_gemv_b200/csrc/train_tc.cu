@@ -288,6 +288,7 @@ struct Tile {
     int nvalid;     // of those, rows that hold slots
     int n0;         // first column
     int nk;         // reduction blocks
+    int last;       // 16-deep steps of the last one
     int64_t r0;     // kTN: first reduction row
     int64_t pos0;   // first row in the caller's sorted order
 };
@@ -319,6 +320,7 @@ __device__ __forceinline__ Tile tile_of(const TcTrain& P, const Tables& tb, int 
     t.half = 0;
     t.e = 0;
     t.r0 = t.pos0 = 0;
+    t.last = kBR / 16;
     if constexpr (KIND == kTN) {
         // expert by expert; within one (dense: within a band of column blocks), the row blocks
         // of a column block in turn
@@ -344,6 +346,8 @@ __device__ __forceinline__ Tile tile_of(const TcTrain& P, const Tables& tb, int 
             n = tb.uoff[t.e + 1] - tb.uoff[t.e];
         }
         t.nk = int((n + kBR - 1) / kBR);
+        // rows past the last 16-deep step with a row are not zeroed, and belong to no product
+        if (P.offsets && t.nk > 0) t.last = int((n - int64_t(t.nk - 1) * kBR + 15) / 16);
         return t;
     }
     t.nk = P.nk;
@@ -377,7 +381,7 @@ __device__ __forceinline__ Tile tile_of(const TcTrain& P, const Tables& tb, int 
     t.row0 = tb.poff[lo] + int64_t(mt) * S::BM;
     t.n0 = nb * S::UNITS;
     const int left = tb.uoff[lo + 1] - tb.uoff[lo] - mt * S::BM;
-    t.limit = max(0, min(S::BM, (left + kBR - 1) / kBR * kBR));
+    t.limit = max(0, min(S::BM, (left + kRowPad - 1) / kRowPad * kRowPad));
     t.nvalid = max(0, min(S::BM, left));
     t.pos0 = tb.uoff[lo] + int64_t(mt) * S::BM;
     return t;
@@ -597,9 +601,11 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                     fence_after();
                     const uint32_t sa = su32(smem + stage * S::STAGE), sb = sa + kABytes;
 #pragma unroll
-                    for (int k = 0; k < kBR / 16; ++k)
+                    for (int k = 0; k < kBR / 16; ++k) {
+                        if (KIND == kTN && k >= t.last && kb == t.nk - 1) break;
                         mma<PAIR>(d0, operand<S::AMN>(sa + k * kStep<S::AMN>), operand<S::BMN>(sb + k * kStep<S::BMN>),
                                   desc, kb > kbeg || k > 0 ? 1u : 0u);
+                    }
                     commit<PAIR>(&empty[stage]);
                     if (++stage == S::STAGES) {
                         stage = 0;
