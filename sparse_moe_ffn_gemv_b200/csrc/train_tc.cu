@@ -112,7 +112,7 @@ __device__ __forceinline__ uint64_t operand(uint32_t saddr) {
 // Bytes from one 16-deep reduction step to the next within a block.
 template <bool MN> constexpr uint32_t kStep = MN ? 16 * 128 : 32;
 
-constexpr uint32_t idesc(bool a_mn, bool b_mn, int m, int n) {  // bf16 x bf16 -> f32
+__host__ __device__ constexpr uint32_t idesc(bool a_mn, bool b_mn, int m, int n) {  // bf16 x bf16 -> f32
     return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
            (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
 }
@@ -517,6 +517,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
             for (int idx = tile0; idx < total && !gave_up; idx += tstep) {
                 const Tile t = tile_of<KIND, EPI, PAIR>(P, tb, idx);
                 const int arow = int(t.row0) + 128 * int(crank);
+                // boxes of operand B that hold columns of D (the others' products are not taken)
+                constexpr int kBox = S::BMN ? 64 : 128;
+                const int boxes = PAIR || S::GATEUP ? S::B_BYTES / (kBox * kBR * 2) : (min(kCols, P.N - t.n0) + kBox - 1) / kBox;
+                const uint32_t bytes = (PAIR ? 2 : 1) * (kABytes + boxes * kBox * kBR * 2);
                 const int kend = kb_end(t);
                 for (int kb = kb_begin(t); kb < kend; ++kb) {
                     if (!wait_bar(&empty[stage], phase ^ 1u)) {
@@ -526,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                     uint8_t* sa = smem + stage * S::STAGE;
                     uint8_t* sb = sa + kABytes;
                     const uint32_t fb = PAIR ? mapa_shared(&full[stage], 0) : 0u;
-                    if (crank == 0) mbar_expect_tx(&full[stage], (PAIR ? 2 : 1) * S::STAGE);
+                    if (crank == 0) mbar_expect_tx(&full[stage], bytes);
                     const int half = KIND == kNN && kb >= P.nk_half ? 1 : 0;
                     const int kc = (kb - half * P.nk_half) * kBR;
                     if constexpr (KIND == kTN) {
@@ -536,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                         const int nb = t.n0 + 128 * int(crank);
 #pragma unroll
                         for (int j = 0; j < S::B_BYTES / 8192; ++j)
-                            load3<PAIR>(sb + j * 8192, &P.b0, &full[stage], fb, nb + 64 * j, r, 0);
+                            if (j < boxes) load3<PAIR>(sb + j * 8192, &P.b0, &full[stage], fb, nb + 64 * j, r, 0);
                     } else {
                         load3<PAIR>(sa, &P.a, &full[stage], fb, kc, half, arow);
                         if constexpr (KIND == kNN) {
@@ -544,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                             const int nb = t.n0 + 128 * int(crank);
 #pragma unroll
                             for (int j = 0; j < S::B_BYTES / 8192; ++j)
-                                load3<PAIR>(sb + j * 8192, mb, &full[stage], fb, nb + 64 * j, kc, t.e);
+                                if (j < boxes) load3<PAIR>(sb + j * 8192, mb, &full[stage], fb, nb + 64 * j, kc, t.e);
                         } else if constexpr (S::GATEUP) {
                             // gate rows, then up rows; of a pair, CTA 0 gate and CTA 1 up
                             if constexpr (PAIR) {
@@ -559,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                             const int nb = t.n0 + 128 * int(crank);
 #pragma unroll
                             for (int j = 0; j < S::B_BYTES / kABytes; ++j)
-                                load4<PAIR>(sb + j * kABytes, &P.b0, &full[stage], fb, kc, 0, nb + 128 * j, t.e);
+                                if (j < boxes) load4<PAIR>(sb + j * kABytes, &P.b0, &full[stage], fb, kc, 0, nb + 128 * j, t.e);
                         }
                     }
                     armed |= 1u << stage;
@@ -592,7 +596,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                 }
                 fence_after();
                 const uint32_t d0 = tmem + ab * kCols;
-                constexpr uint32_t desc = idesc(S::AMN, S::BMN, S::BM, kCols);
+                const uint32_t desc = idesc(S::AMN, S::BMN, S::BM,
+                                            PAIR || S::GATEUP ? kCols : (min(kCols, P.N - t.n0) + 15) / 16 * 16);
                 for (int kb = kbeg; kb < kend; ++kb) {
                     if (!wait_bar(&full[stage], phase)) {
                         gave_up = true;
@@ -635,6 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                 fence_after();
             }
             const int q = warp & 3, ch = (warp - 2) >> 2;
+            if (q * 32 >= (KIND == kTN ? t.limit : t.nvalid)) ok = false;  // rows that nobody reads
 #pragma unroll 1
             for (int c = 4 * ch; ok && c < 4 * ch + 4; ++c) {
                 uint32_t r[32];
@@ -709,20 +715,36 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                 if constexpr (SPLIT) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) r[j] = 0;
-                    for (int p = 0; p < splits; ++p) {
-                        const uint32_t at = mapa_shared(smem + (c * 8 * 128 + q * 32 + lane) * 16, uint32_t(p));
+                    if ((KIND == kTN ? rows : vrows) <= 0) return;
+                    // the ranks' sums in rank order, the next rank's loads under way meanwhile
+                    const uint32_t own = su32(smem + (c * 8 * 128 + q * 32 + lane) * 16);
+                    float4 v[2][8];
+                    auto issue = [&](int p, float4 (&x)[8]) {
+                        uint32_t at;
+                        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(own), "r"(p));
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            float4 v;
+                        for (int j = 0; j < 8; ++j)
                             asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                         : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                                         : "=f"(x[j].x), "=f"(x[j].y), "=f"(x[j].z), "=f"(x[j].w)
                                          : "r"(at + j * 2048)
                                          : "memory");
-                            r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) + v.x);
-                            r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) + v.y);
-                            r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) + v.z);
-                            r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) + v.w);
+                    };
+                    auto add = [&](const float4 (&x)[8]) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) + x[j].x);
+                            r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) + x[j].y);
+                            r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) + x[j].z);
+                            r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) + x[j].w);
                         }
+                    };
+                    issue(0, v[0]);
+#pragma unroll 1
+                    for (int p = 0; p < splits; p += 2) {  // splits is even
+                        issue(p + 1, v[1]);
+                        add(v[0]);
+                        if (p + 2 < splits) issue(p + 2, v[0]);
+                        add(v[1]);
                     }
                 } else {
                     tmem_load(tacc + 32 * c, r);
@@ -1125,13 +1147,56 @@ bool use_pair(const RowPlan& p, int64_t rows, int64_t n_blocks) {
     return blocks_of(rows, 256) * n_blocks >= sms() / 2;
 }
 
-// CTAs per tile: as many (2, 4, 8; at most `most`, what the columns divide into) as the SMs
-// hold at once, each with two reduction blocks or more.
-int splits_of(int64_t tiles, int64_t nk, int most) {
-    int s = 1;
-    while (2 * s <= most && tiles * 2 * s <= sms() && nk >= 4 * s) s *= 2;
-    return s;
+// Clusters of 2, 4 or 8 CTAs of the split kernels that the GPU holds at once (a GPC's SMs do not
+// divide into eights: 16 clusters of 8 took two rounds, 2048 x 64 over 8192 34 us). Every split
+// kernel has the same block and the same shared memory.
+int clusters_of(int s) {
+    static std::atomic<int> fits[4];
+    std::atomic<int>& f = fits[s == 2 ? 0 : s == 4 ? 1 : 2];
+    int n = f.load();
+    if (n > 0) return n;
+    using S = Shape<kNT, kStore, false>;
+    auto kern = tc_train_kernel<kNT, kStore, false, true>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = S::SMEM;
+    cfg.gridDim = dim3(sms() / s * s);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = s;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    static std::atomic<uint64_t> allowed{0};
+    if (allow_smem(kern, S::SMEM, allowed) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+        (void)cudaGetLastError();
+        n = 1;
+    }
+    f.store(n);
+    return n;
 }
+
+// CTAs per tile (1, 2, 4, 8; at most `most`, what the columns divide into): as many as pay and
+// the SMs hold at once. A reduction block takes a CTA about 0.26 us (four 128 x 256 x 16
+// products), the clusters' meeting 2.5 us + 0.2 to 0.6 us per CTA by the tile's rows (measured:
+// 16 x 256 x 64 5.0 us whole, 7.1 us split in two; 16 x 4096 x 64 about 21 us whole, 10.1 us split
+// in eight; 128 rows over 2048 13.4 us split in eight).
+int splits_of(int64_t tiles, int64_t nk, int most, int64_t rows) {
+    int best = 1;
+    int64_t cost = 26 * nk;
+    for (int s = 2; s <= most; s *= 2) {
+        const int64_t c = 26 * ((nk + s - 1) / s) + 250 + (rows > 32 ? 60 : 20) * s;
+        if (c < cost && tiles <= clusters_of(s)) {
+            cost = c;
+            best = s;
+        }
+    }
+    return best;
+}
+
+// Rows of a tile, about.
+int64_t row_hint(const RowPlan& p, int64_t rows) { return p.offsets ? (p.S + p.E - 1) / p.E : rows; }
 
 // Bands of P.band of `n` blocks, with `other` blocks of the other kind in turn in each.
 void set_bands(TcTrain& P, int n, int other) {
@@ -1189,7 +1254,7 @@ cudaError_t launch_tc_gemm_train(const GemmArgs& a, cudaStream_t s) {
             !map_b_n(&P.b0, a.b, 1, rows, a.N, a.ldb, rows * a.ldb))
             return cudaErrorInvalidValue;
         const int64_t tiles = int64_t(P.E) * P.m_blocks * P.halves * P.n_blocks;
-        if (!pair && !grouped) P.splits = splits_of(tiles, blocks_of(a.R, kBR), 8);
+        if (!pair && !grouped) P.splits = splits_of(tiles, blocks_of(a.R, kBR), 8, P.mrows);
         return launch<kTN, kStore>(P, pair, tiles, s);
     }
     const bool pair = use_pair(a.plan, a.M, P.n_blocks);
@@ -1210,7 +1275,7 @@ cudaError_t launch_tc_gemm_train(const GemmArgs& a, cudaStream_t s) {
     const int64_t E = grouped ? a.plan.E : 1;
     if (a.kind == kNT) {
         P.nk = P.nk_half = int(blocks_of(a.R, kBR));
-        if (!pair) P.splits = splits_of(tiles, P.nk, 8);
+        if (!pair) P.splits = splits_of(tiles, P.nk, 8, row_hint(a.plan, a.M));
         if (!map_a(&P.a, a.a, rows, a.lda, a.R, 1, false) || !map_b_k(&P.b0, a.b, E, a.N, 1, a.R)) return cudaErrorInvalidValue;
         return launch<kNT, kStore>(P, pair, tiles, s);
     }
@@ -1218,7 +1283,7 @@ cudaError_t launch_tc_gemm_train(const GemmArgs& a, cudaStream_t s) {
     const int64_t R = a.R / halves;
     P.nk_half = int(blocks_of(R, kBR));
     P.nk = P.nk_half * halves;
-    if (!pair) P.splits = splits_of(tiles, P.nk, 8);
+    if (!pair) P.splits = splits_of(tiles, P.nk, 8, row_hint(a.plan, a.M));
     P.b_split = halves > 1;
     if (!map_a(&P.a, a.a, rows, a.lda, R, halves, false) || !map_b_n(&P.b0, a.b, E, R, a.N, a.ldb, R * a.ldb))
         return cudaErrorInvalidValue;
@@ -1235,7 +1300,7 @@ cudaError_t launch_tc_gateup(const GemmArgs& g, const GatedArgs& ga, cudaStream_
     const int64_t tiles = row_grid(P, g.plan, pair);
     const int64_t rows = grouped ? g.plan.max_rows : g.plan.T, E = grouped ? g.plan.E : 1;
     P.nk = P.nk_half = int(blocks_of(g.R, kBR));
-    if (!pair) P.splits = splits_of(tiles, P.nk, 4);
+    if (!pair) P.splits = splits_of(tiles, P.nk, 4, row_hint(g.plan, g.plan.T));
     P.bias0 = static_cast<const __nv_bfloat16*>(g.bias);
     P.bias1 = static_cast<const __nv_bfloat16*>(g.bias1);
     P.sbias = g.sbias;
@@ -1258,7 +1323,7 @@ int dgated_parts(const RowPlan& p, int I, int64_t R) {
     P.n_blocks = int(blocks_of(I, kCols));
     const bool pair = use_pair(p, p.T, P.n_blocks);
     const int64_t tiles = row_grid(P, p, pair);
-    return 2 * P.n_blocks * (pair ? 1 : splits_of(tiles, blocks_of(R, kBR), 8));
+    return 2 * P.n_blocks * (pair ? 1 : splits_of(tiles, blocks_of(R, kBR), 8, row_hint(p, p.T)));
 }
 
 cudaError_t launch_tc_dgated(const GemmArgs& g, const GatedArgs& ga, float* partial, cudaStream_t s) {
@@ -1270,7 +1335,7 @@ cudaError_t launch_tc_dgated(const GemmArgs& g, const GatedArgs& ga, float* part
     const int64_t tiles = row_grid(P, g.plan, pair);
     const int64_t rows = grouped ? g.plan.max_rows : g.plan.T, E = grouped ? g.plan.E : 1;
     P.nk = P.nk_half = int(blocks_of(g.R, kBR));
-    if (!pair) P.splits = splits_of(tiles, P.nk, 8);
+    if (!pair) P.splits = splits_of(tiles, P.nk, 8, row_hint(g.plan, g.plan.T));
     P.act = ga.act;
     P.limit = ga.limit;
     P.alpha = ga.alpha;
