@@ -66,18 +66,19 @@ moe_status check_linear(const moe_linear_desc* d, int64_t T) {
     return MOE_OK;
 }
 
+// A forward product.
 cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t s) {
-    return g.dtype == MOE_DTYPE_F32 ? launch_simt_gemm(&g, 1, s) : launch_tc_gemm_train(g, s);
+    return g.dtype == MOE_DTYPE_F32 ? launch_simt_gemm(&g, 1, s) : launch_tc_gemm_nt(g, s);
 }
 
-// Independent products: one launch in f32, one each in bf16.
+// A backward pass's independent products; those without an output are left out.
 cudaError_t launch_gemms(const GemmArgs* g, int n, cudaStream_t s) {
-    if (n > 0 && g[0].dtype == MOE_DTYPE_F32) return launch_simt_gemm(g, n, s);
-    for (int i = 0; i < n; ++i) {
-        const cudaError_t e = launch_tc_gemm_train(g[i], s);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    if (g[0].dtype != MOE_DTYPE_F32) return launch_tc_gemms(g, n, s);
+    GemmArgs want[kMaxSimt];
+    int m = 0;
+    for (int i = 0; i < n; ++i)
+        if (g[i].out) want[m++] = g[i];
+    return m ? launch_simt_gemm(want, m, s) : cudaSuccess;
 }
 
 struct LinearWs {
@@ -195,7 +196,7 @@ FfnWs ffn_ws(const FfnShape& f, bool backward) {
         L.dgu = c.take(f.rows * 2 * f.I * f.es);
         L.hw = c.take(f.rows * f.I * f.es);
         if (f.bias)
-            L.partial = c.take(round_rows(f.rows) / kRowTile * std::max(2 * int64_t(f.I), int64_t(f.K)) * 4);
+            L.partial = c.take(round_rows(f.rows) / kRowTile * (2 * int64_t(f.I) + f.K) * 4);
     } else {
         if (f32) L.gp = c.take(f.rows * 2 * f.I * 4);
         L.h = c.take(f.rows * f.I * f.es);
@@ -333,28 +334,21 @@ moe_status moe_linear_backward(const moe_linear_desc* d, const void* dy, int64_t
         MOE_CUDA(launch_dact(a, s));
     }
     GemmArgs g[2];
-    int n = 0;
-    if (dx) {
-        GemmArgs& p = g[n++];
-        p.kind = kNN;
-        p.a = dz; p.lda = lddz;
-        p.b = w; p.ldb = K;
-        p.M = T; p.N = K; p.R = N;
-        p.out = dx; p.ldo = lddx;
-    }
-    if (dw) {
-        GemmArgs& p = g[n++];
-        p.kind = kTN;
-        p.a = dz; p.lda = lddz;
-        p.b = x; p.ldb = ldx;
-        p.M = N; p.N = K; p.R = T;
-        p.out = dw; p.ldo = K;
-    }
-    for (int i = 0; i < n; ++i) {
+    g[0].kind = kNN;
+    g[0].a = dz; g[0].lda = lddz;
+    g[0].b = w; g[0].ldb = K;
+    g[0].M = T; g[0].N = K; g[0].R = N;
+    g[0].out = dx; g[0].ldo = lddx;
+    g[1].kind = kTN;
+    g[1].a = dz; g[1].lda = lddz;
+    g[1].b = x; g[1].ldb = ldx;
+    g[1].M = N; g[1].N = K; g[1].R = T;
+    g[1].out = dw; g[1].ldo = K;
+    for (int i = 0; i < 2; ++i) {
         g[i].plan.status = device_status;
         g[i].dtype = d->dtype;
     }
-    MOE_CUDA(launch_gemms(g, n, s));
+    MOE_CUDA(launch_gemms(g, 2, s));
     return MOE_OK;
 }
 
@@ -582,18 +576,6 @@ moe_status moe_ffn_backward(const moe_config* cfg, const moe_weights* w, const v
     }
     GemmArgs gm[3];
     int n = 0;
-    if (du) {  // du = dg Wg + dv Wu
-        GemmArgs& x = gm[n++];
-        x.kind = kNN;
-        x.a = ga.dgu; x.lda = 2 * f.I;
-        x.b = f.il ? w->gate_up_w : w->gate_w; x.ldb = f.K; x.sb = int64_t(f.I) * f.K * (f.il ? 2 : 1);
-        if (!f.il) {
-            x.b1 = w->up_w;
-            x.split = f.I;
-        }
-        x.M = f.T; x.N = f.K; x.R = 2 * f.I;
-        x.out = dense ? du : at<void>(ws, L.rows_out); x.ldo = dense ? lddu : f.K; x.out_f32 = !dense;
-    }
     {  // dWd = dy^T (w h)
         GemmArgs& t = gm[n++];
         t.kind = kTN;
@@ -614,13 +596,23 @@ moe_status moe_ffn_backward(const moe_config* cfg, const moe_weights* w, const v
             t.split = f.I;
         }
     }
+    {  // du = dg Wg + dv Wu: last, so that the sum over slots finds its rows in L2
+        GemmArgs& x = gm[n++];
+        x.kind = kNN;
+        x.a = ga.dgu; x.lda = 2 * f.I;
+        x.b = f.il ? w->gate_up_w : w->gate_w; x.ldb = f.K; x.sb = int64_t(f.I) * f.K * (f.il ? 2 : 1);
+        if (!f.il) {
+            x.b1 = w->up_w;
+            x.split = f.I;
+        }
+        x.M = f.T; x.N = f.K; x.R = 2 * f.I;
+        x.out = dense || !du ? du : at<void>(ws, L.rows_out); x.ldo = dense ? lddu : f.K; x.out_f32 = !dense;
+    }
     for (int i = 0; i < n; ++i) {
         gm[i].plan = p;
         gm[i].dtype = f.dtype;
     }
-    // f32: all in one launch; bf16: du first, whose rows the sum then finds in L2
-    const int first = f.dtype == MOE_DTYPE_F32 ? n : (du ? 1 : 0);
-    MOE_CUDA(launch_gemms(gm, first, s));
+    MOE_CUDA(launch_gemms(gm, n, s));
     if (du && !dense) {
         SumSlotsArgs sa;
         sa.plan = p;
@@ -630,24 +622,21 @@ moe_status moe_ffn_backward(const moe_config* cfg, const moe_weights* w, const v
         sa.dtype = f.dtype;
         MOE_CUDA(launch_sum_slots(sa, s));
     }
-    MOE_CUDA(launch_gemms(gm + first, n - first, s));
     if (f.bias) {
-        ColsumArgs c;
-        c.plan = p;
-        c.dtype = f.dtype;
-        c.partial = at<float>(ws, L.partial);
-        c.x = ga.dgu; c.ldx = 2 * f.I; c.cols = 2 * f.I;
-        c.out = f.il ? gr->gate_up_b : gr->gate_b; c.so = int64_t(f.I) * (f.il ? 2 : 1);
+        ColsumArgs c[2];
+        c[0].plan = c[1].plan = p;
+        c[0].dtype = c[1].dtype = f.dtype;
+        c[0].partial = at<float>(ws, L.partial);
+        c[0].x = ga.dgu; c[0].ldx = 2 * f.I; c[0].cols = 2 * f.I;
+        c[0].out = f.il ? gr->gate_up_b : gr->gate_b; c[0].so = int64_t(f.I) * (f.il ? 2 : 1);
         if (!f.il) {
-            c.out1 = gr->up_b;
-            c.split = f.I;
+            c[0].out1 = gr->up_b;
+            c[0].split = f.I;
         }
-        MOE_CUDA(launch_colsum(c, s));
-        c.x = dyp; c.ldx = lddyp; c.cols = f.K;
-        c.row_scale = topk_w;
-        c.out = gr->down_b; c.so = f.K;
-        c.out1 = nullptr;
-        c.split = 0;
+        c[1].partial = c[0].partial + round_rows(f.rows) / kRowTile * 2 * f.I;
+        c[1].x = dyp; c[1].ldx = lddyp; c[1].cols = f.K;
+        c[1].row_scale = topk_w;
+        c[1].out = gr->down_b; c[1].so = f.K;
         MOE_CUDA(launch_colsum(c, s));
     }
     return MOE_OK;

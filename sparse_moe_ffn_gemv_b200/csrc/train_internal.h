@@ -97,10 +97,15 @@ struct GemmArgs {
 // f32: n independent products (at most kMaxSimt) in one launch.
 constexpr int kMaxSimt = 3;
 cudaError_t launch_simt_gemm(const GemmArgs* a, int n, cudaStream_t s);
-cudaError_t launch_tc_gemm_train(const GemmArgs& a, cudaStream_t s);  // bf16, any kind
+// bf16: one kNT product; up to three independent kNN and kTN products of one plan (those
+// without an output are not computed).
+cudaError_t launch_tc_gemm_nt(const GemmArgs& a, cudaStream_t s);
+cudaError_t launch_tc_gemms(const GemmArgs* a, int n, cudaStream_t s);
 
-// The forward products for at most kSmallT tokens, both types.
-constexpr int kSmallT = 8;
+// The forward products for at most kSmallT tokens, both types. (Weights cold, us, this / tensor
+// cores: 2048 x 2048 1 token 6.3 / 11.4, 4 tokens 10.3 / 11.5, 8 tokens 16.9 / 11.5; 3584 x 7168
+// 1 token 17.2 / 19.1, 4 tokens 28.5 / 19.1; a gated FFN of 2048 x 768 11.8, 19.1 and 32.6 / 22.3.)
+constexpr int kSmallT = 4;
 struct SmallArgs {
     int T = 0, K = 0, N = 0;  // N: outputs (gated: units)
     int dtype = MOE_DTYPE_BF16;
@@ -164,7 +169,7 @@ struct ColsumArgs {
     float* partial = nullptr;             // [rows / kRowTile rounded up, cols]
     int dtype = MOE_DTYPE_BF16;
 };
-cudaError_t launch_colsum(const ColsumArgs& a, cudaStream_t s);
+cudaError_t launch_colsum(const ColsumArgs (&a)[2], cudaStream_t s);  // of one plan and dtype
 
 // dz = dy * act'(pre), rounded to the activation dtype; partial column sums of the unrounded
 // dz when partial is set (act none: only the sums are taken and dz may be null).

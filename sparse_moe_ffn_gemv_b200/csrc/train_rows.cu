@@ -356,8 +356,10 @@ __global__ void __launch_bounds__(256) dtopk_kernel(const GatedArgs a, const flo
 // 16-byte column vectors; each thread one vector and every 4th row, 8 rows' loads in flight.
 constexpr int kColVecs = 64, kColRows = 4, kColDeep = 8;
 template <typename T>
-__global__ void __launch_bounds__(kColVecs * kColRows) colsum_kernel(const ColsumArgs a) {
+__global__ void __launch_bounds__(kColVecs * kColRows) colsum_kernel(const ColsumArgs a0, const ColsumArgs a1, int blocks0) {
     constexpr int V = Vec<T>::N;
+    const bool second = int(blockIdx.y) >= blocks0;
+    const ColsumArgs& a = second ? a1 : a0;
     const RowPlan& p = a.plan;
     const int64_t b = int64_t(blockIdx.x) * kRowTile;
     int64_t end = p.T;
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(kColVecs * kColRows) colsum_kernel(const Colsu
         end = p.poff[e] + (p.uoff[e + 1] - p.uoff[e]);
     }
     end = min(end, b + kRowTile);
-    const int c = (blockIdx.y * kColVecs + threadIdx.x % kColVecs) * V;
+    const int c = ((blockIdx.y - (second ? blocks0 : 0)) * kColVecs + threadIdx.x % kColVecs) * V;
     const int ry = threadIdx.x / kColVecs;
     float acc[V] = {};
     if (c < a.cols) {
@@ -415,11 +417,13 @@ __global__ void __launch_bounds__(kColVecs * kColRows) colsum_kernel(const Colsu
 // partial row of the expert, then those 8 in order; rounded once. Without a plan (dense): the
 // `parts` rows of one matrix.
 template <typename T>
-__global__ void __launch_bounds__(256) colsum_finish_kernel(const ColsumArgs a, int parts) {
+__global__ void __launch_bounds__(256) colsum_finish_kernel(const ColsumArgs a0, const ColsumArgs a1, int blocks0, int parts) {
     __shared__ float sm[8][33];
     const int e = blockIdx.y;
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + x;
+    const bool second = int(blockIdx.x) >= blocks0;
+    const ColsumArgs& a = second ? a1 : a0;
+    const int c = (blockIdx.x - (second ? blocks0 : 0)) * 32 + x;
     int64_t p0 = 0, p1 = parts;
     if (a.plan.offsets) {
         p0 = a.plan.poff[e] / kRowTile;
@@ -549,17 +553,18 @@ cudaError_t launch_dtopk(const GatedArgs& a, const float* partial, int parts, cu
     return cudaGetLastError();
 }
 
-cudaError_t launch_colsum(const ColsumArgs& a, cudaStream_t s) {
-    const int V = a.dtype == MOE_DTYPE_F32 ? 4 : 8;
-    const int64_t tiles = (a.plan.max_rows + kRowTile - 1) / kRowTile;
-    const dim3 grid(unsigned(tiles), (a.cols / V + kColVecs - 1) / kColVecs);
-    const dim3 fin((a.cols + 31) / 32, a.plan.E);
-    if (a.dtype == MOE_DTYPE_F32) {
-        colsum_kernel<float><<<grid, kColVecs * kColRows, 0, s>>>(a);
-        colsum_finish_kernel<float><<<fin, 256, 0, s>>>(a, int(tiles));
+cudaError_t launch_colsum(const ColsumArgs (&a)[2], cudaStream_t s) {
+    const int V = a[0].dtype == MOE_DTYPE_F32 ? 4 : 8, per = kColVecs * V;
+    const int64_t tiles = (a[0].plan.max_rows + kRowTile - 1) / kRowTile;
+    const int c0 = (a[0].cols + per - 1) / per, c1 = (a[1].cols + per - 1) / per;
+    const int f0 = (a[0].cols + 31) / 32, f1 = (a[1].cols + 31) / 32;
+    const dim3 grid(unsigned(tiles), c0 + c1), fin(f0 + f1, a[0].plan.E);
+    if (a[0].dtype == MOE_DTYPE_F32) {
+        colsum_kernel<float><<<grid, kColVecs * kColRows, 0, s>>>(a[0], a[1], c0);
+        colsum_finish_kernel<float><<<fin, 256, 0, s>>>(a[0], a[1], f0, int(tiles));
     } else {
-        colsum_kernel<__nv_bfloat16><<<grid, kColVecs * kColRows, 0, s>>>(a);
-        colsum_finish_kernel<__nv_bfloat16><<<fin, 256, 0, s>>>(a, int(tiles));
+        colsum_kernel<__nv_bfloat16><<<grid, kColVecs * kColRows, 0, s>>>(a[0], a[1], c0);
+        colsum_finish_kernel<__nv_bfloat16><<<fin, 256, 0, s>>>(a[0], a[1], f0, int(tiles));
     }
     return cudaGetLastError();
 }
@@ -581,8 +586,8 @@ cudaError_t launch_dact(const DactArgs& a, cudaStream_t s) {
         c.out = a.db;
         c.partial = a.partial;
         const unsigned fin = (a.N + 31) / 32;
-        if (a.dtype == MOE_DTYPE_F32) colsum_finish_kernel<float><<<fin, 256, 0, s>>>(c, splits);
-        else colsum_finish_kernel<__nv_bfloat16><<<fin, 256, 0, s>>>(c, splits);
+        if (a.dtype == MOE_DTYPE_F32) colsum_finish_kernel<float><<<fin, 256, 0, s>>>(c, c, fin, splits);
+        else colsum_finish_kernel<__nv_bfloat16><<<fin, 256, 0, s>>>(c, c, fin, splits);
     }
     return cudaGetLastError();
 }

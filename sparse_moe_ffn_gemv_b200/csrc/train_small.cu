@@ -177,8 +177,7 @@ template <typename T, bool GATED>
 cudaError_t launch_t(const SmallArgs& a, cudaStream_t s) {
     if (a.T == 1) return launch_tt<T, 1, GATED>(a, s);
     if (a.T == 2) return launch_tt<T, 2, GATED>(a, s);
-    if (a.T <= 4) return launch_tt<T, 4, GATED>(a, s);
-    return launch_tt<T, 8, GATED>(a, s);
+    return launch_tt<T, kSmallT, GATED>(a, s);
 }
 
 }  // namespace

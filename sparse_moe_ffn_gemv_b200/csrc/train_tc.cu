@@ -6,6 +6,8 @@
 //   kNT  A [m][r], B [n][r]  both operands with the reduction contiguous (K-major)
 //   kNN  A [m][r], B [r][n]  B with n contiguous (MN-major): dz times a weight plane
 //   kTN  A [r][m], B [r][n]  both MN-major: dz^T times the tokens, reduced over an expert's rows
+//   kMix the independent kNN and kTN products of a small backward pass in one launch (large ones
+//        run one after the other: together they measured no faster)
 //
 // No operand is transposed in memory: the matrix instructions read either order from shared
 // memory, and TMA brings either as 64 x 64 (MN-major) or 64 x 128 (K-major) boxes with the
@@ -28,6 +30,7 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
 #include "ptx.cuh"
 #include "train_dev.cuh"
@@ -45,6 +48,8 @@ constexpr int kABytes = 128 * kBR * 2;  // one 128-row operand tile
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 // kGateUpI, kDGatedI: alternating gate / up columns.
+constexpr int kMix = 3;  // besides enum GemmKind
+constexpr int kMaxMix = 3;
 enum Epi { kStore = 0, kGateUp = 1, kGateUpI = 2, kDGated = 3, kDGatedI = 4 };
 
 // Division by a launch constant: n / d = umulhi(n, m) >> s for 0 <= n < 2^31 (m = ceil(2^(32+s) / d)
@@ -68,6 +73,7 @@ FastDiv fast_div(int64_t d) {
 struct TcTrain {
     CUtensorMap a, b0, b1;
     FastDiv d_tile, d_m, d_band, d_width, d_tail;  // see tile_of
+    int tn;                 // kMix: a kTN product
     int splits;             // CTAs of a cluster that share a tile's reduction (SPLIT)
     // rows
     const int32_t *offsets, *poff, *uoff, *row_slot;  // grouped (offsets != null)
@@ -96,6 +102,11 @@ struct TcTrain {
     float* partial;         // kDGated: [rows, parts]
     int parts;
     int* status;
+};
+
+template <int NP> struct TcArgs {
+    TcTrain p[NP];  // one plan and status for all
+    int n;
 };
 
 // ------------------------------------------------------------------ tcgen05
@@ -300,7 +311,8 @@ struct Tables {
 template <int KIND, int EPI, bool PAIR>
 struct Shape {
     static constexpr int BM = PAIR ? 256 : 128;
-    static constexpr bool AMN = KIND == kTN, BMN = KIND != kNT;
+    static constexpr bool BMN = KIND != kNT;
+    static constexpr int NP = KIND == kMix ? kMaxMix : 1;
     static constexpr int B_BYTES = PAIR ? kABytes : 2 * kABytes;
     static constexpr int STAGE = kABytes + B_BYTES;
     static constexpr int STAGES = PAIR ? 6 : 4;
@@ -321,7 +333,7 @@ __device__ __forceinline__ Tile tile_of(const TcTrain& P, const Tables& tb, int 
     t.e = 0;
     t.r0 = t.pos0 = 0;
     t.last = kBR / 16;
-    if constexpr (KIND == kTN) {
+    if (KIND == kTN || (KIND == kMix && P.tn)) {
         // expert by expert; within one (dense: within a band of column blocks), the row blocks
         // of a column block in turn
         t.e = P.d_tile(idx);
@@ -427,7 +439,7 @@ __device__ __forceinline__ void load4(void* dst, const CUtensorMap* m, uint64_t*
 // meet in shared memory, where each CTA adds up a part of the columns (in rank order) and runs
 // the epilogue on it. For problems of fewer tiles than SMs.
 template <int KIND, int EPI, bool PAIR, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_constant__ TcTrain P) {
+__global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_constant__ TcArgs<Shape<KIND, EPI, PAIR>::NP> A) {
     static_assert(!(PAIR && SPLIT), "one or the other");
     using S = Shape<KIND, EPI, PAIR>;
     extern __shared__ uint8_t smem_raw[];
@@ -441,6 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     Tables& tb = *reinterpret_cast<Tables*>(stg + S::STG + 256);
 
+    const TcTrain& P = A.p[0];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t crank = PAIR ? cluster_rank() : 0u;
     const int srank = SPLIT ? int(cluster_rank()) : 0, splits = SPLIT ? P.splits : 1;
@@ -505,9 +518,27 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
     if constexpr (PAIR) cluster_sync();
     fence_after();
     const uint32_t tmem = *tmem_slot;
-    int total;
-    if (KIND == kTN) total = P.E * P.m_blocks * P.halves * P.n_blocks;
-    else total = (P.offsets ? tb.ts[P.E] : P.m_blocks) * P.n_blocks;
+    // tiles of the problems one after the other
+    auto tiles_of = [&](const TcTrain& p) {
+        if (KIND == kTN || (KIND == kMix && p.tn)) return p.E * p.m_blocks * p.halves * p.n_blocks;
+        return (p.offsets ? tb.ts[p.E] : p.m_blocks) * p.n_blocks;
+    };
+    int ends[S::NP];
+    ends[0] = tiles_of(A.p[0]);
+#pragma unroll
+    for (int i = 1; i < S::NP; ++i) ends[i] = ends[i - 1] + (i < A.n ? tiles_of(A.p[i]) : 0);
+    const int total = ends[S::NP - 1];
+    auto problem = [&](int idx, int& local) -> const TcTrain& {
+        int i = 0;
+        local = idx;
+#pragma unroll
+        for (int j = 1; j < S::NP; ++j)
+            if (idx >= ends[j - 1]) {
+                i = j;
+                local = idx - ends[j - 1];
+            }
+        return A.p[S::NP == 1 ? 0 : i];
+    };
     bool gave_up = false;
 
     if (warp == 0) {
@@ -515,7 +546,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
         if (lane == 0) {
             uint32_t stage = 0, phase = 0, armed = 0, last = 0;
             for (int idx = tile0; idx < total && !gave_up; idx += tstep) {
-                const Tile t = tile_of<KIND, EPI, PAIR>(P, tb, idx);
+                int local;
+                const TcTrain& P = problem(idx, local);
+                const bool tn = KIND == kTN || (KIND == kMix && P.tn);
+                const Tile t = tile_of<KIND, EPI, PAIR>(P, tb, local);
                 const int arow = int(t.row0) + 128 * int(crank);
                 // boxes of operand B that hold columns of D (the others' products are not taken)
                 constexpr int kBox = S::BMN ? 64 : 128;
@@ -531,9 +565,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                     uint8_t* sb = sa + kABytes;
                     const uint32_t fb = PAIR ? mapa_shared(&full[stage], 0) : 0u;
                     if (crank == 0) mbar_expect_tx(&full[stage], bytes);
-                    const int half = KIND == kNN && kb >= P.nk_half ? 1 : 0;
+                    const int half = S::BMN && !tn && kb >= P.nk_half ? 1 : 0;
                     const int kc = (kb - half * P.nk_half) * kBR;
-                    if constexpr (KIND == kTN) {
+                    if (tn) {
                         const int r = int(t.r0) + kb * kBR;
                         load3<PAIR>(sa, &P.a, &full[stage], fb, arow, t.half, r);
                         load3<PAIR>(sa + 8192, &P.a, &full[stage], fb, arow + 64, t.half, r);
@@ -543,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                             if (j < boxes) load3<PAIR>(sb + j * 8192, &P.b0, &full[stage], fb, nb + 64 * j, r, 0);
                     } else {
                         load3<PAIR>(sa, &P.a, &full[stage], fb, kc, half, arow);
-                        if constexpr (KIND == kNN) {
+                        if constexpr (S::BMN) {
                             const CUtensorMap* mb = half && P.b_split ? &P.b1 : &P.b0;
                             const int nb = t.n0 + 128 * int(crank);
 #pragma unroll
@@ -585,7 +619,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
             // -------------------------------------------------------- MMA issuer
             uint32_t stage = 0, phase = 0, it = 0;
             for (int idx = tile0; idx < total && !gave_up; idx += tstep) {
-                const Tile t = tile_of<KIND, EPI, PAIR>(P, tb, idx);
+                int local;
+                const TcTrain& P = problem(idx, local);
+                const bool tn = KIND == kTN || (KIND == kMix && P.tn);
+                const Tile t = tile_of<KIND, EPI, PAIR>(P, tb, local);
                 const int kbeg = kb_begin(t), kend = kb_end(t);
                 if (kbeg == kend) continue;
                 const uint32_t ab = it & 1u, ph = (it >> 1) & 1u;
@@ -596,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                 }
                 fence_after();
                 const uint32_t d0 = tmem + ab * kCols;
-                const uint32_t desc = idesc(S::AMN, S::BMN, S::BM,
+                const uint32_t desc = idesc(tn, S::BMN, S::BM,
                                             PAIR || S::GATEUP ? kCols : (min(kCols, P.N - t.n0) + 15) / 16 * 16);
                 for (int kb = kbeg; kb < kend; ++kb) {
                     if (!wait_bar(&full[stage], phase)) {
@@ -605,12 +642,17 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                     }
                     fence_after();
                     const uint32_t sa = su32(smem + stage * S::STAGE), sb = sa + kABytes;
+                    auto products = [&](auto a_mn) {
+                        constexpr bool AMN = decltype(a_mn)::value;
 #pragma unroll
-                    for (int k = 0; k < kBR / 16; ++k) {
-                        if (KIND == kTN && k >= t.last && kb == t.nk - 1) break;
-                        mma<PAIR>(d0, operand<S::AMN>(sa + k * kStep<S::AMN>), operand<S::BMN>(sb + k * kStep<S::BMN>),
-                                  desc, kb > kbeg || k > 0 ? 1u : 0u);
-                    }
+                        for (int k = 0; k < kBR / 16; ++k) {
+                            if (AMN && k >= t.last && kb == t.nk - 1) break;
+                            mma<PAIR>(d0, operand<AMN>(sa + k * kStep<AMN>), operand<S::BMN>(sb + k * kStep<S::BMN>),
+                                      desc, kb > kbeg || k > 0 ? 1u : 0u);
+                        }
+                    };
+                    if (tn) products(std::true_type{});
+                    else products(std::false_type{});
                     commit<PAIR>(&empty[stage]);
                     if (++stage == S::STAGES) {
                         stage = 0;
@@ -631,7 +673,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
         // this CTA's part of the sums into shared memory (the ring: its products are done), 16
         // bytes of four columns per row, rows adjacent
         if (warp >= 2 && tile0 < total) {
-            const Tile t = tile_of<KIND, EPI, PAIR>(P, tb, tile0);
+            int local;
+            const TcTrain& P = problem(tile0, local);
+            const bool tn = KIND == kTN || (KIND == kMix && P.tn);
+            const Tile t = tile_of<KIND, EPI, PAIR>(P, tb, local);
             const bool any = kb_begin(t) < kb_end(t);
             bool ok = true;
             if (any) {
@@ -640,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                 fence_after();
             }
             const int q = warp & 3, ch = (warp - 2) >> 2;
-            if (q * 32 >= (KIND == kTN ? t.limit : t.nvalid)) ok = false;  // rows that nobody reads
+            if (q * 32 >= (tn ? t.limit : t.nvalid)) ok = false;  // rows that nobody reads
 #pragma unroll 1
             for (int c = 4 * ch; ok && c < 4 * ch + 4; ++c) {
                 uint32_t r[32];
@@ -689,13 +734,16 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
             }
         };
         auto epilogue = [&](int idx) -> bool {
-            const Tile t = tile_of<KIND, EPI, PAIR>(P, tb, idx);
+            int local;
+            const TcTrain& P = problem(idx, local);
+            const bool tn = KIND == kTN || (KIND == kMix && P.tn);
+            const Tile t = tile_of<KIND, EPI, PAIR>(P, tb, local);
             const int rows = min(32, t.limit - wrow);     // may be negative
             const int vrows = min(32, t.nvalid - wrow);
             const int64_t row = t.row0 + wrow;            // the warp's first row
             const uint32_t ab = it & 1u, ph = (it >> 1) & 1u;
             float rs = 1.0f;
-            if (KIND != kTN && P.offsets && P.row_scale && lane < vrows) {
+            if (!tn && P.offsets && P.row_scale && lane < vrows) {
                 const int slot = P.row_slot[row + lane];
                 rs = slot < 0 ? 0.0f : P.row_scale[slot];
             }
@@ -715,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                 if constexpr (SPLIT) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) r[j] = 0;
-                    if ((KIND == kTN ? rows : vrows) <= 0) return;
+                    if ((tn ? rows : vrows) <= 0) return;
                     // the ranks' sums in rank order, the next rank's loads under way meanwhile
                     const uint32_t own = su32(smem + (c * 8 * 128 + q * 32 + lane) * 16);
                     float4 v[2][8];
@@ -889,7 +937,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                     put(oh, P.hw + row * P.N + col, int64_t(P.N) * 2, bytes);
                 }
                 if (P.partial && valid) P.partial[(row + lane) * P.parts + ((t.n0 / kCols) * splits + srank) * 2 + ch] = dw;
-            } else if constexpr (KIND == kTN) {
+            } else if (tn) {
                 __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(t.half ? P.out1 : P.out) + t.e * P.so + row * P.ldo;
                 if constexpr (SPLIT) {
 #pragma unroll 1
@@ -1058,8 +1106,11 @@ cudaError_t allow_smem(K kern, int bytes, std::atomic<uint64_t>& done) {
 }
 
 template <int KIND, int EPI, bool PAIR, bool SPLIT>
-cudaError_t launch_t(const TcTrain& P, int64_t max_tiles, cudaStream_t s) {
+cudaError_t launch_t(const TcTrain* P, int np, int64_t max_tiles, cudaStream_t s) {
     using S = Shape<KIND, EPI, PAIR>;
+    TcArgs<S::NP> args;
+    for (int i = 0; i < S::NP; ++i) args.p[i] = P[std::min(i, np - 1)];
+    args.n = np;
     auto kern = tc_train_kernel<KIND, EPI, PAIR, SPLIT>;
     static std::atomic<uint64_t> allowed{0};
     cudaError_t err = allow_smem(kern, S::SMEM, allowed);
@@ -1070,13 +1121,13 @@ cudaError_t launch_t(const TcTrain& P, int64_t max_tiles, cudaStream_t s) {
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = PAIR ? 2 : SPLIT ? P.splits : 1;
+    attr[0].val.clusterDim.x = PAIR ? 2 : SPLIT ? P->splits : 1;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = PAIR || SPLIT ? 1 : 0;
     if (SPLIT) {
-        cfg.gridDim = dim3(unsigned(max_tiles) * P.splits);
-        if ((err = cudaLaunchKernelEx(&cfg, kern, P)) != cudaSuccess) return err;
+        cfg.gridDim = dim3(unsigned(max_tiles) * P->splits);
+        if ((err = cudaLaunchKernelEx(&cfg, kern, args)) != cudaSuccess) return err;
         return cudaGetLastError();
     }
     int most = sms();
@@ -1094,15 +1145,16 @@ cudaError_t launch_t(const TcTrain& P, int64_t max_tiles, cudaStream_t s) {
     const int n = int(std::min<int64_t>(max_tiles, most));
     if (n <= 0) return cudaSuccess;
     cfg.gridDim = dim3(PAIR ? 2 * n : n);
-    if ((err = cudaLaunchKernelEx(&cfg, kern, P)) != cudaSuccess) return err;
+    if ((err = cudaLaunchKernelEx(&cfg, kern, args)) != cudaSuccess) return err;
     return cudaGetLastError();
 }
 
 // The three forms of a product: split, pairs, or one CTA per tile.
 template <int KIND, int EPI>
 cudaError_t launch(const TcTrain& P, bool pair, int64_t max_tiles, cudaStream_t s) {
-    if (P.splits > 1) return launch_t<KIND, EPI, false, true>(P, max_tiles, s);
-    return pair ? launch_t<KIND, EPI, true, false>(P, max_tiles, s) : launch_t<KIND, EPI, false, false>(P, max_tiles, s);
+    if (P.splits > 1) return launch_t<KIND, EPI, false, true>(&P, 1, max_tiles, s);
+    return pair ? launch_t<KIND, EPI, true, false>(&P, 1, max_tiles, s)
+                : launch_t<KIND, EPI, false, false>(&P, 1, max_tiles, s);
 }
 
 int64_t blocks_of(int64_t n, int64_t b) { return (n + b - 1) / b; }
@@ -1227,8 +1279,12 @@ int64_t row_grid(TcTrain& P, const RowPlan& p, bool pair) {
 
 }  // namespace
 
-cudaError_t launch_tc_gemm_train(const GemmArgs& a, cudaStream_t s) {
-    TcTrain P = base_of(a.plan);
+namespace {
+
+// A problem's launch parameters (without an output: no tensor maps), whether it runs on CTA pairs,
+// and its tiles at most.
+bool set_up(const GemmArgs& a, TcTrain& P, bool& pair, int64_t& tiles) {
+    P = base_of(a.plan);
     const bool grouped = a.plan.offsets != nullptr;
     P.N = a.N;
     P.n_blocks = int(blocks_of(a.N, kCols));
@@ -1237,32 +1293,33 @@ cudaError_t launch_tc_gemm_train(const GemmArgs& a, cudaStream_t s) {
     P.ldo = a.ldo;
     P.so = a.so;
     if (a.kind == kTN) {
+        P.tn = 1;
         P.halves = a.split ? 2 : 1;
         P.mrows = a.M / P.halves;
         const int64_t rows = grouped ? a.plan.max_rows : a.R;
         P.rows = a.R;
         P.E = grouped ? a.plan.E : 1;
         const int64_t tiles256 = blocks_of(P.mrows, 256) * P.halves * P.n_blocks * P.E;
-        const bool pair = tiles256 >= sms() / 2;
+        pair = tiles256 >= sms() / 2;
         P.m_blocks = int(blocks_of(P.mrows, pair ? 256 : 128));
         // an expert's tiles: one column block at a time; dense: as many as fill the GPU with every row block
         P.band = grouped ? 1 : band_of(P.n_blocks, P.m_blocks * P.halves, pair ? sms() / 2 : sms());
         set_bands(P, P.n_blocks, P.m_blocks * P.halves);
         P.d_tile = fast_div(int64_t(P.m_blocks) * P.halves * P.n_blocks);
         P.d_m = fast_div(P.m_blocks);
-        if (!map_a(&P.a, a.a, rows, a.lda, P.mrows, P.halves, true) ||
-            !map_b_n(&P.b0, a.b, 1, rows, a.N, a.ldb, rows * a.ldb))
-            return cudaErrorInvalidValue;
-        const int64_t tiles = int64_t(P.E) * P.m_blocks * P.halves * P.n_blocks;
-        if (!pair && !grouped) P.splits = splits_of(tiles, blocks_of(a.R, kBR), 8, P.mrows);
-        return launch<kTN, kStore>(P, pair, tiles, s);
+        tiles = int64_t(P.E) * P.m_blocks * P.halves * P.n_blocks;
+        P.nk = int(blocks_of(a.R, kBR));
+        if (!pair && !grouped) P.splits = splits_of(tiles, P.nk, 8, P.mrows);
+        if (!a.out) return true;
+        return map_a(&P.a, a.a, rows, a.lda, P.mrows, P.halves, true) &&
+               map_b_n(&P.b0, a.b, 1, rows, a.N, a.ldb, rows * a.ldb);
     }
-    const bool pair = use_pair(a.plan, a.M, P.n_blocks);
+    pair = use_pair(a.plan, a.M, P.n_blocks);
     const int64_t rows = grouped ? a.plan.max_rows : a.M;
     if (!grouped) P.rows = a.M;
     RowPlan rp = a.plan;
     rp.T = a.M;
-    const int64_t tiles = row_grid(P, rp, pair);
+    tiles = row_grid(P, rp, pair);
     P.bias0 = static_cast<const __nv_bfloat16*>(a.bias);
     P.sbias = a.sbias;
     P.act = a.act;
@@ -1273,22 +1330,68 @@ cudaError_t launch_tc_gemm_train(const GemmArgs& a, cudaStream_t s) {
     P.ldp = a.ldp;
     P.out_f32 = a.out_f32;
     const int64_t E = grouped ? a.plan.E : 1;
-    if (a.kind == kNT) {
-        P.nk = P.nk_half = int(blocks_of(a.R, kBR));
-        if (!pair) P.splits = splits_of(tiles, P.nk, 8, row_hint(a.plan, a.M));
-        if (!map_a(&P.a, a.a, rows, a.lda, a.R, 1, false) || !map_b_k(&P.b0, a.b, E, a.N, 1, a.R)) return cudaErrorInvalidValue;
-        return launch<kNT, kStore>(P, pair, tiles, s);
-    }
-    const int halves = a.split ? 2 : 1;
+    const int halves = a.kind == kNN && a.split ? 2 : 1;
     const int64_t R = a.R / halves;
     P.nk_half = int(blocks_of(R, kBR));
     P.nk = P.nk_half * halves;
-    if (!pair) P.splits = splits_of(tiles, P.nk, 8, row_hint(a.plan, a.M));
     P.b_split = halves > 1;
-    if (!map_a(&P.a, a.a, rows, a.lda, R, halves, false) || !map_b_n(&P.b0, a.b, E, R, a.N, a.ldb, R * a.ldb))
-        return cudaErrorInvalidValue;
-    if (halves > 1 && !map_b_n(&P.b1, a.b1, E, R, a.N, a.ldb, R * a.ldb)) return cudaErrorInvalidValue;
-    return launch<kNN, kStore>(P, pair, tiles, s);
+    if (!pair) P.splits = splits_of(tiles, P.nk, 8, row_hint(a.plan, a.M));
+    if (!a.out) return true;
+    if (!map_a(&P.a, a.a, rows, a.lda, R, halves, false)) return false;
+    if (a.kind == kNT) return map_b_k(&P.b0, a.b, E, a.N, 1, R);
+    return map_b_n(&P.b0, a.b, E, R, a.N, a.ldb, R * a.ldb) &&
+           (halves == 1 || map_b_n(&P.b1, a.b1, E, R, a.N, a.ldb, R * a.ldb));
+}
+
+}  // namespace
+
+cudaError_t launch_tc_gemm_nt(const GemmArgs& a, cudaStream_t s) {
+    TcTrain P;
+    bool pair;
+    int64_t tiles;
+    if (!set_up(a, P, pair, tiles)) return cudaErrorInvalidValue;
+    return launch<kNT, kStore>(P, pair, tiles, s);
+}
+
+cudaError_t launch_tc_gemms(const GemmArgs* a, int n, cudaStream_t s) {
+    TcTrain P[kMaxMix];
+    bool pair[kMaxMix];
+    int64_t tiles[kMaxMix];
+    if (n > kMaxMix) return cudaErrorInvalidValue;
+    for (int i = 0; i < n; ++i)
+        if (!set_up(a[i], P[i], pair[i], tiles[i])) return cudaErrorInvalidValue;
+    // together no more tiles than SMs: one launch, split by the longest reduction. Gradients that
+    // were not asked for count here too, so that the others do not depend on them.
+    int64_t sum = 0, nk = 0, rows = 0;
+    bool any_pair = false;
+    for (int i = 0; i < n; ++i) {
+        sum += tiles[i];
+        nk = std::max<int64_t>(nk, P[i].nk);
+        rows = std::max<int64_t>(rows, P[i].tn ? P[i].mrows : row_hint(a[i].plan, a[i].M));
+        any_pair = any_pair || pair[i];
+    }
+    if (n > 1 && !any_pair && sum <= sms()) {
+        const int splits = splits_of(sum, nk, 8, rows);
+        int m = 0;
+        sum = 0;
+        for (int i = 0; i < n; ++i) {
+            if (!a[i].out) continue;
+            P[m] = P[i];
+            P[m++].splits = splits;
+            sum += tiles[i];
+        }
+        if (m == 0) return cudaSuccess;
+        n = m;
+        return splits > 1 ? launch_t<kMix, kStore, false, true>(P, n, sum, s)
+                          : launch_t<kMix, kStore, false, false>(P, n, sum, s);
+    }
+    for (int i = 0; i < n; ++i) {
+        if (!a[i].out) continue;
+        const cudaError_t e = P[i].tn ? launch<kTN, kStore>(P[i], pair[i], tiles[i], s)
+                                      : launch<kNN, kStore>(P[i], pair[i], tiles[i], s);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 cudaError_t launch_tc_gateup(const GemmArgs& g, const GatedArgs& ga, cudaStream_t s) {
