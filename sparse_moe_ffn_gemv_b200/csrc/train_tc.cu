@@ -50,7 +50,8 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 // kGateUpI, kDGatedI: alternating gate / up columns.
 constexpr int kMix = 3;  // besides enum GemmKind
 constexpr int kMaxMix = 3;
-enum Epi { kStore = 0, kGateUp = 1, kGateUpI = 2, kDGated = 3, kDGatedI = 4 };
+// kStoreBulk: kTN on pairs, D leaves by TMA.
+enum Epi { kStore = 0, kGateUp = 1, kGateUpI = 2, kDGated = 3, kDGatedI = 4, kStoreBulk = 5 };
 
 // Division by a launch constant: n / d = umulhi(n, m) >> s for 0 <= n < 2^31 (m = ceil(2^(32+s) / d)
 // with 2^s < d <= 2^(s+1)), two instructions in place of a divide in every role's tile walk.
@@ -72,8 +73,10 @@ FastDiv fast_div(int64_t d) {
 
 struct TcTrain {
     CUtensorMap a, b0, b1;
+    CUtensorMap o0, o1;     // kTN on pairs: the planes of D
     FastDiv d_tile, d_m, d_band, d_width, d_tail;  // see tile_of
     int tn;                 // kMix: a kTN product
+    int bulk_out;           // host: kStoreBulk
     int splits;             // CTAs of a cluster that share a tile's reduction (SPLIT)
     // rows
     const int32_t *offsets, *poff, *uoff, *row_slot;  // grouped (offsets != null)
@@ -184,10 +187,15 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
                  : "memory");
 }
 
-// Bounded wait; the clock starts when the wait does, so that a long launch is no timeout.
+// Bounded wait; the clock starts when the wait does, so that a long launch is no timeout. The
+// thread sleeps in the test (it wakes when the phase completes): under the power cap polling
+// costs clocks, 8192^3 took 10% longer with the products' issuer spinning.
 __device__ __forceinline__ bool wait_bar(uint64_t* b, uint32_t parity) {
-    if (mbar_try(b, parity) || mbar_try(b, parity)) return true;
-    return mbar_wait_sleep(b, parity, gtimer() + kWaitNs);
+    if (mbar_try_sleep(b, parity, 20000u)) return true;
+    const uint64_t deadline = gtimer() + kWaitNs;
+    while (!mbar_try_sleep(b, parity, 20000u))
+        if (gtimer() > deadline) return false;
+    return true;
 }
 
 // ------------------------------------------------------------------ 64-byte row segments
@@ -315,9 +323,16 @@ struct Shape {
     static constexpr int NP = KIND == kMix ? kMaxMix : 1;
     static constexpr int B_BYTES = PAIR ? kABytes : 2 * kABytes;
     static constexpr int STAGE = kABytes + B_BYTES;
-    static constexpr int STAGES = PAIR ? 6 : 4;
+    // Short reductions on pairs (an expert's few rows): a tile of D leaves through shared memory by
+    // TMA, 8 KB per epilogue warp, for which two stages of the ring go. The warps' own stores made
+    // the epilogue 3.7 k cycles per tile, more than the products of 170 rows (256 experts of 2048 x
+    // 768, 4096 tokens: both weight gradients 585 -> 523 us); with long reductions the two stages
+    // are worth more (8192^3 764 us with them, 809 without).
+    static constexpr bool TMA_OUT = EPI == kStoreBulk;
+    static constexpr int STAGES = PAIR && !TMA_OUT ? 6 : 4;
     static constexpr int RING = STAGES * STAGE;
-    static constexpr int STG = kEpiWarps * 2048;
+    static constexpr int STG_WARP = TMA_OUT ? 8192 : 2048;
+    static constexpr int STG = kEpiWarps * STG_WARP;
     static constexpr int SMEM = RING + STG + 256 + int(sizeof(Tables)) + 1024;
     static constexpr bool GATEUP = EPI == kGateUp || EPI == kGateUpI, DGATED = EPI == kDGated || EPI == kDGatedI;
     static constexpr bool IL = EPI == kGateUpI || EPI == kDGatedI;
@@ -644,11 +659,15 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                     const uint32_t sa = su32(smem + stage * S::STAGE), sb = sa + kABytes;
                     auto products = [&](auto a_mn) {
                         constexpr bool AMN = decltype(a_mn)::value;
-#pragma unroll
-                        for (int k = 0; k < kBR / 16; ++k) {
-                            if (AMN && k >= t.last && kb == t.nk - 1) break;
+                        auto step = [&](int k) {
                             mma<PAIR>(d0, operand<AMN>(sa + k * kStep<AMN>), operand<S::BMN>(sb + k * kStep<S::BMN>),
                                       desc, kb > kbeg || k > 0 ? 1u : 0u);
+                        };
+                        if (AMN && t.last < kBR / 16 && kb == t.nk - 1) {
+                            for (int k = 0; k < t.last; ++k) step(k);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < kBR / 16; ++k) step(k);
                         }
                     };
                     if (tn) products(std::true_type{});
@@ -708,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
     if (warp >= 2) {
         const int q = warp & 3;                    // TMEM lane quarter of this warp
         const int ch = (warp - 2) >> 2;            // column half
-        uint8_t* sm = stg + (warp - 2) * 2048;
+        uint8_t* sm = stg + (warp - 2) * S::STG_WARP;
         const int wrow = int(crank) * 128 + q * 32;  // first tile row of the warp
         uint32_t it = 0;
         // the warp's 32-column chunks of a tile (kGateUp: of its 128 units)
@@ -751,8 +770,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                 if (c0 < c1) fetch_pre(t, c0, vrows);
             if (!SPLIT && t.nk > 0) {
                 ++it;
-                if (!wait_bar(&acc_full[ab], ph)) {
-                    set_status(P.status, MOE_ERR_DEVICE_TIMEOUT);
+                const int ok = lane == 0 ? int(wait_bar(&acc_full[ab], ph)) : 0;  // one lane waits
+                if (!__shfl_sync(0xffffffffu, ok, 0)) {
+                    if (lane == 0) set_status(P.status, MOE_ERR_DEVICE_TIMEOUT);
                     return false;
                 }
                 fence_after();
@@ -938,6 +958,46 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                 }
                 if (P.partial && valid) P.partial[(row + lane) * P.parts + ((t.n0 / kCols) * splits + srank) * 2 + ch] = dw;
             } else if (tn) {
+                if constexpr (S::TMA_OUT) {
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the tile before
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint4 w[4];
+                        float f[32];
+                        if (t.nk > 0) {
+                            uint32_t dr[32];
+                            acc(4 * ch + c, dr);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(dr[j]);
+                        } else {  // an expert without rows: its gradient is zero
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) f[j] = 0.0f;
+                        }
+                        if (c == 3 && t.nk > 0) release();
+                        pack_row(f, w);
+                        // two boxes of 64 columns, 128-byte swizzle
+                        uint8_t* box = sm + (c >> 1) * 4096 + lane * 128;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<uint4*>(box + ((((c & 1) * 4 + j) ^ (lane & 7)) << 4)) = w[j];
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0 && rows > 0) {
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            const int col = t.n0 + 128 * ch + 64 * b;
+                            if (col < P.N)
+                                asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                                                 reinterpret_cast<uint64_t>(t.half ? &P.o1 : &P.o0)),
+                                             "r"(col), "r"(int(row)), "r"(t.e), "r"(su32(sm + b * 4096))
+                                             : "memory");
+                        }
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
+                    return true;
+                }
                 __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(t.half ? P.out1 : P.out) + t.e * P.so + row * P.ldo;
                 if constexpr (SPLIT) {
 #pragma unroll 1
@@ -1036,6 +1096,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
             for (int idx = tile0; idx < total; idx += tstep)
                 if (!epilogue(idx)) break;
         }
+        if constexpr (S::TMA_OUT)
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         __syncwarp();
     }
     fence_before();
@@ -1193,6 +1255,13 @@ bool map_b_n(CUtensorMap* m, const void* b, int64_t E, int64_t r, int64_t n, int
     return encode(m, b, 3, d, st, box);
 }
 
+// Planes [E][rows][n] of a weight gradient, written in boxes of 64 columns x 32 rows.
+bool map_out(CUtensorMap* m, const void* o, int64_t E, int64_t rows, int64_t n, int64_t ld, int64_t plane) {
+    const int64_t d[3] = {n, rows, E}, st[2] = {ld, E > 1 ? plane : rows * ld};
+    const int box[3] = {64, 32, 1};
+    return encode(m, o, 3, d, st, box);
+}
+
 // 256-row tiles on CTA pairs where they fill the GPU about as well as 128-row tiles.
 bool use_pair(const RowPlan& p, int64_t rows, int64_t n_blocks) {
     if (p.offsets) return p.S >= 384 * int64_t(p.E);
@@ -1311,6 +1380,10 @@ bool set_up(const GemmArgs& a, TcTrain& P, bool& pair, int64_t& tiles) {
         P.nk = int(blocks_of(a.R, kBR));
         if (!pair && !grouped) P.splits = splits_of(tiles, P.nk, 8, P.mrows);
         if (!a.out) return true;
+        P.bulk_out = pair && (grouped ? a.plan.S / a.plan.E : a.R) < 16 * kBR;
+        if (P.bulk_out && (!map_out(&P.o0, a.out, P.E, P.mrows, a.N, a.ldo, a.so) ||
+                     (P.halves > 1 && !map_out(&P.o1, a.out1, P.E, P.mrows, a.N, a.ldo, a.so))))
+            return false;
         return map_a(&P.a, a.a, rows, a.lda, P.mrows, P.halves, true) &&
                map_b_n(&P.b0, a.b, 1, rows, a.N, a.ldb, rows * a.ldb);
     }
@@ -1387,8 +1460,9 @@ cudaError_t launch_tc_gemms(const GemmArgs* a, int n, cudaStream_t s) {
     }
     for (int i = 0; i < n; ++i) {
         if (!a[i].out) continue;
-        const cudaError_t e = P[i].tn ? launch<kTN, kStore>(P[i], pair[i], tiles[i], s)
-                                      : launch<kNN, kStore>(P[i], pair[i], tiles[i], s);
+        const cudaError_t e = P[i].bulk_out ? launch_t<kTN, kStoreBulk, true, false>(&P[i], 1, tiles[i], s)
+                              : P[i].tn     ? launch<kTN, kStore>(P[i], pair[i], tiles[i], s)
+                                            : launch<kNN, kStore>(P[i], pair[i], tiles[i], s);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
