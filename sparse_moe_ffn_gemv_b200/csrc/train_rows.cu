@@ -444,8 +444,10 @@ __global__ void __launch_bounds__(256) colsum_finish_kernel(const ColsumArgs a0,
     *o = from_f<T>(s);
 }
 
+// dz of a block of rows, and its column sums: two rows of loads in flight per thread, four
+// blocks per SM.
 template <typename T>
-__global__ void __launch_bounds__(kColVecs * kColRows) dact_kernel(const DactArgs a, int splits) {
+__global__ void __launch_bounds__(kColVecs * kColRows, 4) dact_kernel(const DactArgs a, int splits) {
     constexpr int V = Vec<T>::N;
     constexpr bool FAST = V == 8;
     const int64_t per = (a.T + splits - 1) / splits;
@@ -454,10 +456,10 @@ __global__ void __launch_bounds__(kColVecs * kColRows) dact_kernel(const DactArg
     const int ry = threadIdx.x / kColVecs;
     float acc[V] = {};
     if (c < a.N) {
-        for (int64_t r = b + ry; r < end; r += 4 * kColRows) {
-            uint4 dv[4], zv[4];
+        for (int64_t r = b + ry; r < end; r += 2 * kColRows) {
+            uint4 dv[2], zv[2];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < 2; ++u) {
                 const int64_t ru = r + u * kColRows;
                 dv[u] = zv[u] = make_uint4(0, 0, 0, 0);
                 if (ru >= end) continue;
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(kColVecs * kColRows) dact_kernel(const DactArg
                     zv[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.pre) + ru * a.N + c);
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < 2; ++u) {
                 const int64_t ru = r + u * kColRows;
                 float f[V];
                 unpack_vec<T>(dv[u], f);
