@@ -145,6 +145,18 @@ FFN = [  # T, experts with rows (None: all), spec
     (777, 9, dict(num_experts=12, top_k=2, hidden=200, intermediate=328)),
     (900, None, dict(num_experts=4, top_k=3, hidden=320, intermediate=520, activation="swiglu_clamped")),
     (2100, None, dict(num_experts=2, top_k=1, hidden=264, intermediate=264)),
+    # large enough for the CTA-pair tiles, the token-wise copies and the bulk stores
+    (3001, None, dict(hidden=1096, intermediate=1160, has_expert_bias=True)),
+    (2900, None, dict(hidden=1288, intermediate=1032, gate_up_interleaved=True, has_expert_bias=True,
+                      activation="swiglu_clamped", swiglu_limit=1.0)),
+    (3000, None, dict(num_experts=5, top_k=3, hidden=1096, intermediate=712)),
+    (2500, None, dict(num_experts=4, top_k=2, hidden=1160, intermediate=520, gate_up_interleaved=True,
+                      has_expert_bias=True, activation="swiglu_clamped", swiglu_limit=1.0)),
+    (1500, 50, dict(num_experts=64, top_k=4, hidden=1032, intermediate=264, has_expert_bias=True)),
+    (1700, None, dict(num_experts=32, top_k=4, hidden=776, intermediate=328)),
+    (650, None, dict(num_experts=3, top_k=2, hidden=4200, intermediate=72, has_expert_bias=True)),
+    (700, None, dict(num_experts=2, top_k=2, hidden=8200, intermediate=40)),
+    (40, None, dict(num_experts=512, top_k=16, hidden=72, intermediate=40, has_expert_bias=True)),
     (16, None, dict(num_experts=8, top_k=2, act_dtype="f32")),
     (1, None, dict(hidden=100, intermediate=36, act_dtype="f32", has_expert_bias=True)),
     (150, None, dict(hidden=68, intermediate=132, act_dtype="f32", gate_up_interleaved=True, has_expert_bias=True,
@@ -193,6 +205,43 @@ def test_ffn_backward(T, experts, kw):
     assert all(torch.equal(got[n], again[n]) for n in got)  # no sum depends on the run
     less = op.backward(dy, x, w, pre, routing=routing, input_grad=False)
     assert "x" not in less and torch.equal(less["down_w"], got["down_w"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_ffn_one_expert_routed_is_the_dense_ffn(dtype):
+    """One expert with a routing in token order and weights of one: the dense form's result, up to
+    the rounding both may carry; and a permuted routing is the same function."""
+    spec = spec_of(hidden=136, intermediate=72, act_dtype=dtype)
+    g = gen(6)
+    T = 190
+    w, x, dy = planes(spec, g), rand(g, (T, 136), dtype), rand(g, (T, 136), dtype)
+    op = train.GatedFfn(spec)
+    want_y, want_pre = R.ffn_forward(x, w, spec, None, None)
+    off = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    order = torch.randperm(T, generator=g).to(torch.int32).cuda()
+    routing = (off, order, torch.ones(T, 1, device="cuda"))
+    y, pre = op.forward(x, w, routing=routing)
+    R.check(y, want_y, "y")
+    R.check(pre, tuple(t[order.long()] for t in want_pre), "pre")
+    got = op.backward(dy, x, w, pre, routing=routing)
+    ok(op)
+    want = R.ffn_backward(dy, x, w, pre, spec, routing)
+    for name in want:
+        R.check(got[name], want[name], name)
+
+
+def test_ffn_output_rows_may_be_strided():
+    spec = spec_of(num_experts=3, top_k=2, hidden=72, intermediate=40)
+    g = gen(7)
+    for T in (1, 4, 50):
+        w, x = planes(spec, g), rand(g, (T, 72), "bf16")
+        routing = R.make_routing(T, spec, g, "cuda")
+        op = train.GatedFfn(spec)
+        wide = torch.full((T, 88), 5.0, dtype=torch.bfloat16, device="cuda")
+        y, _ = op.forward(x, w, routing=routing, out=wide[:, 8:80])
+        assert y.data_ptr() == wide[:, 8:80].data_ptr()
+        R.check(y, R.ffn_forward(x, w, spec, routing, None)[0], "y")
+        assert (wide[:, :8] == 5).all() and (wide[:, 80:] == 5).all()
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -572,6 +621,44 @@ def steps():
     ]
 
 
+def test_refusals_name_the_tensor():
+    """Shapes, types and strides that the library would misread are refused before the call."""
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    lin = train.Linear(64, 128)
+    x, w = torch.zeros(5, 64, **bf), torch.zeros(128, 64, **bf)
+    for bad, name in ((dict(x=x.float()), "x"), (dict(x=x[:, :32]), "x"), (dict(x=torch.zeros(64, 5, **bf).t()), "x"),
+                      (dict(x=x.cpu()), "x"), (dict(w=w[:64]), "w"), (dict(w=torch.zeros(64, 128, **bf).t()), "w"),
+                      (dict(bias=torch.zeros(64, **bf)), "bias"), (dict(residual=torch.zeros(4, 128, **bf)), "residual"),
+                      (dict(out=torch.zeros(5, 64, **bf)), "out")):
+        with pytest.raises(ValueError, match=name):
+            lin.forward(**{**dict(x=x, w=w), **bad})
+    with pytest.raises(M.MoeError) as e:  # a row stride that is no multiple of 16 bytes
+        lin.forward(torch.zeros(5, 68, **bf)[:, :64], w)
+    assert e.value.name == "MOE_ERR_INVALID_ARGUMENT"
+    with pytest.raises(M.MoeError) as e:
+        lin.forward(torch.zeros(5, 72, **bf)[:, 1:65], w)  # rows that do not begin at 16 bytes
+    assert e.value.name == "MOE_ERR_INVALID_ARGUMENT"
+    with pytest.raises(M.MoeError) as e:
+        train.Linear(64, 128, activation="silu").backward(torch.zeros(5, 128, **bf), x, w)
+    assert e.value.name == "MOE_ERR_MISSING_TENSOR"
+    ffn = train.GatedFfn(spec_of(num_experts=2, top_k=1))
+    p = planes(ffn.spec, gen(1))
+    with pytest.raises(ValueError, match="routing"):
+        ffn.forward(x, p)
+    with pytest.raises(M.MoeError, match="down_w"):
+        ffn.forward(x, {k: v for k, v in p.items() if k != "down_w"}, routing=R.make_routing(5, ffn.spec, gen(1), "cuda"))
+    with pytest.raises(ValueError, match="bias"):
+        train.Norm(64).backward(x, x, w[0], torch.zeros(5, 2, device="cuda"), bias_grad=True)
+    for make in (lambda: train.Linear(64, 128, activation="relu"), lambda: train.Linear(64, 128, dtype="fp16"),
+                 lambda: train.Norm(64, kind="batch"), lambda: train.Linear(64, 128, device="cpu")):
+        with pytest.raises(ValueError):
+            make()
+    with pytest.raises(M.MoeError):
+        train.Linear(60, 128)
+    with pytest.raises(M.MoeError):
+        train.GatedFfn(spec_of(hidden=128, intermediate=64, weight_format="mxfp4", group_size=32))
+
+
 def test_calls_on_two_streams_at_once():
     calls = steps()
     want = [[t.clone() for t in c()] for _, c in calls]
@@ -620,6 +707,43 @@ def test_captured_and_replayed_in_two_graphs():
             torch.cuda.synchronize()
             for (name, _), o, w in zip(calls, outs, want):
                 assert all(torch.equal(a, b) for a, b in zip(o, w)), name
+
+
+def test_ffn_offsets_past_32_bits():
+    """Routed rows whose element offsets pass 2^31: 40,000 tokens in 8 slots each of 7168 values.
+    A few tokens are not zero; the others' rows and gradients are zeros."""
+    spec = spec_of(num_experts=9, top_k=8, hidden=7168, intermediate=64)
+    T = 40_000
+    g = gen(52)
+    w = planes(spec, g)
+    idx = (torch.arange(T)[:, None] + torch.arange(8)) % 9
+    routing = R.routing_of(idx, torch.rand(T, 8, generator=g), 9, "cuda")
+    rows = torch.tensor([0, 17, 20_001, 39_990, 39_999])
+    x = torch.zeros((T, 7168), dtype=torch.bfloat16, device="cuda")
+    dy = torch.zeros_like(x)
+    x[rows.cuda()], dy[rows.cuda()] = rand(g, (5, 7168), "bf16"), rand(g, (5, 7168), "bf16")
+    op = train.GatedFfn(spec)
+    y, pre = op.forward(x, w, routing=routing)
+    got = op.backward(dy, x, w, pre, routing=routing)
+    ok(op)
+    # the same five tokens alone
+    sub = R.routing_of(idx[rows], routing[2].cpu()[rows], 9, "cuda")
+    xs, dys = x[rows.cuda()], dy[rows.cuda()]
+    want_y, _ = R.ffn_forward(xs, w, spec, sub, None)
+    R.check(y[rows.cuda()], want_y, "y")
+    # their rows of pre (the pass's own input): sorted position of each of their slots
+    at = torch.empty(T * 8, dtype=torch.long)
+    at[routing[1].cpu().long()] = torch.arange(T * 8)
+    slots = sub[1].cpu().long()
+    pre_s = pre[at[rows[slots // 8] * 8 + slots % 8].cuda()]
+    want = R.ffn_backward(dys, xs, w, pre_s, spec, sub)
+    R.check(got["x"][rows.cuda()], want["x"], "x")
+    R.check(got["topk_w"][rows.cuda()], want["topk_w"], "topk_w")
+    for n in ("gate_w", "up_w", "down_w"):
+        R.check(got[n], want[n], n)
+    rest = torch.ones(T, dtype=torch.bool)
+    rest[rows] = False
+    assert not y[rest.cuda()].any() and not got["x"][rest.cuda()].any()
 
 
 def test_offsets_past_32_bits():
