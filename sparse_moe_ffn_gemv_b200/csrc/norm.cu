@@ -28,34 +28,6 @@ __device__ __forceinline__ float block_sum(float v, float* sm) {
     return s;
 }
 
-// Two f32 operations per instruction (sm_100): the backward pass is bound by issue slots as
-// much as by HBM.
-__device__ __forceinline__ uint64_t bits2(float2 a) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
-    return r;
-}
-__device__ __forceinline__ float2 pair2(uint64_t a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
-    return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
-    return pair2(r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-    return pair2(r);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-    return pair2(r);
-}
-
 // Sums of two values over the tpr threads of a row group (a multiple of 32), through red[warp].
 // One block barrier; calls in a row alternate between two arrays.
 __device__ __forceinline__ void group_sum2(float& x, float& y, int tpr, float2* red) {

@@ -102,6 +102,63 @@ __device__ __forceinline__ float linear_dact(int act, float z) {
     return 1.0f;
 }
 
+// Two f32 operations per instruction (sm_100), for the passes that are bound by issue slots as
+// much as by HBM.
+__device__ __forceinline__ uint64_t bits2(float2 a) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+    return r;
+}
+__device__ __forceinline__ float2 pair2(uint64_t a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return pair2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return pair2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return pair2(r);
+}
+
+// The hardware's exponential (base 2) and reciprocal: relative errors about 2^-22 and 2^-23.
+__device__ __forceinline__ float ex2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// min and max that keep a NaN (fminf and fmaxf return the other operand).
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// 1 / (1 + 2^(c z)) for two values, c = -alpha log2(e).
+__device__ __forceinline__ float2 logistic2(float2 z, float c) {
+    const float2 x = mul2(z, make_float2(c, c));
+    const float2 q = add2(make_float2(ex2_fast(x.x), ex2_fast(x.y)), make_float2(1.0f, 1.0f));
+    return make_float2(rcp_fast(q.x), rcp_fast(q.y));
+}
+
 // min(x, top) that keeps a NaN (fminf would return top).
 __device__ __forceinline__ float clamp_above(float x, float top) { return x > top ? top : x; }
 
@@ -131,6 +188,43 @@ __device__ __forceinline__ void gated_grad(int act, float g, float v, float limi
     h = gp * v1;
     hg = g > limit ? 0.0f : (p + alpha * gp * (1.0f - p)) * v1;
     hv = (v < -limit || v > limit) ? 0.0f : gp;
+}
+
+// gated_grad for two units at once, for results that are rounded to bf16 next (one call per unit
+// with the activation chosen inside took 55 issue slots per unit, this about 15; the epilogue
+// that calls it was longer than its product). cexp = -log2(e), or -alpha log2(e) clamped.
+template <bool CLAMPED>
+__device__ __forceinline__ void gated_grad2(float2 g, float2 v, float limit, float alpha, float cexp, float2& h, float2& hg,
+                                            float2& hv) {
+    float2 gc = g, v1 = v;
+    if constexpr (CLAMPED) {
+        gc = make_float2(min_nan(g.x, limit), min_nan(g.y, limit));
+        v1 = add2(make_float2(max_nan(min_nan(v.x, limit), -limit), max_nan(min_nan(v.y, limit), -limit)),
+                  make_float2(1.0f, 1.0f));
+    }
+    const float2 p = logistic2(gc, cexp);
+    const float2 gp = mul2(gc, p);
+    // p + alpha gp (1 - p)
+    const float2 w = fma2(make_float2(-gp.x, -gp.y), p, gp);
+    float2 t = CLAMPED ? fma2(w, make_float2(alpha, alpha), p) : add2(w, p);
+    h = mul2(gp, v1);
+    hg = mul2(t, v1);
+    hv = gp;
+    if constexpr (CLAMPED) {
+        if (g.x > limit) hg.x = 0.0f;
+        if (g.y > limit) hg.y = 0.0f;
+        if (fabsf(v.x) > limit) hv.x = 0.0f;
+        if (fabsf(v.y) > limit) hv.y = 0.0f;
+    }
+}
+template <bool CLAMPED>
+__device__ __forceinline__ float2 gated_h2(float2 g, float2 v, float limit, float cexp) {
+    if constexpr (CLAMPED) {
+        g = make_float2(min_nan(g.x, limit), min_nan(g.y, limit));
+        v = add2(make_float2(max_nan(min_nan(v.x, limit), -limit), max_nan(min_nan(v.y, limit), -limit)),
+                 make_float2(1.0f, 1.0f));
+    }
+    return mul2(mul2(g, logistic2(g, cexp)), v);
 }
 
 // Expert of padded row r: the last e with poff[e] <= r.

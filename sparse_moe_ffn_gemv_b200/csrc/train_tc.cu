@@ -100,7 +100,7 @@ struct TcTrain {
     void *out, *out1;
     int64_t ldo, so;
     int out_f32;
-    float limit, alpha;
+    float limit, alpha, cexp;
     __nv_bfloat16 *dgu, *hw;
     float* partial;         // kDGated: [rows, parts]
     int parts;
@@ -883,13 +883,22 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                             store_rows(sm, lane, w, pr + P.N + u0, P.ldp * 2, vrows, bytes);
                         }
                     }
+                    auto units = [&](auto clamped) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) g[j] = gated_h<true>(P.act, g[j], v[j], P.limit, P.alpha);
+                        for (int j = 0; j < 32; j += 2) {
+                            const float2 h = gated_h2<decltype(clamped)::value>(make_float2(g[j], g[j + 1]),
+                                                                                make_float2(v[j], v[j + 1]), P.limit, P.cexp);
+                            g[j] = h.x;
+                            g[j + 1] = h.y;
+                        }
+                    };
+                    if (P.act == MOE_ACT_SWIGLU) units(std::false_type{});
+                    else units(std::true_type{});
                     pack_row(g, w);
                     store_rows(sm, lane, w, static_cast<__nv_bfloat16*>(P.out) + row * P.ldo + u0, P.ldo * 2, vrows, bytes);
                 }
             } else if constexpr (S::DGATED) {
-                float dw = 0.0f;
+                float2 dw = make_float2(0.0f, 0.0f);
                 const bool valid = lane < vrows;
 #pragma unroll 1
                 for (int c = c0; c < c1; ++c) {
@@ -907,38 +916,44 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                     if (c == c1 - 1) release();
                     if (bytes <= 0 || rows <= 0) continue;
                     uint32_t o0[16], o1[16], oh[16];  // dg and dv (or alternating), w h
+                    auto units = [&](auto clamped, auto whole) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        float d[2], dg[2], dv[2], h[2];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int u = j + i;
-                            float g, v;
+                        for (int j = 0; j < 32; j += 2) {
+                            float2 g, v, h, hg, hv;
                             if constexpr (S::IL) {
-                                const uint32_t x = u < 16 ? a0[u] : a1[u - 16];
-                                g = bf16lo(x);
-                                v = bf16hi(x);
+                                const uint32_t xa = j < 16 ? a0[j % 16] : a1[j % 16], xb = j < 16 ? a0[j % 16 + 1] : a1[j % 16 + 1];
+                                g = make_float2(bf16lo(xa), bf16lo(xb));
+                                v = make_float2(bf16hi(xa), bf16hi(xb));
                             } else {
-                                g = i ? bf16hi(a0[u / 2]) : bf16lo(a0[u / 2]);
-                                v = i ? bf16hi(a1[u / 2]) : bf16lo(a1[u / 2]);
+                                g = make_float2(bf16lo(a0[j / 2]), bf16hi(a0[j / 2]));
+                                v = make_float2(bf16lo(a1[j / 2]), bf16hi(a1[j / 2]));
                             }
-                            float hg, hv;
-                            gated_grad<true>(P.act, g, v, P.limit, P.alpha, h[i], hg, hv);
-                            d[i] = __uint_as_float(dr[u]);
-                            if (8 * (j / 8) * 2 < bytes) dw += d[i] * h[i];  // columns past N hold no unit
-                            // rows without a slot are zeros: the weight gradients reduce over them
-                            dg[i] = valid ? d[i] * rs * hg : 0.0f;
-                            dv[i] = valid ? d[i] * rs * hv : 0.0f;
-                            h[i] = valid ? h[i] * rs : 0.0f;
+                            gated_grad2<decltype(clamped)::value>(g, v, P.limit, P.alpha, P.cexp, h, hg, hv);
+                            const float2 d = make_float2(__uint_as_float(dr[j]), __uint_as_float(dr[j + 1]));
+                            // columns past N hold no unit
+                            if (decltype(whole)::value || 8 * (j / 8) * 2 < bytes) dw = fma2(d, h, dw);
+                            const float2 dr2 = mul2(d, make_float2(rs, rs));
+                            const float2 dg = mul2(dr2, hg), dv = mul2(dr2, hv);
+                            h = mul2(h, make_float2(rs, rs));
+                            if constexpr (S::IL) {
+                                (j < 16 ? o0[j % 16] : o1[j % 16]) = pack2(dg.x, dv.x);
+                                (j < 16 ? o0[j % 16 + 1] : o1[j % 16 + 1]) = pack2(dg.y, dv.y);
+                            } else {
+                                o0[j / 2] = pack2(dg.x, dg.y);
+                                o1[j / 2] = pack2(dv.x, dv.y);
+                            }
+                            oh[j / 2] = pack2(h.x, h.y);
                         }
-                        if constexpr (S::IL) {
-                            (j < 16 ? o0[j % 16] : o1[j % 16]) = pack2(dg[0], dv[0]);
-                            (j < 16 ? o0[j % 16 + 1] : o1[j % 16 + 1]) = pack2(dg[1], dv[1]);
-                        } else {
-                            o0[j / 2] = pack2(dg[0], dg[1]);
-                            o1[j / 2] = pack2(dv[0], dv[1]);
-                        }
-                        oh[j / 2] = pack2(h[0], h[1]);
+                    };
+                    auto either = [&](auto whole) {
+                        if (P.act == MOE_ACT_SWIGLU) units(std::false_type{}, whole);
+                        else units(std::true_type{}, whole);
+                    };
+                    if (bytes >= 64) either(std::true_type{});
+                    else either(std::false_type{});
+                    if (vrows < 32 && !valid) {  // rows without a slot are zeros: the weight gradients reduce over them
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o0[j] = o1[j] = oh[j] = 0;
                     }
                     __nv_bfloat16* o = P.dgu + row * 2 * P.N;
                     const int64_t ldb = int64_t(P.N) * 4;
@@ -956,7 +971,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                     }
                     put(oh, P.hw + row * P.N + col, int64_t(P.N) * 2, bytes);
                 }
-                if (P.partial && valid) P.partial[(row + lane) * P.parts + ((t.n0 / kCols) * splits + srank) * 2 + ch] = dw;
+                if (P.partial && valid) P.partial[(row + lane) * P.parts + ((t.n0 / kCols) * splits + srank) * 2 + ch] = dw.x + dw.y;
             } else if (tn) {
                 if constexpr (S::TMA_OUT) {
                     if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the tile before
@@ -1484,6 +1499,7 @@ cudaError_t launch_tc_gateup(const GemmArgs& g, const GatedArgs& ga, cudaStream_
     P.act = ga.act;
     P.limit = ga.limit;
     P.alpha = ga.alpha;
+    P.cexp = -1.44269504f * (ga.act == MOE_ACT_SWIGLU ? 1.0f : ga.alpha);  // exp as a power of two
     P.pre = static_cast<__nv_bfloat16*>(ga.pre);
     P.ldp = 2 * ga.I;
     P.out = ga.h;
@@ -1516,6 +1532,7 @@ cudaError_t launch_tc_dgated(const GemmArgs& g, const GatedArgs& ga, float* part
     P.act = ga.act;
     P.limit = ga.limit;
     P.alpha = ga.alpha;
+    P.cexp = -1.44269504f * (ga.act == MOE_ACT_SWIGLU ? 1.0f : ga.alpha);  // exp as a power of two
     P.row_scale = ga.topk_w;
     P.pre = static_cast<__nv_bfloat16*>(ga.pre);
     P.ldp = 2 * ga.I;
