@@ -77,6 +77,7 @@ struct TcTrain {
     FastDiv d_tile, d_m, d_band, d_width, d_tail;  // see tile_of
     int tn;                 // kMix: a kTN product
     int bulk_out;           // host: kStoreBulk
+    int wide_a, wide_b;     // MN-major operand in boxes of two 64-column blocks (see map_mn)
     int splits;             // CTAs of a cluster that share a tile's reduction (SPLIT)
     // rows
     const int32_t *offsets, *poff, *uoff, *row_slot;  // grouped (offsets != null)
@@ -450,6 +451,22 @@ __device__ __forceinline__ void load4(void* dst, const CUtensorMap* m, uint64_t*
             : "memory");
 }
 
+// An MN-major operand tile of BYTES: columns from col on, 64 reduction rows from r on, of plane e.
+// `boxes`: 64-column boxes that are wanted (narrow maps), or 128-column ones (wide).
+template <bool PAIR, int BYTES>
+__device__ __forceinline__ void load_mn(uint8_t* dst, const CUtensorMap* m, int wide, int boxes, uint64_t* bar, uint32_t bar_c,
+                                        int col, int r, int e) {
+    if (wide) {
+#pragma unroll
+        for (int j = 0; j < BYTES / 16384; ++j)
+            if (j < boxes) load4<PAIR>(dst + j * 16384, m, bar, bar_c, 0, r, col / 64 + 2 * j, e);
+    } else {
+#pragma unroll
+        for (int j = 0; j < BYTES / 8192; ++j)
+            if (j < boxes) load4<PAIR>(dst + j * 8192, m, bar, bar_c, col + 64 * j, r, 0, e);
+    }
+}
+
 // SPLIT: the CTAs of a cluster share one tile, each a part of its reduction; their accumulators
 // meet in shared memory, where each CTA adds up a part of the columns (in rank order) and runs
 // the epilogue on it. For problems of fewer tiles than SMs.
@@ -567,9 +584,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                 const Tile t = tile_of<KIND, EPI, PAIR>(P, tb, local);
                 const int arow = int(t.row0) + 128 * int(crank);
                 // boxes of operand B that hold columns of D (the others' products are not taken)
-                constexpr int kBox = S::BMN ? 64 : 128;
-                const int boxes = PAIR || S::GATEUP ? S::B_BYTES / (kBox * kBR * 2) : (min(kCols, P.N - t.n0) + kBox - 1) / kBox;
-                const uint32_t bytes = (PAIR ? 2 : 1) * (kABytes + boxes * kBox * kBR * 2);
+                const int box = !S::BMN || P.wide_b ? 128 : 64;
+                const int boxes = PAIR || S::GATEUP ? S::B_BYTES / (box * kBR * 2) : (min(kCols, P.N - t.n0) + box - 1) / box;
+                const uint32_t bytes = (PAIR ? 2 : 1) * (kABytes + boxes * box * kBR * 2);
                 const int kend = kb_end(t);
                 for (int kb = kb_begin(t); kb < kend; ++kb) {
                     if (!wait_bar(&empty[stage], phase ^ 1u)) {
@@ -584,20 +601,13 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                     const int kc = (kb - half * P.nk_half) * kBR;
                     if (tn) {
                         const int r = int(t.r0) + kb * kBR;
-                        load3<PAIR>(sa, &P.a, &full[stage], fb, arow, t.half, r);
-                        load3<PAIR>(sa + 8192, &P.a, &full[stage], fb, arow + 64, t.half, r);
-                        const int nb = t.n0 + 128 * int(crank);
-#pragma unroll
-                        for (int j = 0; j < S::B_BYTES / 8192; ++j)
-                            if (j < boxes) load3<PAIR>(sb + j * 8192, &P.b0, &full[stage], fb, nb + 64 * j, r, 0);
+                        load_mn<PAIR, kABytes>(sa, &P.a, P.wide_a, 2, &full[stage], fb, arow, r, t.half);
+                        load_mn<PAIR, S::B_BYTES>(sb, &P.b0, P.wide_b, boxes, &full[stage], fb, t.n0 + 128 * int(crank), r, 0);
                     } else {
                         load3<PAIR>(sa, &P.a, &full[stage], fb, kc, half, arow);
                         if constexpr (S::BMN) {
-                            const CUtensorMap* mb = half && P.b_split ? &P.b1 : &P.b0;
-                            const int nb = t.n0 + 128 * int(crank);
-#pragma unroll
-                            for (int j = 0; j < S::B_BYTES / 8192; ++j)
-                                if (j < boxes) load3<PAIR>(sb + j * 8192, mb, &full[stage], fb, nb + 64 * j, kc, t.e);
+                            load_mn<PAIR, S::B_BYTES>(sb, half && P.b_split ? &P.b1 : &P.b0, P.wide_b, boxes, &full[stage], fb,
+                                                      t.n0 + 128 * int(crank), kc, t.e);
                         } else if constexpr (S::GATEUP) {
                             // gate rows, then up rows; of a pair, CTA 0 gate and CTA 1 up
                             if constexpr (PAIR) {
@@ -1251,11 +1261,22 @@ TcTrain base_of(const RowPlan& p) {
     return P;
 }
 
-// A as [rows][halves][cols of a half]: K-major boxes of 64 columns x 128 rows, MN-major 64 x 64.
-bool map_a(CUtensorMap* m, const void* a, int64_t rows, int64_t ld, int64_t cols, int halves, bool mn) {
+// A as [rows][halves][cols of a half], K-major boxes of 64 columns x 128 rows.
+bool map_a_k(CUtensorMap* m, const void* a, int64_t rows, int64_t ld, int64_t cols, int halves) {
     const int64_t d[3] = {cols, halves, rows}, st[2] = {halves > 1 ? cols : ld, ld};
-    const int box[3] = {64, 1, mn ? 64 : 128};
+    const int box[3] = {64, 1, 128};
     return encode(m, a, 3, d, st, box);
+}
+// MN-major operand of planes [E][r][n]: 64 x 64 boxes, whose inner row is one 128-byte swizzle
+// row. Where n is a multiple of 64 the columns are a dimension of blocks of their own, and one
+// copy brings two blocks: the producer's one thread issues a copy in about 100 cycles, and with
+// four per 512-cycle reduction block it starved the products (32 experts of 2880 x 2880: 8.3
+// blocks took 6.9 k cycles).
+bool map_mn(CUtensorMap* m, int& wide, const void* b, int64_t E, int64_t r, int64_t n, int64_t ld, int64_t plane) {
+    wide = n % 64 == 0;
+    const int64_t d[4] = {wide ? 64 : n, r, wide ? n / 64 : 1, E}, st[3] = {ld, 64, plane};
+    const int box[4] = {64, 64, wide ? 2 : 1, 1};
+    return encode(m, b, 4, d, st, box);
 }
 // Weight planes [E][rows][halves][K] as the K-major B operand.
 bool map_b_k(CUtensorMap* m, const void* b, int64_t E, int64_t rows, int halves, int64_t K) {
@@ -1263,13 +1284,6 @@ bool map_b_k(CUtensorMap* m, const void* b, int64_t E, int64_t rows, int halves,
     const int box[4] = {64, 1, 128, 1};
     return encode(m, b, 4, d, st, box);
 }
-// [E][r][n] as the MN-major B operand.
-bool map_b_n(CUtensorMap* m, const void* b, int64_t E, int64_t r, int64_t n, int64_t ld, int64_t plane) {
-    const int64_t d[3] = {n, r, E}, st[2] = {ld, plane};
-    const int box[3] = {64, 64, 1};
-    return encode(m, b, 3, d, st, box);
-}
-
 // Planes [E][rows][n] of a weight gradient, written in boxes of 64 columns x 32 rows.
 bool map_out(CUtensorMap* m, const void* o, int64_t E, int64_t rows, int64_t n, int64_t ld, int64_t plane) {
     const int64_t d[3] = {n, rows, E}, st[2] = {ld, E > 1 ? plane : rows * ld};
@@ -1399,8 +1413,8 @@ bool set_up(const GemmArgs& a, TcTrain& P, bool& pair, int64_t& tiles) {
         if (P.bulk_out && (!map_out(&P.o0, a.out, P.E, P.mrows, a.N, a.ldo, a.so) ||
                      (P.halves > 1 && !map_out(&P.o1, a.out1, P.E, P.mrows, a.N, a.ldo, a.so))))
             return false;
-        return map_a(&P.a, a.a, rows, a.lda, P.mrows, P.halves, true) &&
-               map_b_n(&P.b0, a.b, 1, rows, a.N, a.ldb, rows * a.ldb);
+        return map_mn(&P.a, P.wide_a, a.a, P.halves, rows, P.mrows, a.lda, P.halves > 1 ? P.mrows : rows * a.lda) &&
+               map_mn(&P.b0, P.wide_b, a.b, 1, rows, a.N, a.ldb, rows * a.ldb);
     }
     pair = use_pair(a.plan, a.M, P.n_blocks);
     const int64_t rows = grouped ? a.plan.max_rows : a.M;
@@ -1425,10 +1439,10 @@ bool set_up(const GemmArgs& a, TcTrain& P, bool& pair, int64_t& tiles) {
     P.b_split = halves > 1;
     if (!pair) P.splits = splits_of(tiles, P.nk, 8, row_hint(a.plan, a.M));
     if (!a.out) return true;
-    if (!map_a(&P.a, a.a, rows, a.lda, R, halves, false)) return false;
+    if (!map_a_k(&P.a, a.a, rows, a.lda, R, halves)) return false;
     if (a.kind == kNT) return map_b_k(&P.b0, a.b, E, a.N, 1, R);
-    return map_b_n(&P.b0, a.b, E, R, a.N, a.ldb, R * a.ldb) &&
-           (halves == 1 || map_b_n(&P.b1, a.b1, E, R, a.N, a.ldb, R * a.ldb));
+    return map_mn(&P.b0, P.wide_b, a.b, E, R, a.N, a.ldb, R * a.ldb) &&
+           (halves == 1 || map_mn(&P.b1, P.wide_b, a.b1, E, R, a.N, a.ldb, R * a.ldb));
 }
 
 }  // namespace
@@ -1504,7 +1518,7 @@ cudaError_t launch_tc_gateup(const GemmArgs& g, const GatedArgs& ga, cudaStream_
     P.ldp = 2 * ga.I;
     P.out = ga.h;
     P.ldo = ga.I;
-    if (!map_a(&P.a, g.a, rows, g.lda, g.R, 1, false) || !map_b_k(&P.b0, g.b, E, ga.I, ga.interleaved ? 2 : 1, g.R))
+    if (!map_a_k(&P.a, g.a, rows, g.lda, g.R, 1) || !map_b_k(&P.b0, g.b, E, ga.I, ga.interleaved ? 2 : 1, g.R))
         return cudaErrorInvalidValue;
     if (!ga.interleaved && !map_b_k(&P.b1, g.b1, E, ga.I, 1, g.R)) return cudaErrorInvalidValue;
     if (ga.interleaved) return launch<kNT, kGateUpI>(P, pair, tiles, s);
@@ -1540,7 +1554,7 @@ cudaError_t launch_tc_dgated(const GemmArgs& g, const GatedArgs& ga, float* part
     P.hw = static_cast<__nv_bfloat16*>(ga.hw);
     P.partial = partial;
     P.parts = dgated_parts(g.plan, ga.I, g.R);
-    if (!map_a(&P.a, g.a, rows, g.lda, g.R, 1, false) || !map_b_n(&P.b0, g.b, E, g.R, ga.I, g.ldb, g.sb))
+    if (!map_a_k(&P.a, g.a, rows, g.lda, g.R, 1) || !map_mn(&P.b0, P.wide_b, g.b, E, g.R, ga.I, g.ldb, g.sb))
         return cudaErrorInvalidValue;
     if (ga.interleaved) return launch<kNN, kDGatedI>(P, pair, tiles, s);
     return launch<kNN, kDGated>(P, pair, tiles, s);
