@@ -51,7 +51,8 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kMix = 3;  // besides enum GemmKind
 constexpr int kMaxMix = 3;
 // kStoreBulk: kTN on pairs, D leaves by TMA.
-enum Epi { kStore = 0, kGateUp = 1, kGateUpI = 2, kDGated = 3, kDGatedI = 4, kStoreBulk = 5 };
+// kStoreTall: pairs on tiles of 512 rows.
+enum Epi { kStore = 0, kGateUp = 1, kGateUpI = 2, kDGated = 3, kDGatedI = 4, kStoreBulk = 5, kStoreTall = 6 };
 
 // Division by a launch constant: n / d = umulhi(n, m) >> s for 0 <= n < 2^31 (m = ceil(2^(32+s) / d)
 // with 2^s < d <= 2^(s+1)), two instructions in place of a divide in every role's tile walk.
@@ -76,7 +77,7 @@ struct TcTrain {
     CUtensorMap o0, o1;     // kTN on pairs: the planes of D
     FastDiv d_tile, d_m, d_band, d_width, d_tail;  // see tile_of
     int tn;                 // kMix: a kTN product
-    int bulk_out;           // host: kStoreBulk
+    int bulk_out, tall;     // host: kStoreBulk, kStoreTall
     int wide_a, wide_b;     // MN-major operand in boxes of two 64-column blocks (see map_mn)
     int splits;             // CTAs of a cluster that share a tile's reduction (SPLIT)
     // rows
@@ -319,18 +320,25 @@ struct Tables {
 
 template <int KIND, int EPI, bool PAIR>
 struct Shape {
-    static constexpr int BM = PAIR ? 256 : 128;
+    // Tall: each CTA holds two 128-row halves of A against one half of B, 48 KB of operands per
+    // 1024 cycles of products in place of 32 KB per 512 (a CTA's copies bring about 64 bytes per
+    // cycle, so that the shorter tile has none to spare). Both accumulator sets belong to one
+    // tile: the epilogue of a half runs beside the next tile's products on the other.
+    static constexpr bool TALL = EPI == kStoreTall;
+    static constexpr int MH = TALL ? 2 : 1;             // 128-row halves per CTA
+    static constexpr int BM = (PAIR ? 256 : 128) * MH;
     static constexpr bool BMN = KIND != kNT;
     static constexpr int NP = KIND == kMix ? kMaxMix : 1;
     static constexpr int B_BYTES = PAIR ? kABytes : 2 * kABytes;
-    static constexpr int STAGE = kABytes + B_BYTES;
+    static constexpr int A_BYTES = MH * kABytes;
+    static constexpr int STAGE = A_BYTES + B_BYTES;
     // Short reductions on pairs (an expert's few rows): a tile of D leaves through shared memory by
     // TMA, 8 KB per epilogue warp, for which two stages of the ring go. The warps' own stores made
     // the epilogue 3.7 k cycles per tile, more than the products of 170 rows (256 experts of 2048 x
     // 768, 4096 tokens: both weight gradients 585 -> 523 us); with long reductions the two stages
     // are worth more (8192^3 764 us with them, 809 without).
     static constexpr bool TMA_OUT = EPI == kStoreBulk;
-    static constexpr int STAGES = PAIR && !TMA_OUT ? 6 : 4;
+    static constexpr int STAGES = PAIR && !TMA_OUT && !TALL ? 6 : 4;
     static constexpr int RING = STAGES * STAGE;
     static constexpr int STG_WARP = TMA_OUT ? 8192 : 2048;
     static constexpr int STG = kEpiWarps * STG_WARP;
@@ -586,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                 // boxes of operand B that hold columns of D (the others' products are not taken)
                 const int box = !S::BMN || P.wide_b ? 128 : 64;
                 const int boxes = PAIR || S::GATEUP ? S::B_BYTES / (box * kBR * 2) : (min(kCols, P.N - t.n0) + box - 1) / box;
-                const uint32_t bytes = (PAIR ? 2 : 1) * (kABytes + boxes * box * kBR * 2);
+                const uint32_t bytes = (PAIR ? 2 : 1) * (S::A_BYTES + boxes * box * kBR * 2);
                 const int kend = kb_end(t);
                 for (int kb = kb_begin(t); kb < kend; ++kb) {
                     if (!wait_bar(&empty[stage], phase ^ 1u)) {
@@ -594,17 +602,21 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                         break;
                     }
                     uint8_t* sa = smem + stage * S::STAGE;
-                    uint8_t* sb = sa + kABytes;
+                    uint8_t* sb = sa + S::A_BYTES;
                     const uint32_t fb = PAIR ? mapa_shared(&full[stage], 0) : 0u;
                     if (crank == 0) mbar_expect_tx(&full[stage], bytes);
                     const int half = S::BMN && !tn && kb >= P.nk_half ? 1 : 0;
                     const int kc = (kb - half * P.nk_half) * kBR;
                     if (tn) {
                         const int r = int(t.r0) + kb * kBR;
-                        load_mn<PAIR, kABytes>(sa, &P.a, P.wide_a, 2, &full[stage], fb, arow, r, t.half);
+#pragma unroll
+                        for (int h = 0; h < S::MH; ++h)
+                            load_mn<PAIR, kABytes>(sa + h * kABytes, &P.a, P.wide_a, 2, &full[stage], fb, arow + 256 * h, r, t.half);
                         load_mn<PAIR, S::B_BYTES>(sb, &P.b0, P.wide_b, boxes, &full[stage], fb, t.n0 + 128 * int(crank), r, 0);
                     } else {
-                        load3<PAIR>(sa, &P.a, &full[stage], fb, kc, half, arow);
+#pragma unroll
+                        for (int h = 0; h < S::MH; ++h)
+                            load3<PAIR>(sa + h * kABytes, &P.a, &full[stage], fb, kc, half, arow + 256 * h);
                         if constexpr (S::BMN) {
                             load_mn<PAIR, S::B_BYTES>(sb, half && P.b_split ? &P.b1 : &P.b0, P.wide_b, boxes, &full[stage], fb,
                                                       t.n0 + 128 * int(crank), kc, t.e);
@@ -650,7 +662,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                 const Tile t = tile_of<KIND, EPI, PAIR>(P, tb, local);
                 const int kbeg = kb_begin(t), kend = kb_end(t);
                 if (kbeg == kend) continue;
-                const uint32_t ab = it & 1u, ph = (it >> 1) & 1u;
+                // accumulator set (tall: of the first half) and its phase
+                const uint32_t ab = S::TALL ? 0u : it & 1u, ph = S::TALL ? it & 1u : (it >> 1) & 1u;
                 ++it;
                 if (!wait_bar(&acc_empty[ab], ph ^ 1u)) {
                     gave_up = true;
@@ -658,20 +671,17 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                 }
                 fence_after();
                 const uint32_t d0 = tmem + ab * kCols;
-                const uint32_t desc = idesc(tn, S::BMN, S::BM,
+                const uint32_t desc = idesc(tn, S::BMN, S::TALL ? 256 : S::BM,
                                             PAIR || S::GATEUP ? kCols : (min(kCols, P.N - t.n0) + 15) / 16 * 16);
-                for (int kb = kbeg; kb < kend; ++kb) {
-                    if (!wait_bar(&full[stage], phase)) {
-                        gave_up = true;
-                        break;
-                    }
-                    fence_after();
-                    const uint32_t sa = su32(smem + stage * S::STAGE), sb = sa + kABytes;
+                // the four (or last) 16-deep steps of one block for half h
+                auto block = [&](uint32_t st, int kb, int h) {
+                    const uint32_t sa = su32(smem + st * S::STAGE) + h * kABytes;
+                    const uint32_t sb = su32(smem + st * S::STAGE) + S::A_BYTES;
                     auto products = [&](auto a_mn) {
                         constexpr bool AMN = decltype(a_mn)::value;
                         auto step = [&](int k) {
-                            mma<PAIR>(d0, operand<AMN>(sa + k * kStep<AMN>), operand<S::BMN>(sb + k * kStep<S::BMN>),
-                                      desc, kb > kbeg || k > 0 ? 1u : 0u);
+                            mma<PAIR>(d0 + h * kCols, operand<AMN>(sa + k * kStep<AMN>),
+                                      operand<S::BMN>(sb + k * kStep<S::BMN>), desc, kb > kbeg || k > 0 ? 1u : 0u);
                         };
                         if (AMN && t.last < kBR / 16 && kb == t.nk - 1) {
                             for (int k = 0; k < t.last; ++k) step(k);
@@ -682,6 +692,56 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                     };
                     if (tn) products(std::true_type{});
                     else products(std::false_type{});
+                };
+                int kb = kbeg;
+                if constexpr (S::TALL) {
+                    // the first ring's worth of blocks on the first half before any on the second,
+                    // whose accumulators the epilogue of the tile before still reads
+                    const int head = min(kend, kbeg + S::STAGES);
+                    uint32_t st = stage, sp = phase;
+                    for (; kb < head; ++kb) {
+                        if (!wait_bar(&full[st], sp)) {
+                            gave_up = true;
+                            break;
+                        }
+                        fence_after();
+                        block(st, kb, 0);
+                        if (++st == S::STAGES) {
+                            st = 0;
+                            sp ^= 1u;
+                        }
+                    }
+                    if (gave_up) break;
+                    if (head == kend) commit<PAIR>(&acc_full[0]);
+                    if (!wait_bar(&acc_empty[1], ph ^ 1u)) {
+                        gave_up = true;
+                        break;
+                    }
+                    fence_after();
+                    for (kb = kbeg; kb < head; ++kb) {
+                        block(stage, kb, 1);
+                        commit<PAIR>(&empty[stage]);
+                        if (++stage == S::STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (head == kend) {
+                        commit<PAIR>(&acc_full[1]);
+                        continue;
+                    }
+                }
+                for (; kb < kend; ++kb) {
+                    if (!wait_bar(&full[stage], phase)) {
+                        gave_up = true;
+                        break;
+                    }
+                    fence_after();
+                    block(stage, kb, 0);
+                    if constexpr (S::TALL) {
+                        if (kb == kend - 1) commit<PAIR>(&acc_full[0]);
+                        block(stage, kb, 1);
+                    }
                     commit<PAIR>(&empty[stage]);
                     if (++stage == S::STAGES) {
                         stage = 0;
@@ -689,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                     }
                 }
                 if (gave_up) break;
-                commit<PAIR>(&acc_full[ab]);
+                commit<PAIR>(&acc_full[S::TALL ? 1 : ab]);
             }
             commit<PAIR>(drain);
             wait_bar(drain, 0);
@@ -738,7 +798,6 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
         const int q = warp & 3;                    // TMEM lane quarter of this warp
         const int ch = (warp - 2) >> 2;            // column half
         uint8_t* sm = stg + (warp - 2) * S::STG_WARP;
-        const int wrow = int(crank) * 128 + q * 32;  // first tile row of the warp
         uint32_t it = 0;
         // the warp's 32-column chunks of a tile (kGateUp: of its 128 units)
         constexpr int kChunks = S::GATEUP ? 4 : 8;
@@ -750,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
         }
         // kDGated: pre-activations of the next 32 columns (gate, up), one chunk ahead
         uint4 x0[4], x1[4];
-        auto fetch_pre = [&](const Tile& t, int c, int vrows) {
+        auto fetch_pre = [&](const Tile& t, int wrow, int c, int vrows) {
             const int col = t.n0 + 32 * c;
             const int bytes = (P.N - col) * 2;
             const __nv_bfloat16* pr = P.pre + (t.pos0 + wrow) * P.ldp;
@@ -762,7 +821,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                 fetch_rows(lane, x1, pr + P.N + col, P.ldp * 2, vrows, bytes);
             }
         };
-        auto epilogue = [&](int idx) -> bool {
+        auto epilogue = [&](int idx, int h) -> bool {
+            const int wrow = 256 * h + int(crank) * 128 + q * 32;  // first tile row of the warp
             int local;
             const TcTrain& P = problem(idx, local);
             const bool tn = KIND == kTN || (KIND == kMix && P.tn);
@@ -770,16 +830,16 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
             const int rows = min(32, t.limit - wrow);     // may be negative
             const int vrows = min(32, t.nvalid - wrow);
             const int64_t row = t.row0 + wrow;            // the warp's first row
-            const uint32_t ab = it & 1u, ph = (it >> 1) & 1u;
+            const uint32_t ab = S::TALL ? uint32_t(h) : it & 1u, ph = S::TALL ? it & 1u : (it >> 1) & 1u;
             float rs = 1.0f;
             if (!tn && P.offsets && P.row_scale && lane < vrows) {
                 const int slot = P.row_slot[row + lane];
                 rs = slot < 0 ? 0.0f : P.row_scale[slot];
             }
             if constexpr (S::DGATED)
-                if (c0 < c1) fetch_pre(t, c0, vrows);
+                if (c0 < c1) fetch_pre(t, wrow, c0, vrows);
             if (!SPLIT && t.nk > 0) {
-                ++it;
+                if (h == S::MH - 1) ++it;
                 const int ok = lane == 0 ? int(wait_bar(&acc_full[ab], ph)) : 0;  // one lane waits
                 if (!__shfl_sync(0xffffffffu, ok, 0)) {
                     if (lane == 0) set_status(P.status, MOE_ERR_DEVICE_TIMEOUT);
@@ -920,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                                              x0[2].x, x0[2].y, x0[2].z, x0[2].w, x0[3].x, x0[3].y, x0[3].z, x0[3].w};
                     const uint32_t a1[16] = {x1[0].x, x1[0].y, x1[0].z, x1[0].w, x1[1].x, x1[1].y, x1[1].z, x1[1].w,
                                              x1[2].x, x1[2].y, x1[2].z, x1[2].w, x1[3].x, x1[3].y, x1[3].z, x1[3].w};
-                    if (c + 1 < c1) fetch_pre(t, c + 1, vrows);
+                    if (c + 1 < c1) fetch_pre(t, wrow, c + 1, vrows);
                     uint32_t dr[32];
                     acc(c, dr);
                     if (c == c1 - 1) release();
@@ -1116,10 +1176,14 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
             return true;
         };
         if constexpr (SPLIT) {
-            if (tile0 < total) epilogue(tile0);
+            if (tile0 < total) epilogue(tile0, 0);
         } else {
-            for (int idx = tile0; idx < total; idx += tstep)
-                if (!epilogue(idx)) break;
+            for (int idx = tile0; idx < total; idx += tstep) {
+                bool ok = true;
+#pragma unroll 1
+                for (int h = 0; h < S::MH && ok; ++h) ok = epilogue(idx, h);
+                if (!ok) break;
+            }
         }
         if constexpr (S::TMA_OUT)
             if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -1236,9 +1300,11 @@ cudaError_t launch_t(const TcTrain* P, int np, int64_t max_tiles, cudaStream_t s
     return cudaGetLastError();
 }
 
-// The three forms of a product: split, pairs, or one CTA per tile.
+// The forms of a product: split, pairs (tall where P says so), or one CTA per tile.
 template <int KIND, int EPI>
 cudaError_t launch(const TcTrain& P, bool pair, int64_t max_tiles, cudaStream_t s) {
+    if constexpr (EPI == kStore)
+        if (P.tall) return launch_t<KIND, kStoreTall, true, false>(&P, 1, max_tiles, s);
     if (P.splits > 1) return launch_t<KIND, EPI, false, true>(&P, 1, max_tiles, s);
     return pair ? launch_t<KIND, EPI, true, false>(&P, 1, max_tiles, s)
                 : launch_t<KIND, EPI, false, false>(&P, 1, max_tiles, s);
@@ -1289,6 +1355,16 @@ bool map_out(CUtensorMap* m, const void* o, int64_t E, int64_t rows, int64_t n, 
     const int64_t d[3] = {n, rows, E}, st[2] = {ld, E > 1 ? plane : rows * ld};
     const int box[3] = {64, 32, 1};
     return encode(m, o, 3, d, st, box);
+}
+
+// 512-row tiles where their rounds over the GPU's pairs cost less, and the reduction is long: a
+// round of them takes about 1.94 rounds of 256-row tiles over 8192 (8192^3: 7 of 101 us against 14
+// of 52), 2.1 over 4096 (their epilogue hides less), and their number divides worse.
+bool use_tall(int64_t rows, int64_t halves, int64_t n_blocks, int64_t nk) {
+    const int64_t pairs = sms() / 2;
+    const int64_t tall = blocks_of(blocks_of(rows, 512) * halves * n_blocks, pairs);
+    const int64_t flat = blocks_of(blocks_of(rows, 256) * halves * n_blocks, pairs);
+    return nk >= 96 && 97 * tall < 50 * flat;
 }
 
 // 256-row tiles on CTA pairs where they fill the GPU about as well as 128-row tiles.
@@ -1366,7 +1442,7 @@ int band_of(int n, int other, int conc) {
 
 // Row tiles at most, and the dense problem's bands.
 int64_t row_grid(TcTrain& P, const RowPlan& p, bool pair) {
-    const int BM = pair ? 256 : 128;
+    const int BM = P.tall ? 512 : pair ? 256 : 128;
     P.m_blocks = int(p.offsets ? blocks_of(p.max_rows, BM) + (pair ? std::min<int64_t>(p.E, p.S) : 0)
                                : blocks_of(p.T, BM));
     const int conc = pair ? sms() / 2 : sms();
@@ -1399,7 +1475,8 @@ bool set_up(const GemmArgs& a, TcTrain& P, bool& pair, int64_t& tiles) {
         P.E = grouped ? a.plan.E : 1;
         const int64_t tiles256 = blocks_of(P.mrows, 256) * P.halves * P.n_blocks * P.E;
         pair = tiles256 >= sms() / 2;
-        P.m_blocks = int(blocks_of(P.mrows, pair ? 256 : 128));
+        P.tall = pair && !grouped && use_tall(P.mrows, P.halves, P.n_blocks, blocks_of(a.R, kBR));
+        P.m_blocks = int(blocks_of(P.mrows, P.tall ? 512 : pair ? 256 : 128));
         // an expert's tiles: one column block at a time; dense: as many as fill the GPU with every row block
         P.band = grouped ? 1 : band_of(P.n_blocks, P.m_blocks * P.halves, pair ? sms() / 2 : sms());
         set_bands(P, P.n_blocks, P.m_blocks * P.halves);
@@ -1421,6 +1498,7 @@ bool set_up(const GemmArgs& a, TcTrain& P, bool& pair, int64_t& tiles) {
     if (!grouped) P.rows = a.M;
     RowPlan rp = a.plan;
     rp.T = a.M;
+    P.tall = pair && !grouped && use_tall(a.M, 1, P.n_blocks, blocks_of(a.R, kBR));
     tiles = row_grid(P, rp, pair);
     P.bias0 = static_cast<const __nv_bfloat16*>(a.bias);
     P.sbias = a.sbias;

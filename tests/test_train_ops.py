@@ -44,6 +44,9 @@ LINEAR = [  # dtype, T, K, N, act, bias, residual, pad
     ("bf16", 1030, 328, 776, "silu", True, True, 24),
     ("bf16", 2049, 2048, 264, "gelu", True, False, 0),
     ("bf16", 4096, 512, 2304, "none", True, True, 0),
+    ("bf16", 4700, 6152, 1032, "silu", True, True, 8),   # long reductions on 512-row tiles: forward,
+    ("bf16", 4700, 1032, 6152, "none", False, False, 0),  # input gradient
+    ("bf16", 6200, 1800, 2600, "gelu", True, False, 8),   # and weight gradient
     ("f32", 1, 4, 4, "none", False, False, 0),
     ("f32", 1, 1028, 132, "gelu", True, True, 4),
     ("f32", 33, 100, 60, "silu", True, True, 4),
