@@ -103,8 +103,8 @@ cudaError_t launch_tc_gemm_nt(const GemmArgs& a, cudaStream_t s);
 cudaError_t launch_tc_gemms(const GemmArgs* a, int n, cudaStream_t s);
 
 // The forward products for at most kSmallT tokens, both types. (Weights cold, us, this / tensor
-// cores: 2048 x 2048 1 token 6.3 / 11.4, 4 tokens 10.3 / 11.5, 8 tokens 16.9 / 11.5; 3584 x 7168
-// 1 token 17.2 / 19.1, 4 tokens 28.5 / 19.1; a gated FFN of 2048 x 768 11.8, 19.1 and 32.6 / 22.3.)
+// cores: 2048 x 2048 1 token 6.3 / 11.4, 4 tokens 10.3 / 11.5, 8 tokens 16.9 / 11.5; a gated FFN of
+// 2048 x 768 1 token 11.8 / 22.3, 4 tokens 19.1 / 22.3, 8 tokens 32.6 / 22.3.)
 constexpr int kSmallT = 4;
 struct SmallArgs {
     int T = 0, K = 0, N = 0;  // N: outputs (gated: units)

@@ -19,11 +19,14 @@ namespace {
 constexpr int kSmallThreads = 256;
 
 // Vectors of up to U rounds of a row: lane's columns (w * 32 + lane) + 32 * ks * round.
+// A full SM of warps with few loads each beats half of one with many for the linear form (3584 x
+// 7168, weights cold: one token 14.3 -> 12.6 us, two 18.0 -> 14.4), not for the gated one (7168 x
+// 2048: 30.4 us with 8 loads per row, 35.2 with 2).
 template <typename T, int TT, bool GATED>
-__global__ void __launch_bounds__(kSmallThreads) small_kernel(const SmallArgs a) {
+__global__ void __launch_bounds__(kSmallThreads, GATED ? 1 : TT <= 2 ? 8 : 4) small_kernel(const SmallArgs a) {
     constexpr int V = Vec<T>::N;
     constexpr bool FAST = V == 8;
-    constexpr int R = GATED ? 2 : (TT <= 2 ? 1 : 2), U = TT == 1 ? 8 : TT == 2 ? 4 : 2;
+    constexpr int R = GATED ? 2 : (TT <= 2 ? 1 : 2), U = GATED ? 8 / TT : TT == 1 ? 4 : 2;
     __shared__ float part[8][TT * R];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ks = a.ks;                     // warps per row group
