@@ -259,7 +259,7 @@ moe_status moe_linear_forward(const moe_linear_desc* d, const void* x, int64_t l
     MOE_CHECK(stride(ldy, N, d->dtype));
     if (residual) MOE_CHECK(stride(ldr, N, d->dtype));
     MOE_CHECK(check_ws(ws, ws_bytes, linear_ws(d, T, false).total));
-    if (T <= kSmallT) {
+    if (small_form(T, int64_t(K) * N, d->dtype)) {
         SmallArgs a;
         a.T = int(T); a.K = K; a.N = N; a.dtype = d->dtype; a.act = d->activation;
         a.x = x; a.ldx = ldx; a.w = w; a.bias = bias;
@@ -385,7 +385,7 @@ moe_status moe_ffn_forward(const moe_config* cfg, const moe_weights* w, const vo
     MOE_CHECK(check_ws(ws, ws_bytes, L.total));
     cudaStream_t s = (cudaStream_t)stream;
     const RowPlan p = row_plan(f, expert_offsets, sorted_slot, ws, L, device_status);
-    if (dense && T <= kSmallT) {
+    if (dense && small_form(T, 3 * int64_t(f.K) * f.I, f.dtype)) {
         SmallArgs a;
         a.T = int(T); a.K = f.K; a.N = f.I; a.dtype = f.dtype;
         a.gated = true; a.interleaved = f.il; a.act = cfg->activation; a.limit = cfg->swiglu_limit;

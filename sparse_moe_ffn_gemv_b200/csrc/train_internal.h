@@ -102,10 +102,15 @@ cudaError_t launch_simt_gemm(const GemmArgs* a, int n, cudaStream_t s);
 cudaError_t launch_tc_gemm_nt(const GemmArgs& a, cudaStream_t s);
 cudaError_t launch_tc_gemms(const GemmArgs* a, int n, cudaStream_t s);
 
-// The forward products for at most kSmallT tokens, both types. (Weights cold, us, this / tensor
-// cores: 2048 x 2048 1 token 6.3 / 11.4, 4 tokens 10.3 / 11.5, 8 tokens 16.9 / 11.5; a gated FFN of
-// 2048 x 768 1 token 11.8 / 22.3, 4 tokens 19.1 / 22.3, 8 tokens 32.6 / 22.3.)
+// The forward products for a few tokens, both types.
 constexpr int kSmallT = 4;
+// Whether they take this form: one or two tokens, or up to four over at most 10 MB of weights
+// (weights cold, us, this / tensor cores: 2048 x 2048 1 token 6.2 / 11.4, 4 tokens 10.2 / 11.5;
+// 3584 x 7168 1 token 15.4 / 19.1, 2 tokens 20.3 / 19.1, 4 tokens 28.8 / 19.1; gated FFN 2048 x 768
+// 4 tokens 18.7 / 21.3, 7168 x 2048 2 tokens 37.5 / 39.4, 4 tokens 57.1 / 39.4).
+inline bool small_form(int64_t T, int64_t weights, int dtype) {
+    return T <= 2 || (T <= kSmallT && (dtype == MOE_DTYPE_F32 || weights <= 5 << 20));
+}
 struct SmallArgs {
     int T = 0, K = 0, N = 0;  // N: outputs (gated: units)
     int dtype = MOE_DTYPE_BF16;

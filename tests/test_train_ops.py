@@ -33,6 +33,9 @@ LINEAR = [  # dtype, T, K, N, act, bias, residual, pad
     ("bf16", 1, 8, 8, "none", False, False, 0),
     ("bf16", 1, 2880, 2048, "gelu", True, True, 8),
     ("bf16", 2, 72, 136, "silu", True, False, 16),
+    ("bf16", 3, 1032, 328, "gelu", True, True, 8),
+    ("bf16", 4, 2056, 776, "none", False, False, 0),
+    ("bf16", 4, 2304, 2304, "silu", True, True, 8),
     ("bf16", 7, 1000, 8, "none", True, True, 0),
     ("bf16", 8, 520, 776, "silu", False, True, 8),
     ("bf16", 17, 200, 264, "gelu", True, True, 8),
@@ -132,7 +135,11 @@ def planes(spec, g):
 FFN = [  # T, experts with rows (None: all), spec
     (1, None, dict()),
     (1, None, dict(hidden=2048, intermediate=768)),
+    (2, None, dict(hidden=1032, intermediate=520, has_expert_bias=True)),
     (3, None, dict(hidden=200, intermediate=72, has_expert_bias=True)),
+    (4, None, dict(hidden=264, intermediate=200, gate_up_interleaved=True, has_expert_bias=True,
+                   activation="swiglu_clamped", swiglu_limit=0.8)),
+    (4, None, dict(hidden=1544, intermediate=1160)),
     (8, None, dict(hidden=520, intermediate=264, gate_up_interleaved=True)),
     (65, None, dict(hidden=72, intermediate=136, activation="swiglu_clamped", swiglu_limit=0.7,
                     gate_up_interleaved=True, has_expert_bias=True)),
