@@ -1,10 +1,10 @@
 // train_simt.cu -- matrix products on the CUDA cores, for f32 operands (the tensor cores have
 // no 32-bit product) in every operand order the training operators need.
 //
-// 64 x 64 outputs per block, 32 reduction steps per shared-memory stage, a 4 x 4 register tile
-// per thread; the next stage's operands are loaded into registers (16-byte vectors) while the
-// current one is multiplied. The tile is small because f32 blocks are small (a launch of few tiles leaves
-// SMs idle sooner than it meets the FMA rate).
+// 4 x 4 outputs per thread, 64 x 64 per block, or 32 x 32 with the reduction shared by four groups
+// of threads where 64 x 64 gives fewer than two blocks per SM (a small f32 block is bound by
+// latency: 77 x 192 x 320 took 14.8 us on 10 blocks of 256 threads, 11.6 us on 30 of 64, 9.4 us on
+// 30 of four groups of 64). The operands of two more stages wait in registers.
 #include <algorithm>
 
 #include "train_dev.cuh"
@@ -13,36 +13,42 @@ namespace moe {
 
 namespace {
 
-constexpr int kBR = 32;
-
-// TD x TD threads, 4 x 4 outputs each.
-template <int TD> struct Shared {
-    float a[2][kBR][4 * TD + 4], b[2][kBR][4 * TD + 4];
+// TD x TD threads of 4 x 4 outputs each, in KG groups that take every KG-th stage of BR
+// reduction steps.
+template <int TD_, int KG_, int BR_> struct Form {
+    static constexpr int TD = TD_, KG = KG_, BR = BR_;
+    static constexpr int GROUP = TD * TD, THREADS = GROUP * KG, B = 4 * TD;
+    static constexpr int VECS = B * BR / 4 / GROUP;  // 16-byte vectors of an operand per thread and stage
+    struct Shared {
+        float a[KG][2][BR][B + 4], b[KG][2][BR][B + 4];
+    };
+    static_assert(sizeof(Shared) <= 48 * 1024 && GROUP * 16 * 4 * (KG - 1) <= int(sizeof(Shared)), "shared memory");
 };
 
-// One operand tile [4 TD i][32 r] as V 16-byte vectors per thread. RMAJOR: memory rows are
-// reduction indices (vectors along i), else vectors along r. at(i, r) gives a vector's address,
-// or null outside the operand (row lengths are multiples of 4, so a vector is in or out whole).
-template <int TD> constexpr int kVecs = 4 * TD * kBR / 4 / (TD * TD);
-template <int TD, bool RMAJOR, typename At>
-__device__ __forceinline__ void fetch(float4 (&v)[kVecs<TD>], At at) {
+// One operand tile [B i][BR r] as vectors. RMAJOR: memory rows are reduction indices (vectors
+// along i), else vectors along r. at(i, r) gives a vector's address, or null outside the operand
+// (row lengths are multiples of 4, so a vector is in or out whole).
+template <typename F, bool RMAJOR, typename At>
+__device__ __forceinline__ void fetch(float4 (&v)[F::VECS], int tid, At at) {
+    constexpr int Q = F::BR / 4;
 #pragma unroll
-    for (int q = 0; q < kVecs<TD>; ++q) {
-        const int idx = threadIdx.x + q * TD * TD;
-        const int i = RMAJOR ? idx % TD * 4 : idx / 8, r = RMAJOR ? idx / TD : idx % 8 * 4;
+    for (int q = 0; q < F::VECS; ++q) {
+        const int idx = tid + q * F::GROUP;
+        const int i = RMAJOR ? idx % F::TD * 4 : idx / Q, r = RMAJOR ? idx / F::TD : idx % Q * 4;
         const float* p = at(i, r);
         v[q] = p ? *reinterpret_cast<const float4*>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 }
-template <int TD, bool RMAJOR>
-__device__ __forceinline__ void stash(float (&sm)[kBR][4 * TD + 4], const float4 (&v)[kVecs<TD>]) {
+template <typename F, bool RMAJOR>
+__device__ __forceinline__ void stash(float (&sm)[F::BR][F::B + 4], int tid, const float4 (&v)[F::VECS]) {
+    constexpr int Q = F::BR / 4;
 #pragma unroll
-    for (int q = 0; q < kVecs<TD>; ++q) {
-        const int idx = threadIdx.x + q * TD * TD;
+    for (int q = 0; q < F::VECS; ++q) {
+        const int idx = tid + q * F::GROUP;
         if (RMAJOR) {
-            *reinterpret_cast<float4*>(&sm[idx / TD][idx % TD * 4]) = v[q];
+            *reinterpret_cast<float4*>(&sm[idx / F::TD][idx % F::TD * 4]) = v[q];
         } else {
-            const int i = idx / 8, r = idx % 8 * 4;
+            const int i = idx / Q, r = idx % Q * 4;
             sm[r][i] = v[q].x;
             sm[r + 1][i] = v[q].y;
             sm[r + 2][i] = v[q].z;
@@ -51,8 +57,9 @@ __device__ __forceinline__ void stash(float (&sm)[kBR][4 * TD + 4], const float4
     }
 }
 
-template <int TD, int KIND>
-__device__ __forceinline__ void simt_tile(const GemmArgs& a, int64_t m0, int64_t n0, int z, Shared<TD>& sh) {
+template <typename F, int KIND>
+__device__ __forceinline__ void simt_tile(const GemmArgs& a, int64_t m0, int64_t n0, int z, typename F::Shared& sh) {
+    constexpr int TD = F::TD;
     constexpr bool AR = KIND == kTN, BR = KIND != kNT;  // operand rows are reduction indices
     const RowPlan& p = a.plan;
     const bool grouped = p.offsets != nullptr;
@@ -72,14 +79,15 @@ __device__ __forceinline__ void simt_tile(const GemmArgs& a, int64_t m0, int64_t
     const float* A = static_cast<const float*>(a.a);
     const float* B = static_cast<const float*>(a.b) + int64_t(e) * (KIND == kTN ? 0 : a.sb);
     const float* B1 = a.b1 ? static_cast<const float*>(a.b1) + int64_t(e) * a.sb : nullptr;
+    const int g = threadIdx.x / F::GROUP, tid = threadIdx.x % F::GROUP;
     // two stages of operands in registers ahead of the one in shared memory
-    float4 va[2][kVecs<TD>], vb[2][kVecs<TD>];
-    auto fetch_ab = [&](float4 (&xa)[kVecs<TD>], float4 (&xb)[kVecs<TD>], int64_t rb) {
-        fetch<TD, AR>(xa, [&](int i, int r) -> const float* {
+    float4 va[2][F::VECS], vb[2][F::VECS];
+    auto fetch_ab = [&](float4 (&xa)[F::VECS], float4 (&xb)[F::VECS], int64_t rb) {
+        fetch<F, AR>(xa, tid, [&](int i, int r) -> const float* {
             const int64_t gi = m0 + i, gr = rb + r;
             return gi < M && gr < R ? A + (AR ? gr * a.lda + gi : gi * a.lda + gr) : nullptr;
         });
-        fetch<TD, BR>(xb, [&](int i, int r) -> const float* {
+        fetch<F, BR>(xb, tid, [&](int i, int r) -> const float* {
             const int64_t gi = n0 + i, gr = rb + r;
             if (gi >= a.N || gr >= R) return nullptr;
             if (KIND == kNN && a.split && gr >= a.split) return B1 + (gr - a.split) * a.ldb + gi;
@@ -88,21 +96,23 @@ __device__ __forceinline__ void simt_tile(const GemmArgs& a, int64_t m0, int64_t
         });
     };
     float acc[4][4] = {};
-    const int ty = threadIdx.x / TD, tx = threadIdx.x % TD;
-    fetch_ab(va[0], vb[0], r0);
-    fetch_ab(va[1], vb[1], r0 + kBR);
-    for (int64_t r = r0; r < R; r += 2 * kBR) {
+    const int ty = tid / TD, tx = tid % TD;
+    constexpr int64_t step = int64_t(F::KG) * F::BR;  // of one stage of every group
+    const int64_t rg = r0 + g * F::BR;
+    fetch_ab(va[0], vb[0], rg);
+    fetch_ab(va[1], vb[1], rg + step);
+    for (int64_t r = r0; r < R; r += 2 * step) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             // one barrier per stage: the other buffer's readers are past the barrier before it
-            stash<TD, AR>(sh.a[h], va[h]);
-            stash<TD, BR>(sh.b[h], vb[h]);
+            stash<F, AR>(sh.a[g][h], tid, va[h]);
+            stash<F, BR>(sh.b[g][h], tid, vb[h]);
             __syncthreads();
-            fetch_ab(va[h], vb[h], r + (2 + h) * kBR);
+            fetch_ab(va[h], vb[h], r + g * F::BR + (2 + h) * step);
 #pragma unroll 8
-            for (int q = 0; q < kBR; ++q) {
-                const float4 x = *reinterpret_cast<const float4*>(&sh.a[h][q][ty * 4]);
-                const float4 y = *reinterpret_cast<const float4*>(&sh.b[h][q][tx * 4]);
+            for (int q = 0; q < F::BR; ++q) {
+                const float4 x = *reinterpret_cast<const float4*>(&sh.a[g][h][q][ty * 4]);
+                const float4 y = *reinterpret_cast<const float4*>(&sh.b[g][h][q][tx * 4]);
                 const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -110,6 +120,23 @@ __device__ __forceinline__ void simt_tile(const GemmArgs& a, int64_t m0, int64_t
                     for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xs[i], ys[j], acc[i][j]);
             }
         }
+    }
+    if constexpr (F::KG > 1) {  // the groups' sums in order, through shared memory
+        float4* part = reinterpret_cast<float4*>(&sh);
+        __syncthreads();
+        if (g > 0)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                part[((g - 1) * 4 + i) * F::GROUP + tid] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        __syncthreads();
+        if (g > 0) return;
+#pragma unroll
+        for (int j = 0; j < F::KG - 1; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 v = part[(j * 4 + i) * F::GROUP + tid];
+                acc[i][0] += v.x; acc[i][1] += v.y; acc[i][2] += v.z; acc[i][3] += v.w;
+            }
     }
     const int64_t n = n0 + tx * 4;
     if (n >= a.N) return;
@@ -158,10 +185,10 @@ struct Simt {
 
 // FWD: every problem is kNT; else kNN and kTN (one kernel per pass keeps its code small: a tiny
 // launch spends much of its time fetching instructions).
-template <int TD, bool FWD>
-__global__ void __launch_bounds__(TD * TD) simt_gemm_kernel(const __grid_constant__ Simt S) {
-    __shared__ Shared<TD> sh;
-    constexpr int kBM = 4 * TD, kBN = 4 * TD;
+template <typename F, bool FWD>
+__global__ void __launch_bounds__(F::THREADS) simt_gemm_kernel(const __grid_constant__ Simt S) {
+    __shared__ typename F::Shared sh;
+    constexpr int kBM = F::B, kBN = F::B;
     int64_t t = blockIdx.x;
     int i = 0;
     while (i < S.n - 1 && t >= S.end[i]) ++i;
@@ -170,14 +197,14 @@ __global__ void __launch_bounds__(TD * TD) simt_gemm_kernel(const __grid_constan
     const int64_t mt = t % S.tx[i], r = t / S.tx[i];
     const int nt = int(r % S.ty[i]), z = int(r / S.ty[i]);
     const GemmArgs& a = S.p[i];
-    if constexpr (FWD) simt_tile<TD, kNT>(a, mt * kBM, int64_t(nt) * kBN, z, sh);
-    else if (a.kind == kNN) simt_tile<TD, kNN>(a, mt * kBM, int64_t(nt) * kBN, z, sh);
-    else simt_tile<TD, kTN>(a, mt * kBM, int64_t(nt) * kBN, z, sh);
+    if constexpr (FWD) simt_tile<F, kNT>(a, mt * kBM, int64_t(nt) * kBN, z, sh);
+    else if (a.kind == kNN) simt_tile<F, kNN>(a, mt * kBM, int64_t(nt) * kBN, z, sh);
+    else simt_tile<F, kTN>(a, mt * kBM, int64_t(nt) * kBN, z, sh);
 }
 
-template <int TD>
-cudaError_t launch_td(Simt& S, cudaStream_t s) {
-    constexpr int B = 4 * TD;
+template <typename F>
+cudaError_t launch_form(Simt& S, cudaStream_t s) {
+    constexpr int B = F::B;
     int64_t tiles = 0;
     for (int i = 0; i < S.n; ++i) {
         const GemmArgs& a = S.p[i];
@@ -189,8 +216,8 @@ cudaError_t launch_td(Simt& S, cudaStream_t s) {
         S.end[i] = tiles;
     }
     if (tiles >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-    if (S.p[0].kind == kNT) simt_gemm_kernel<TD, true><<<unsigned(tiles), TD * TD, 0, s>>>(S);
-    else simt_gemm_kernel<TD, false><<<unsigned(tiles), TD * TD, 0, s>>>(S);
+    if (S.p[0].kind == kNT) simt_gemm_kernel<F, true><<<unsigned(tiles), F::THREADS, 0, s>>>(S);
+    else simt_gemm_kernel<F, false><<<unsigned(tiles), F::THREADS, 0, s>>>(S);
     return cudaGetLastError();
 }
 
@@ -206,7 +233,7 @@ cudaError_t launch_simt_gemm(const GemmArgs* a, int n, cudaStream_t s) {
         const int64_t rows = a[i].kind != kTN && grouped ? a[i].plan.S : a[i].M;
         tiles += ((rows + 63) / 64) * ((a[i].N + 63) / 64) * (a[i].kind == kTN && grouped ? a[i].plan.E : 1);
     }
-    return tiles >= 2 * 148 ? launch_td<16>(S, s) : launch_td<8>(S, s);
+    return tiles >= 2 * 148 ? launch_form<Form<16, 1, 32>>(S, s) : launch_form<Form<8, 4, 16>>(S, s);
 }
 
 }  // namespace moe
