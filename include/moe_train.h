@@ -25,7 +25,8 @@
  * size is 0.
  *
  * device_status (optional, caller-owned int32 on the device, zeroed by the caller) receives
- * MOE_ERR_DEVICE_CHECK (a slot id or an offset out of range; such rows are dropped) or
+ * MOE_ERR_DEVICE_CHECK (a slot id or an offset out of range: such rows are dropped; or a slot
+ * that stands twice, seen where y or du is computed: the results are not valid) or
  * MOE_ERR_DEVICE_TIMEOUT (a bounded wait gave up; the results are not valid). The first
  * error stays.
  *

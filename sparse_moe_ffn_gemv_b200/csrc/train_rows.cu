@@ -84,6 +84,10 @@ __device__ __forceinline__ void zero_row(const GatherArgs& a, int r, int lane) {
             for (int64_t c = lane; c < vpr; c += 32) static_cast<uint4*>(a.dst[j])[int64_t(r) * vpr + c] = make_uint4(0, 0, 0, 0);
 }
 
+// A slot that stands twice among the sorted ones has two rows, and slot_row names one of them. The
+// other is dropped: whether row r, of that slot, is one.
+__device__ __forceinline__ bool is_repeat(const RowPlan& p, int r, int slot) { return slot >= 0 && p.slot_row[slot] != r; }
+
 // Few rows: the plan and the copies in one launch, a warp per padded row. Padding is zeroed as
 // far as a reduction over the expert's rows reads; rows of dropped slots are zeros too.
 __global__ void __launch_bounds__(kGatherThreads) gather_padded_kernel(const GatherArgs a) {
@@ -173,6 +177,8 @@ __global__ void __launch_bounds__(kCopyWarps * 32) copy_tokens_kernel(const Gath
             __syncwarp();
             if (!mbar_try(&full[warp], phase) && !mbar_wait(&full[warp], phase, gtimer() + 2000000000ull)) {
                 set_status(p.status, MOE_ERR_DEVICE_TIMEOUT);
+                mbar_wait(&full[warp], phase, gtimer() + 2000000000ull);  // its copies may still land
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
                 return;
             }
             phase ^= 1u;
@@ -217,12 +223,25 @@ __global__ void __launch_bounds__(kCopyWarps * 32) copy_tokens_kernel(const Gath
             }
         }
     }
+    // rows that no token names (a slot that stands twice): zeros, and of no slot
+    const int total = pad[p.E], step = gridDim.x * blockDim.x;
+    for (int r0 = blockIdx.x * blockDim.x + threadIdx.x - lane; r0 < total; r0 += step) {
+        const bool repeat = is_repeat(p, r0 + lane, p.row_slot[r0 + lane]);
+        if (repeat) {
+            p.row_slot[r0 + lane] = -1;
+            set_status(p.status, MOE_ERR_DEVICE_CHECK);
+        }
+        for (unsigned m = __ballot_sync(0xffffffffu, repeat); m; m &= m - 1) zero_row(a, r0 + __ffs(m) - 1, lane);
+    }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-// Each token's slots' rows added in slot order in f32.
+// Each token's slots' rows added in slot order in f32. (gather_padded_kernel cannot see a slot that
+// stands twice, since its blocks plan side by side: it shows here.)
 template <typename T>
 __global__ void __launch_bounds__(256) sum_slots_kernel(const SumSlotsArgs a) {
+    for (int r = blockIdx.x * 256 + threadIdx.x; r < a.plan.poff[a.plan.E]; r += gridDim.x * 256)
+        if (is_repeat(a.plan, r, a.plan.row_slot[r])) set_status(a.plan.status, MOE_ERR_DEVICE_CHECK);
     constexpr int V = Vec<T>::N;
     const int vpr = a.K / V;
     const int64_t n = a.plan.T * vpr;

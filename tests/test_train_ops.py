@@ -402,6 +402,39 @@ def test_ffn_bad_permutations_are_reported():
     assert op.device_status() == 0  # read and cleared
 
 
+@pytest.mark.parametrize("T,width,kw", [
+    (20, 64, {}), (20, 64, dict(has_expert_bias=True)), (2100, 1024, {}), (2100, 1024, dict(has_expert_bias=True)),
+    (20, 64, dict(act_dtype="f32")), (2100, 1024, dict(act_dtype="f32", has_expert_bias=True)),
+])
+def test_ffn_slot_that_stands_twice_is_reported(T, width, kw):
+    """One slot in place of another: the status says so, the other tokens keep their results, and
+    no value that was in the workspace before gets into a gradient."""
+    spec = spec_of(num_experts=4, top_k=2, hidden=width, intermediate=64, **kw)
+    g = gen(15)
+    off, ss, wts = R.make_routing(T, spec, g, "cuda")
+    w, x, dy = planes(spec, g), rand(g, (T, width), spec.act_dtype), rand(g, (T, width), spec.act_dtype)
+    op = train.GatedFfn(spec)
+    want, _ = op.forward(x, w, routing=(off, ss, wts))
+    ok(op)
+    bad = ss.clone()
+    bad[11] = bad[int(off[2]) + 3]
+    gone = torch.tensor([int(bad[11]) // 2, int(ss[11]) // 2])
+    keep = torch.ones(T, dtype=torch.bool)
+    keep[gone] = False
+    for _ in range(2):
+        poison = torch.full((1 << 26,), float("nan"), device="cuda")  # what the next workspace holds
+        del poison
+        y, pre = op.forward(x, w, routing=(off, bad, wts))
+        assert op.device_status() == M.STATUS_CODE["MOE_ERR_DEVICE_CHECK"]
+        assert torch.equal(y[keep.cuda()], want[keep.cuda()])
+        poison = torch.full((1 << 26,), float("nan"), device="cuda")
+        del poison
+        got = op.backward(dy, x, w, torch.nan_to_num(pre), routing=(off, bad, wts))
+        assert op.device_status() == M.STATUS_CODE["MOE_ERR_DEVICE_CHECK"]
+        for name, t in got.items():
+            assert torch.isfinite(t).all(), name
+
+
 # ------------------------------------------------------------------ norm
 NORM = [  # dtype, T, H, kind, bias, pad
     ("bf16", 1, 8, "rms", False, 0), ("bf16", 1, 3584, "rms", False, 0), ("bf16", 3, 64, "layer", True, 8),
