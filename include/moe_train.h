@@ -20,7 +20,12 @@
  * bytes); everything else is contiguous. Pointers are 16-byte aligned, row lengths multiples
  * of 16 bytes. Row indices and offsets are 64-bit throughout.
  *
- * Workspace: ws of at least the matching *_workspace_size bytes, any contents. Calls that may
+ * Outputs overlap no input of the call and no other output, except that y may be the residual's
+ * tensor (linear, ffn), u (ffn) or x (norm) with its stride. Rows against rows are checked
+ * (MOE_ERR_INVALID_ARGUMENT); side by side in wider rows is fine. Widths above 2^28, more than
+ * 2^30 rows or slots, and tensors above 2^46 elements are refused (MOE_ERR_SHAPE_OVERFLOW).
+ *
+ * Workspace: ws of at least the matching *_workspace_size bytes for that T, any contents. Calls that may
  * overlap on the GPU (two streams, two graphs) each need their own. NULL is accepted where the
  * size is 0.
  *
@@ -59,8 +64,7 @@ MOE_API moe_status moe_linear_workspace_size(const moe_linear_desc *d, int64_t T
 
 /* y [T, N] = act(x W^T + bias) + residual. x [T, K] with row stride ldx, w [N, K], bias [N]
  * or NULL, residual [T, N] with row stride ldr or NULL, y with row stride ldy. pre (optional,
- * [T, N] contiguous) receives z, which the backward pass of an activation needs. y may be
- * the residual's buffer; it may not overlap x. */
+ * [T, N] contiguous) receives z, which the backward pass of an activation needs. */
 MOE_API moe_status moe_linear_forward(const moe_linear_desc *d, const void *x, int64_t ldx, const void *w,
                                       const void *bias, const void *residual, int64_t ldr, int64_t T, void *y,
                                       int64_t ldy, void *pre, void *ws, size_t ws_bytes, int32_t *device_status,
@@ -95,8 +99,8 @@ typedef struct moe_ffn_grads {
 MOE_API moe_status moe_ffn_workspace_size(const moe_config *cfg, int64_t T, int32_t backward, size_t *bytes);
 
 /* y [T, K] (row stride ldy) from u [T, K] (row stride ldu), plus residual [T, K] (row stride
- * ldr) or NULL. pre (optional) is kept for the backward pass; its rows of dropped slots are
- * not written. bf16: h is rounded to bf16 before the down product (the operand type of the
+ * ldr) or NULL. pre (optional) is kept for the backward pass; its rows behind the last sorted
+ * position (slots that moe_permute dropped) are not written. bf16: h is rounded to bf16 before the down product (the operand type of the
  * matrix instructions); the slots' weighted output rows are summed in f32. */
 MOE_API moe_status moe_ffn_forward(const moe_config *cfg, const moe_weights *w, const void *u, int64_t ldu,
                                    int64_t T, const int32_t *expert_offsets, const int32_t *sorted_slot,
@@ -108,7 +112,9 @@ MOE_API moe_status moe_ffn_forward(const moe_config *cfg, const moe_weights *w, 
  * (routed; may be NULL) and the gradients of the planes, [E, rows, cols] like the planes
  * (experts without rows get zeros). Required gradients: those of the planes that the config
  * has; du may be NULL. The activations are recomputed from pre. bf16: dg, dv and w h are
- * rounded to bf16 before their products; the slots' rows of du are summed in f32. T == 0 clears the gradients. */
+ * rounded to bf16 before their products; the slots' rows of du are summed in f32; dtopk_w keeps the
+ * matrix instructions' truncated additions (up to 3e-6 of its value low). T == 0 clears the
+ * gradients. */
 MOE_API moe_status moe_ffn_backward(const moe_config *cfg, const moe_weights *w, const void *u, int64_t ldu,
                                     int64_t T, const int32_t *expert_offsets, const int32_t *sorted_slot,
                                     const float *topk_w, const void *pre, const void *dy, int64_t lddy, void *du,
@@ -128,7 +134,7 @@ typedef struct moe_norm_desc {
 MOE_API moe_status moe_norm_workspace_size(const moe_norm_desc *d, int64_t T, int32_t backward, size_t *bytes);
 
 /* y [T, H] (row stride ldy) from x [T, H] (row stride ldx), w [H], b [H] or NULL (layer norm
- * only). stats [T, 2] f32 (optional): mean (0 for RMS) and 1 / sqrt(var + eps). y may be x. */
+ * only). stats [T, 2] f32 (optional): mean (0 for RMS) and 1 / sqrt(var + eps). */
 MOE_API moe_status moe_norm_forward(const moe_norm_desc *d, const void *x, int64_t ldx, const void *w,
                                     const void *b, int64_t T, void *y, int64_t ldy, float *stats,
                                     moe_stream_t stream);

@@ -21,6 +21,7 @@ namespace {
 
 constexpr int64_t kMaxRows = int64_t(1) << 30;   // slots (their padded rows fit 32 bits)
 constexpr int64_t kMaxElems = int64_t(1) << 46;  // elements of any one tensor
+constexpr int kMaxWidth = 1 << 28;               // columns (twice as many, and tiles of them, fit 32 bits)
 
 int esize(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
 
@@ -33,6 +34,22 @@ moe_status maybe(const void* p) { return p ? need(p) : MOE_OK; }
 moe_status stride(int64_t ld, int64_t cols, int dtype) {
     if (ld < cols || (ld * esize(dtype)) % 16 != 0) return MOE_ERR_INVALID_ARGUMENT;
     return ld >= (int64_t(1) << 36) ? MOE_ERR_SHAPE_OVERFLOW : MOE_OK;
+}
+// An output of rows against an input of rows: they may be the same tensor (`same`), or hold no
+// element in common, side by side in wider rows included.
+moe_status apart(const void* in, int64_t ldi, int64_t ci, const void* out, int64_t ldo, int64_t co, int64_t T, int dtype,
+                 bool same) {
+    if (!in || !out) return MOE_OK;
+    if (same && in == out && (ldi == ldo || T == 1) && ci == co) return MOE_OK;
+    const int64_t es = esize(dtype);
+    const uintptr_t i0 = reinterpret_cast<uintptr_t>(in), o0 = reinterpret_cast<uintptr_t>(out);
+    const uintptr_t i1 = i0 + uintptr_t(((T - 1) * ldi + ci) * es), o1 = o0 + uintptr_t(((T - 1) * ldo + co) * es);
+    if (i1 <= o0 || o1 <= i0) return MOE_OK;
+    if (T > 1 && ldi == ldo) {
+        const int64_t ld = ldi * es, d = (int64_t(o0 - i0) % ld + ld) % ld;
+        if (d >= ci * es && d + co * es <= ld) return MOE_OK;
+    }
+    return MOE_ERR_INVALID_ARGUMENT;
 }
 moe_status check_status_ptr(const int32_t* p) {
     return (reinterpret_cast<uintptr_t>(p) & 3u) == 0 ? MOE_OK : MOE_ERR_INVALID_ARGUMENT;
@@ -62,6 +79,7 @@ moe_status check_linear(const moe_linear_desc* d, int64_t T) {
     const int q = 16 / esize(d->dtype);
     if (d->in_features % q || d->out_features % q) return MOE_ERR_INVALID_ARGUMENT;
     if (T < 0) return MOE_ERR_INVALID_ARGUMENT;
+    if (d->in_features > kMaxWidth || d->out_features > kMaxWidth) return MOE_ERR_SHAPE_OVERFLOW;
     if (T > kMaxRows || T * std::max(d->in_features, d->out_features) > kMaxElems) return MOE_ERR_SHAPE_OVERFLOW;
     return MOE_OK;
 }
@@ -118,6 +136,7 @@ moe_status check_ffn(const moe_config* c, int64_t T, bool dense, FfnShape* f) {
     f->bias = c->has_expert_bias != 0;
     f->T = T;
     f->dense = dense;
+    if (f->K > kMaxWidth || f->I > kMaxWidth) return MOE_ERR_SHAPE_OVERFLOW;
     if (T > kMaxRows || T * f->k > kMaxRows) return MOE_ERR_SHAPE_OVERFLOW;
     f->S = T * f->k;
     f->rows = dense ? T : max_padded_rows(f->S, f->E);
@@ -259,6 +278,8 @@ moe_status moe_linear_forward(const moe_linear_desc* d, const void* x, int64_t l
     MOE_CHECK(stride(ldy, N, d->dtype));
     if (residual) MOE_CHECK(stride(ldr, N, d->dtype));
     MOE_CHECK(check_ws(ws, ws_bytes, linear_ws(d, T, false).total));
+    MOE_CHECK(apart(x, ldx, K, y, ldy, N, T, d->dtype, false));
+    MOE_CHECK(apart(residual, ldr, N, y, ldy, N, T, d->dtype, true));
     if (small_form(T, int64_t(K) * N, d->dtype)) {
         SmallArgs a;
         a.T = int(T); a.K = K; a.N = N; a.dtype = d->dtype; a.act = d->activation;
@@ -315,6 +336,8 @@ moe_status moe_linear_backward(const moe_linear_desc* d, const void* dy, int64_t
     }
     const LinearWs L = linear_ws(d, T, true);
     MOE_CHECK(check_ws(ws, ws_bytes, L.total));
+    MOE_CHECK(apart(dy, lddy, N, dx, lddx, K, T, d->dtype, false));
+    if (dw) MOE_CHECK(apart(x, ldx, K, dx, lddx, K, T, d->dtype, false));
     const void* dz = dy;
     int64_t lddz = lddy;
     if (act || db) {
@@ -383,6 +406,8 @@ moe_status moe_ffn_forward(const moe_config* cfg, const moe_weights* w, const vo
     if (residual) MOE_CHECK(stride(ldr, f.K, f.dtype));
     const FfnWs L = ffn_ws(f, false);
     MOE_CHECK(check_ws(ws, ws_bytes, L.total));
+    MOE_CHECK(apart(u, ldu, f.K, y, ldy, f.K, T, f.dtype, true));
+    MOE_CHECK(apart(residual, ldr, f.K, y, ldy, f.K, T, f.dtype, true));
     cudaStream_t s = (cudaStream_t)stream;
     const RowPlan p = row_plan(f, expert_offsets, sorted_slot, ws, L, device_status);
     if (dense && small_form(T, 3 * int64_t(f.K) * f.I, f.dtype)) {
@@ -523,6 +548,8 @@ moe_status moe_ffn_backward(const moe_config* cfg, const moe_weights* w, const v
     if (du) MOE_CHECK(stride(lddu, f.K, f.dtype));
     const FfnWs L = ffn_ws(f, true);
     MOE_CHECK(check_ws(ws, ws_bytes, L.total));
+    MOE_CHECK(apart(u, ldu, f.K, du, lddu, f.K, T, f.dtype, false));
+    MOE_CHECK(apart(dy, lddy, f.K, du, lddu, f.K, T, f.dtype, false));
     const RowPlan p = row_plan(f, expert_offsets, sorted_slot, ws, L, device_status);
     const void *up = u, *dyp = dy;
     int64_t ldup = ldu, lddyp = lddy;
@@ -652,6 +679,7 @@ moe_status check_norm(const moe_norm_desc* d, int64_t T) {
     if (!std::isfinite(d->eps) || d->eps <= 0.f) return MOE_ERR_INVALID_ARGUMENT;
     if (d->width % (16 / esize(d->dtype))) return MOE_ERR_INVALID_ARGUMENT;
     if (T < 0) return MOE_ERR_INVALID_ARGUMENT;
+    if (d->width > kMaxWidth) return MOE_ERR_SHAPE_OVERFLOW;
     if (T > kMaxRows || T * d->width > kMaxElems) return MOE_ERR_SHAPE_OVERFLOW;
     return MOE_OK;
 }
@@ -681,6 +709,7 @@ moe_status moe_norm_forward(const moe_norm_desc* d, const void* x, int64_t ldx, 
     MOE_CHECK(maybe(stats));
     MOE_CHECK(stride(ldx, d->width, d->dtype));
     MOE_CHECK(stride(ldy, d->width, d->dtype));
+    MOE_CHECK(apart(x, ldx, d->width, y, ldy, d->width, T, d->dtype, true));
     NormArgs a;
     a.T = T; a.H = d->width; a.kind = d->kind; a.dtype = d->dtype; a.eps = d->eps;
     a.x = x; a.ldx = ldx; a.w = w; a.b = b;
@@ -712,6 +741,8 @@ moe_status moe_norm_backward(const moe_norm_desc* d, const void* dy, int64_t ldd
     MOE_CHECK(stride(ldx, d->width, d->dtype));
     if (dx) MOE_CHECK(stride(lddx, d->width, d->dtype));
     MOE_CHECK(check_ws(ws, ws_bytes, norm_ws(d, T, true)));
+    MOE_CHECK(apart(x, ldx, d->width, dx, lddx, d->width, T, d->dtype, false));
+    MOE_CHECK(apart(dy, lddy, d->width, dx, lddx, d->width, T, d->dtype, false));
     NormArgs a;
     a.T = T; a.H = d->width; a.kind = d->kind; a.dtype = d->dtype; a.eps = d->eps;
     a.x = x; a.ldx = ldx; a.w = w;

@@ -58,7 +58,7 @@ __device__ __forceinline__ float logistic(float z) {
 // Phi(z) and the normal density for results that are rounded to bf16 next: Phi(-|z|) =
 // erfc(|z| / sqrt 2) / 2 by Abramowitz and Stegun 7.1.26, t (a1 + ... + a5 t^4) e^(-z^2 / 2) with
 // t = 1 / (1 + p |z| / sqrt 2), absolute error below 1.5e-7; the exponential is the density's.
-// 23.8 -> 10 us against erfcf in the derivative pass of 4097 x 2048 (the erfcf made it
+// 23.8 -> 15.2 us against erfcf in the derivative pass of 4097 x 2048 (the erfcf made it
 // compute bound).
 __device__ __forceinline__ void normal_fast(float z, float& Phi, float& phi) {
     const float e = __expf(-0.5f * z * z);

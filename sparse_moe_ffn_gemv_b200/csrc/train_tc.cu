@@ -10,11 +10,11 @@
 //        run one after the other: together they measured no faster)
 //
 // No operand is transposed in memory: the matrix instructions read either order from shared
-// memory, and TMA brings either as 64 x 64 (MN-major) or 64 x 128 (K-major) boxes with the
-// 128-byte swizzle. Tiles are 128 x 256 on one CTA, or 256 x 256 on a pair of CTAs
-// (cta_group::2: each CTA loads half of both operands, which halves the operand traffic per
-// product; one CTA's tile needs 96 bytes per cycle of L2 reads to keep its tensor core busy,
-// a pair's 64).
+// memory, and TMA brings either as boxes of one or two 64-column blocks (MN-major, 64 rows) or
+// 64 x 128 (K-major) with the 128-byte swizzle. Tiles are 128 x 256 on one CTA, or 256 x 256 on a
+// pair of CTAs (cta_group::2: each CTA loads half of both operands, which halves the operand
+// traffic per product; one CTA's tile needs 96 bytes per cycle of L2 reads to keep its tensor core
+// busy, a pair's 64), or 512 x 256 on a pair (48 bytes) for long dense reductions.
 //
 // One persistent CTA (pair) per SM (pair):
 //   warp 0      TMA producer into a ring of 64-deep reduction blocks
@@ -47,9 +47,9 @@ constexpr int kMaxE = 512;
 constexpr int kABytes = 128 * kBR * 2;  // one 128-row operand tile
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-// kGateUpI, kDGatedI: alternating gate / up columns.
 constexpr int kMix = 3;  // besides enum GemmKind
 constexpr int kMaxMix = 3;
+// kGateUpI, kDGatedI: alternating gate / up columns.
 // kStoreBulk: kTN on pairs, D leaves by TMA.
 // kStoreTall: pairs on tiles of 512 rows.
 enum Epi { kStore = 0, kGateUp = 1, kGateUpI = 2, kDGated = 3, kDGatedI = 4, kStoreBulk = 5, kStoreTall = 6 };
@@ -74,7 +74,7 @@ FastDiv fast_div(int64_t d) {
 
 struct TcTrain {
     CUtensorMap a, b0, b1;
-    CUtensorMap o0, o1;     // kTN on pairs: the planes of D
+    CUtensorMap o0, o1;     // kStoreBulk: the planes of D
     FastDiv d_tile, d_m, d_band, d_width, d_tail;  // see tile_of
     int tn;                 // kMix: a kTN product
     int bulk_out, tall;     // host: kStoreBulk, kStoreTall

@@ -202,3 +202,47 @@ def test_norm_backward_refusals(kind, kw, status):
     a.update(kw)
     d = train.MoeNormDesc(64, kind, 1, 1e-6)
     assert train.lib().moe_norm_backward(ctypes.byref(d), *a.values(), None) == status
+
+
+FAR = 1 << 30  # from one tensor to the next: nothing overlaps
+
+
+@pytest.mark.parametrize("y,kw", [
+    (PTR, dict()), (PTR + 16, dict()), (PTR - 16, dict()), (PTR + 9 * 128, dict()),  # x's own, shifted, its last row
+    (PTR + 112, dict(ldx=200, ldy=200)), (PTR + 128, dict(ldx=136, ldy=136)),        # side by side, but not quite
+    (PTR + 128, dict(ldx=256, ldy=128)),                                             # other strides: not told apart
+])
+def test_linear_output_over_its_input(y, kw):
+    assert linear_forward(w=FAR, y=y, **kw) == INVALID
+
+
+@pytest.mark.parametrize("residual,ldr", [(2 * FAR + 16, 128), (2 * FAR, 136), (2 * FAR - 256, 128)])
+def test_outputs_over_a_shifted_residual(residual, ldr):
+    assert linear_forward(w=FAR, y=2 * FAR, residual=residual, ldr=ldr) == INVALID
+    assert ffn_forward(y=2 * FAR, ldy=128, residual=residual, ldr=ldr) == INVALID
+
+
+def test_input_gradients_over_inputs():
+    assert linear_backward(dx=PTR, dy=FAR) == INVALID            # x's
+    assert linear_backward(dx=PTR, x=FAR) == INVALID             # dy's
+    assert ffn_backward(du=PTR, dy=FAR) == INVALID
+    assert ffn_backward(du=PTR, u=FAR) == INVALID
+    assert ffn_forward(u=PTR, y=PTR + 128) == INVALID            # u itself would be right, its next row is not
+    d = train.MoeNormDesc(64, 0, 1, 1e-6)
+    norm = train.lib().moe_norm_backward
+    for dy, x in ((PTR, FAR), (FAR, PTR)):
+        assert norm(ctypes.byref(d), dy, 64, x, 64, PTR, PTR, 10, PTR, 64, None, None, PTR, 1 << 30, None) == INVALID
+    fwd = train.lib().moe_norm_forward
+    assert fwd(ctypes.byref(d), PTR, 64, PTR, None, 10, PTR + 128, 64, None, None) == INVALID
+    assert fwd(ctypes.byref(d), PTR, 64, PTR, None, 10, PTR, 72, None, None) == INVALID
+
+
+def test_widths_past_their_limit():
+    wide = 1 << 28
+    assert size("moe_linear_workspace_size", train.MoeLinearDesc(wide + 8, 8, 0, 1), 1, 0)[0] == OVERFLOW
+    assert size("moe_linear_workspace_size", train.MoeLinearDesc(8, wide + 8, 0, 1), 1, 0)[0] == OVERFLOW
+    assert size("moe_linear_workspace_size", train.MoeLinearDesc(8, wide, 0, 1), 1, 1)[0] == 0
+    assert size("moe_norm_workspace_size", train.MoeNormDesc(wide + 8, 0, 1, 1e-6), 1, 0)[0] == OVERFLOW
+    one = SPEC.replace(num_experts=1, top_k=1, hidden=8)
+    assert size("moe_ffn_workspace_size", M.config_from_spec(one.replace(intermediate=wide + 8)), 1, 0)[0] == OVERFLOW
+    assert size("moe_ffn_workspace_size", M.config_from_spec(one.replace(intermediate=wide)), 1, 1)[0] == 0

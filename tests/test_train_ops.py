@@ -435,6 +435,41 @@ def test_ffn_slot_that_stands_twice_is_reported(T, width, kw):
             assert torch.isfinite(t).all(), name
 
 
+@pytest.mark.parametrize("T,kw", [
+    (1, dict(num_experts=1, top_k=1)), (4, dict(num_experts=1, top_k=1)), (300, dict(num_experts=1, top_k=1)),
+    (50, dict(num_experts=4, top_k=2)), (60, dict(num_experts=1, top_k=1, act_dtype="f32")),
+    (2100, dict(num_experts=4, top_k=2, hidden=1024)),
+])
+def test_ffn_output_may_be_its_input_and_residual(T, kw):
+    spec = spec_of(**{**dict(hidden=72, intermediate=40), **kw})
+    g = gen(16)
+    w, x = planes(spec, g), rand(g, (T, spec.expert_in), spec.act_dtype)
+    routing = None if spec.num_experts == 1 else R.make_routing(T, spec, g, "cuda")
+    op = train.GatedFfn(spec)
+    want, _ = op.forward(x, w, routing=routing, residual=x)
+    got = x.clone()
+    op.forward(got, w, routing=routing, residual=got, out=got)
+    ok(op)
+    assert torch.equal(got, want)
+
+
+def test_linear_output_beside_its_input():
+    """x and y as column slices of one buffer; y over x is refused."""
+    g = gen(17)
+    for T, dtype in ((1, "bf16"), (3, "bf16"), (400, "bf16"), (90, "f32")):
+        x, w = rand(g, (T, 72), dtype), rand(g, (72, 72), dtype)
+        op = train.Linear(72, 72, dtype=dtype)
+        both = torch.zeros((T, 160), dtype=DT[dtype], device="cuda")
+        both[:, 8:80] = x
+        y = op.forward(both[:, 8:80], w, out=both[:, 80:152])
+        ok(op)
+        assert torch.equal(y, op.forward(x, w)) and torch.equal(both[:, 8:80], x) and (both[:, 152:] == 0).all()
+        with pytest.raises(M.MoeError):
+            op.forward(both[:, 8:80], w, out=both[:, 8:80])
+        with pytest.raises(M.MoeError):
+            op.forward(both[:, 8:80], w, out=both[:, 72:144])
+
+
 # ------------------------------------------------------------------ norm
 NORM = [  # dtype, T, H, kind, bias, pad
     ("bf16", 1, 8, "rms", False, 0), ("bf16", 1, 3584, "rms", False, 0), ("bf16", 3, 64, "layer", True, 8),
