@@ -34,6 +34,14 @@ NORM_KIND = {"layer": 0, "rms": 1}
 GRAD_FIELDS = ["gate_w", "up_w", "gate_up_w", "gate_b", "up_b", "gate_up_b", "down_w", "down_b"]
 _DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16}
 
+# What a call needs of PyTorch's CUDA runtime, without the checks of the public wrappers (a current
+# device, a stream and a workspace cost 2 us less per call). The allocator is the same one: memory
+# freed after the launch is handed out again on that stream only, in a graph's pool within it.
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+_allocate = torch._C._cuda_cudaCachingAllocator_raw_alloc
+_free = torch._C._cuda_cudaCachingAllocator_raw_delete
+
 
 class MoeLinearDesc(ctypes.Structure):
     _fields_ = [("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32),
@@ -97,7 +105,7 @@ class _Operator:
         self._index = self.device.index
         self.lib = lib()
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
-        self._status_p = self.status.data_ptr()
+        self._tail = (self.status.data_ptr(),)  # what follows the workspace in a call
         self._ws_bytes: Dict[Tuple[int, int], int] = {}
 
     def device_status(self) -> int:
@@ -109,7 +117,7 @@ class _Operator:
 
     def _elsewhere(self, stream) -> bool:
         """Whether the call names a stream, or another device is current."""
-        return stream is not None or torch.cuda.current_device() != self._index
+        return stream is not None or _current_device() != self._index
 
     @contextlib.contextmanager
     def _on(self, stream):
@@ -145,28 +153,38 @@ class _Operator:
             raise ValueError(f"{name}: strides {(ld, unit)}: the columns of a row must be contiguous")
         return t.data_ptr(), ld if n > 1 else width
 
-    def _workspace(self, size_fn, desc_ref, T: int, backward: int):
+    def _size(self, size_fn, desc_ref, T: int, backward: int) -> int:
+        """Bytes of workspace; also the library's check of the operator's shape."""
+        out = ctypes.c_size_t(0)
+        M._check(size_fn(desc_ref, T, backward, ctypes.byref(out)), size_fn.__name__)
+        if len(self._ws_bytes) >= 1024:
+            self._ws_bytes.clear()
+        self._ws_bytes[(T, backward)] = out.value
+        return out.value
+
+    def _launch(self, fn, size_fn, desc_ref, T: int, backward: int, *args):
+        """fn(desc, args, workspace, its size, status, stream) on the current stream."""
         n = self._ws_bytes.get((T, backward))
         if n is None:
-            out = ctypes.c_size_t(0)
-            M._check(size_fn(desc_ref, T, backward, ctypes.byref(out)), size_fn.__name__)
-            if len(self._ws_bytes) >= 1024:
-                self._ws_bytes.clear()
-            n = self._ws_bytes[(T, backward)] = out.value
-        return (torch.empty(n, dtype=torch.uint8, device=self.device), n) if n else (None, 0)
+            n = self._size(size_fn, desc_ref, T, backward)
+        stream = _current_stream(self._index)
+        ws = _allocate(n, stream) if n else None
+        try:
+            status = fn(desc_ref, *args, ws, n, *self._tail, stream)
+        finally:
+            if n:
+                _free(ws)
+        if status:
+            M._check(status, fn.__name__)
 
     def _empty(self, *shape, dtype=None):
         return torch.empty(shape, dtype=dtype or self.dtype, device=self.device)
 
-    def _like(self, t, *shape):
-        """An uninitialised tensor of the handle's dtype; like t where t has that shape
-        (a microsecond less than torch.empty)."""
-        if t.shape == shape and t.is_contiguous():
-            return torch.empty_like(t)
-        return t.new_empty(shape)
-
-    def _stream(self):
-        return torch._C._cuda_getCurrentRawStream(self._index)
+    @staticmethod
+    def _like(t, shape):
+        """An uninitialised tensor of t's dtype; like t where t has that shape (half a
+        microsecond less than by its sizes)."""
+        return torch.empty_like(t) if t.shape == shape and t.is_contiguous() else t.new_empty(shape)
 
 
 class Linear(_Operator):
@@ -180,7 +198,7 @@ class Linear(_Operator):
         self.n_in, self.n_out, self.activation = in_features, out_features, activation
         self.desc = MoeLinearDesc(in_features, out_features, LINEAR_ACTIVATION[activation], inputs.DTYPE[dtype])
         self._desc = ctypes.byref(self.desc)
-        self._workspace(self.lib.moe_linear_workspace_size, self._desc, 0, 0)  # checks the shape
+        self._size(self.lib.moe_linear_workspace_size, self._desc, 0, 0)  # checks the shape
 
     def forward(self, x, w, bias=None, residual=None, keep: bool = False, out=None, stream=None):
         """y, or (y, pre) with keep: pre = x W^T + b is what backward needs of an activation."""
@@ -192,13 +210,15 @@ class Linear(_Operator):
         wp = self._flat("w", w, N * K)
         bp = None if bias is None else self._flat("bias", bias, N)
         rp, ldr = (None, 0) if residual is None else self._rows("residual", residual, N, T)
-        y = (x.new_empty((T, N)) if residual is None else self._like(residual, T, N)) if out is None else out
-        yp, ldy = self._rows("out", y, N, T)
+        if out is None:
+            y = self._like(x if residual is None else residual, (T, N))
+            yp, ldy = y.data_ptr(), N
+        else:
+            y = out
+            yp, ldy = self._rows("out", out, N, T)
         pre = self._empty(T, N) if keep else None
-        ws, n = self._workspace(self.lib.moe_linear_workspace_size, self._desc, T, 0)
-        M._check(self.lib.moe_linear_forward(self._desc, xp, ldx, wp, bp, rp, ldr, T, yp, ldy,
-                                             _p(pre), _p(ws), n, self._status_p, self._stream()),
-                 "moe_linear_forward")
+        self._launch(self.lib.moe_linear_forward, self.lib.moe_linear_workspace_size, self._desc, T, 0,
+                     xp, ldx, wp, bp, rp, ldr, T, yp, ldy, _p(pre))
         return (y, pre) if keep else y
 
     def backward(self, dy, x, w, pre=None, bias_grad: bool = True, input_grad: bool = True,
@@ -212,13 +232,11 @@ class Linear(_Operator):
         xp, ldx = self._rows("x", x, K)
         wp = self._flat("w", w, N * K)
         pp = None if pre is None else self._flat("pre", pre, T * N)
-        dx = self._like(x, T, K) if input_grad else None
-        dw = self._like(w, N, K) if weight_grad else None
+        dx = self._like(x, (T, K)) if input_grad else None
+        dw = self._like(w, (N, K)) if weight_grad else None
         db = self._empty(N) if bias_grad else None
-        ws, n = self._workspace(self.lib.moe_linear_workspace_size, self._desc, T, 1)
-        M._check(self.lib.moe_linear_backward(self._desc, gp, ldg, xp, ldx, wp, pp, T, _p(dx), K,
-                                              _p(dw), _p(db), _p(ws), n, self._status_p,
-                                              self._stream()), "moe_linear_backward")
+        self._launch(self.lib.moe_linear_backward, self.lib.moe_linear_workspace_size, self._desc, T, 1,
+                     gp, ldg, xp, ldx, wp, pp, T, _p(dx), K, _p(dw), _p(db))
         return dx, dw, db
 
 
@@ -238,7 +256,7 @@ class GatedFfn(_Operator):
         M._check(M.moe_config_validate(self.cfg), "moe_config_validate")
         E, I, K = spec.num_experts, spec.intermediate, spec.expert_in
         self.E, self.k, self.I, self.K = E, spec.top_k, I, K
-        self._workspace(self.lib.moe_ffn_workspace_size, self._cfg, 0, 0)  # checks the weight format
+        self._size(self.lib.moe_ffn_workspace_size, self._cfg, 0, 0)  # checks the weight format
         shapes = {"gate_up_w": (E, 2 * I, K)} if spec.gate_up_interleaved else {"gate_w": (E, I, K), "up_w": (E, I, K)}
         shapes["down_w"] = (E, K, I)
         if spec.has_expert_bias:
@@ -280,13 +298,15 @@ class GatedFfn(_Operator):
         w = self._planes(weights)
         off, slots, wts = self._routing(routing, T)
         rp, ldr = (None, 0) if residual is None else self._rows("residual", residual, self.K, T)
-        y = self._like(u, T, self.K) if out is None else out
-        yp, ldy = self._rows("out", y, self.K, T)
+        if out is None:
+            y = self._like(u, (T, self.K))
+            yp, ldy = y.data_ptr(), self.K
+        else:
+            y = out
+            yp, ldy = self._rows("out", out, self.K, T)
         pre = self._empty(T * self.k, 2 * self.I) if keep else None
-        ws, n = self._workspace(self.lib.moe_ffn_workspace_size, self._cfg, T, 0)
-        M._check(self.lib.moe_ffn_forward(self._cfg, ctypes.byref(w), up, ldu, T, off, slots, wts, rp,
-                                          ldr, yp, ldy, _p(pre), _p(ws), n, self._status_p,
-                                          self._stream()), "moe_ffn_forward")
+        self._launch(self.lib.moe_ffn_forward, self.lib.moe_ffn_workspace_size, self._cfg, T, 0,
+                     ctypes.byref(w), up, ldu, T, off, slots, wts, rp, ldr, yp, ldy, _p(pre))
         return y, pre
 
     def backward(self, dy, u, weights: Dict[str, torch.Tensor], pre, routing=None, input_grad: bool = True,
@@ -301,16 +321,15 @@ class GatedFfn(_Operator):
         w = self._planes(weights)
         off, slots, wts = self._routing(routing, T)
         pp = self._flat("pre", pre, T * self.k * 2 * self.I)
-        grads = {f: self._like(weights[f], *s) for f, s in self.shapes.items()}
+        grads = {f: self._like(weights[f], s) for f, s in self.shapes.items()}
         g = MoeFfnGrads()
         for f, t in grads.items():
             setattr(g, f, t.data_ptr())
         dwt = None if off is None else self._empty(T, self.k, dtype=torch.float32)
-        du = self._like(u, T, self.K) if input_grad else None
-        ws, n = self._workspace(self.lib.moe_ffn_workspace_size, self._cfg, T, 1)
-        M._check(self.lib.moe_ffn_backward(self._cfg, ctypes.byref(w), up, ldu, T, off, slots, wts, pp,
-                                           gp, ldg, _p(du), self.K, _p(dwt), ctypes.byref(g), _p(ws), n,
-                                           self._status_p, self._stream()), "moe_ffn_backward")
+        du = self._like(u, (T, self.K)) if input_grad else None
+        self._launch(self.lib.moe_ffn_backward, self.lib.moe_ffn_workspace_size, self._cfg, T, 1,
+                     ctypes.byref(w), up, ldu, T, off, slots, wts, pp, gp, ldg, _p(du), self.K, _p(dwt),
+                     ctypes.byref(g))
         if du is not None:
             grads["x"] = du
         if dwt is not None:
@@ -328,7 +347,8 @@ class Norm(_Operator):
         self.width, self.kind = width, kind
         self.desc = MoeNormDesc(width, NORM_KIND[kind], inputs.DTYPE[dtype], eps)
         self._desc = ctypes.byref(self.desc)
-        self._workspace(self.lib.moe_norm_workspace_size, self._desc, 0, 0)  # checks the shape
+        self._size(self.lib.moe_norm_workspace_size, self._desc, 0, 0)  # checks the shape
+        self._tail = ()  # these calls take no status
 
     def forward(self, x, w, bias=None, out=None, stream=None):
         """(y, stats): stats [T, 2] f32 (mean, 1 / sqrt(var + eps)) is what backward takes."""
@@ -339,11 +359,15 @@ class Norm(_Operator):
         xp, ldx = self._rows("x", x, H)
         wp = self._flat("w", w, H)
         bp = None if bias is None else self._flat("bias", bias, H)
-        y = self._like(x, T, H) if out is None else out
-        yp, ldy = self._rows("out", y, H, T)
+        if out is None:
+            y = self._like(x, (T, H))
+            yp, ldy = y.data_ptr(), H
+        else:
+            y = out
+            yp, ldy = self._rows("out", out, H, T)
         stats = self._empty(T, 2, dtype=torch.float32)
         M._check(self.lib.moe_norm_forward(self._desc, xp, ldx, wp, bp, T, yp, ldy, stats.data_ptr(),
-                                           self._stream()), "moe_norm_forward")
+                                           _current_stream(self._index)), "moe_norm_forward")
         return y, stats
 
     def backward(self, dy, x, w, stats, bias_grad: Optional[bool] = None, input_grad: bool = True,
@@ -361,10 +385,9 @@ class Norm(_Operator):
         xp, ldx = self._rows("x", x, H)
         wp = self._flat("w", w, H)
         sp = self._flat("stats", stats, 2 * T, torch.float32)
-        dx = self._like(x, T, H) if input_grad else None
-        dw = self._like(w, H)
-        db = self._like(w, H) if bias_grad else None
-        ws, n = self._workspace(self.lib.moe_norm_workspace_size, self._desc, T, 1)
-        M._check(self.lib.moe_norm_backward(self._desc, gp, ldg, xp, ldx, wp, sp, T, _p(dx), H,
-                                            _p(dw), _p(db), _p(ws), n, self._stream()), "moe_norm_backward")
+        dx = self._like(x, (T, H)) if input_grad else None
+        dw = self._like(w, (H,))
+        db = self._like(w, (H,)) if bias_grad else None
+        self._launch(self.lib.moe_norm_backward, self.lib.moe_norm_workspace_size, self._desc, T, 1,
+                     gp, ldg, xp, ldx, wp, sp, T, _p(dx), H, _p(dw), _p(db))
         return dx, dw, db
