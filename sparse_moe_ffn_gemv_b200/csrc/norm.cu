@@ -49,6 +49,7 @@ __device__ __forceinline__ void group_sum2(float& x, float& y, int tpr, float2* 
 constexpr int kVpt = 4;
 template <typename T, bool LAYER>
 __global__ void __launch_bounds__(kNormThreads) norm_forward_rows_kernel(const NormArgs a, int tpr) {
+    pdl_begin();
     constexpr int V = Vec<T>::N;
     __shared__ float2 red[2][kNormThreads / 32];
     const int n = a.H / V, g = threadIdx.x / tpr, c0 = threadIdx.x % tpr;
@@ -59,7 +60,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_forward_rows_kernel(const N
 #pragma unroll
     for (int i = 0; i < kVpt; ++i) {
         const int c = c0 + i * tpr;
-        xv[i] = live && c < n ? ld_stream16(x + c * V) : make_uint4(0, 0, 0, 0);
+        xv[i] = live && c < n ? ld_once16(x + c * V) : make_uint4(0, 0, 0, 0);
     }
     float mean = 0.f, s = 0.f, unused = 0.f;
     if constexpr (LAYER) {
@@ -104,6 +105,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_forward_rows_kernel(const N
 // Wider rows: read again (from L2) for each pass.
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) norm_forward_kernel(const NormArgs a) {
+    pdl_begin();
     constexpr int V = Vec<T>::N;
     __shared__ float sm[kNormThreads / 32];
     const int n = a.H / V;
@@ -163,12 +165,13 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_backward_rows_kernel(con
     uint8_t* ring = sm + (row_bytes + 127) / 128 * 128;
     const uint32_t stage_bytes = 2 * G * row_bytes;
     const int64_t groups = (a.T + G - 1) / G;
-    for (int c = threadIdx.x; c < n; c += kNormThreads)
-        reinterpret_cast<uint4*>(sm)[c] = reinterpret_cast<const uint4*>(a.w)[c];
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    pdl_begin();
+    for (int c = threadIdx.x; c < n; c += kNormThreads)
+        reinterpret_cast<uint4*>(sm)[c] = reinterpret_cast<const uint4*>(a.w)[c];
     __syncthreads();
     const uint64_t pol = policy_evict_first();
     auto fill = [&](int64_t grp, int st) {  // one thread
@@ -193,7 +196,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_backward_rows_kernel(con
     uint32_t phase = 0;
     auto stats_of = [&](int64_t grp) {
         const int64_t t = grp * G + g;
-        return t < a.T ? __ldg(reinterpret_cast<const float2*>(a.cstats + 2 * t)) : make_float2(0.f, 0.f);
+        return t < a.T ? *reinterpret_cast<const float2*>(a.cstats + 2 * t) : make_float2(0.f, 0.f);
     };
     float2 ms = stats_of(blockIdx.x);
     for (int64_t grp = blockIdx.x; grp < groups; grp += gridDim.x, ++it) {
@@ -286,6 +289,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_backward_rows_kernel(con
 // Wider rows.
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) norm_dx_kernel(const NormArgs a) {
+    pdl_begin();
     constexpr int V = Vec<T>::N;
     __shared__ float sm[kNormThreads / 32];
     const int n = a.H / V;
@@ -324,6 +328,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_dx_kernel(const NormArgs a)
 constexpr int kColVecs = 64, kColRows = 4;
 template <typename T>
 __global__ void __launch_bounds__(kColVecs * kColRows) norm_dw_kernel(const NormArgs a) {
+    pdl_begin();
     constexpr int V = Vec<T>::N;
     const int c = (blockIdx.x * kColVecs + threadIdx.x % kColVecs) * V;
     const int ry = threadIdx.x / kColVecs;
@@ -367,6 +372,7 @@ __global__ void __launch_bounds__(kColVecs * kColRows) norm_dw_kernel(const Norm
 template <typename T>
 __global__ void __launch_bounds__(256) norm_finish_kernel(const NormArgs a, int parts) {
     __shared__ float sm[8][33];
+    pdl_begin();
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + x;
     T* o = static_cast<T*>(blockIdx.y ? a.db : a.dw);
@@ -426,7 +432,7 @@ cudaError_t backward_rows(const NormArgs& a, int parts, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         allowed.fetch_or(bit);
     }
-    norm_backward_rows_kernel<T, LAYER><<<parts, kNormThreads, ring.bytes, s>>>(a, tpr, ring.stages);
+    launch_chained(norm_backward_rows_kernel<T, LAYER>, parts, kNormThreads, ring.bytes, s, a, tpr, ring.stages);
     return cudaGetLastError();
 }
 
@@ -442,10 +448,10 @@ cudaError_t backward_t(NormArgs a, cudaStream_t s) {
         const cudaError_t e = a.kind == MOE_NORM_LAYER ? backward_rows<T, true>(a, parts, s) : backward_rows<T, false>(a, parts, s);
         if (e != cudaSuccess) return e;
     } else {
-        if (a.dx) norm_dx_kernel<T><<<unsigned(std::min<int64_t>(a.T, 148 * 8)), kNormThreads, 0, s>>>(a);
-        if (sums) norm_dw_kernel<T><<<dim3((a.H / V + kColVecs - 1) / kColVecs, parts), kColVecs * kColRows, 0, s>>>(a);
+        if (a.dx) launch_chained(norm_dx_kernel<T>, unsigned(std::min<int64_t>(a.T, 148 * 8)), kNormThreads, 0, s, a);
+        if (sums) launch_chained(norm_dw_kernel<T>, dim3((a.H / V + kColVecs - 1) / kColVecs, parts), kColVecs * kColRows, 0, s, a);
     }
-    if (sums) norm_finish_kernel<T><<<dim3((a.H + 31) / 32, a.db ? 2 : 1), 256, 0, s>>>(a, parts);
+    if (sums) launch_chained(norm_finish_kernel<T>, dim3((a.H + 31) / 32, a.db ? 2 : 1), 256, 0, s, a, parts);
     return cudaGetLastError();
 }
 
@@ -453,12 +459,12 @@ template <typename T>
 cudaError_t forward_t(const NormArgs& a, cudaStream_t s) {
     const int tpr = threads_per_row(a.H, Vec<T>::N);
     if (!tpr) {
-        norm_forward_kernel<T><<<unsigned(std::min<int64_t>(a.T, 148 * 8)), kNormThreads, 0, s>>>(a);
+        launch_chained(norm_forward_kernel<T>, unsigned(std::min<int64_t>(a.T, 148 * 8)), kNormThreads, 0, s, a);
         return cudaGetLastError();
     }
     const unsigned grid = unsigned((a.T + kNormThreads / tpr - 1) / (kNormThreads / tpr));
-    if (a.kind == MOE_NORM_LAYER) norm_forward_rows_kernel<T, true><<<grid, kNormThreads, 0, s>>>(a, tpr);
-    else norm_forward_rows_kernel<T, false><<<grid, kNormThreads, 0, s>>>(a, tpr);
+    if (a.kind == MOE_NORM_LAYER) launch_chained(norm_forward_rows_kernel<T, true>, grid, kNormThreads, 0, s, a, tpr);
+    else launch_chained(norm_forward_rows_kernel<T, false>, grid, kNormThreads, 0, s, a, tpr);
     return cudaGetLastError();
 }
 

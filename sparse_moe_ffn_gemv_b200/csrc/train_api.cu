@@ -430,7 +430,7 @@ moe_status moe_ffn_forward(const moe_config* cfg, const moe_weights* w, const vo
         o.bias = f.bias ? w->down_b : nullptr;
         o.residual = residual; o.ldr = ldr;
         o.y = y; o.ldy = ldy;
-        o.wait_input = true;
+        o.prefetch = true;
         MOE_CUDA(launch_small(o, s));
         return MOE_OK;
     }

@@ -123,9 +123,7 @@ struct SmallArgs {
     const void* residual = nullptr; int64_t ldr = 0;
     void* pre = nullptr;                     // [T, N] (gated: [T, 2N])
     void* y = nullptr; int64_t ldy = 0;
-    // x is written by the launch just before (a launch of this kernel): this one may start
-    // early and waits for it
-    bool wait_input = false;
+    bool prefetch = false;  // a launch of this kernel comes just before: this one starts in its tail
     int ks = 1;  // set by the launcher
 };
 cudaError_t launch_small(const SmallArgs& a, cudaStream_t s);

@@ -92,6 +92,7 @@ __device__ __forceinline__ bool is_repeat(const RowPlan& p, int r, int slot) { r
 // far as a reduction over the expert's rows reads; rows of dropped slots are zeros too.
 __global__ void __launch_bounds__(kGatherThreads) gather_padded_kernel(const GatherArgs a) {
     __shared__ PlanSmem sm;
+    pdl_begin();
     const RowPlan& p = a.plan;
     const int total = build_plan(p, sm);
     const int lane = threadIdx.x & 31;
@@ -113,10 +114,10 @@ __global__ void __launch_bounds__(kGatherThreads) gather_padded_kernel(const Gat
             uint4* d = static_cast<uint4*>(a.dst[j]) + int64_t(r) * vpr;
             int64_t c = lane;
             for (; c + 96 < vpr; c += 128) {  // four vectors in flight per lane
-                const uint4 v0 = __ldg(s + c), v1 = __ldg(s + c + 32), v2 = __ldg(s + c + 64), v3 = __ldg(s + c + 96);
+                const uint4 v0 = s[c], v1 = s[c + 32], v2 = s[c + 64], v3 = s[c + 96];
                 d[c] = v0; d[c + 32] = v1; d[c + 64] = v2; d[c + 96] = v3;
             }
-            for (; c < vpr; c += 32) d[c] = __ldg(s + c);
+            for (; c < vpr; c += 32) d[c] = s[c];
         }
     }
 }
@@ -124,6 +125,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_padded_kernel(const Gat
 // Many rows: the plan, a thread per padded row, and the zero rows; copy_tokens_kernel does the rest.
 __global__ void __launch_bounds__(kGatherThreads) plan_rows_kernel(const GatherArgs a) {
     __shared__ PlanSmem sm;
+    pdl_begin();
     const RowPlan& p = a.plan;
     const int total = build_plan(p, sm);
     const int lane = threadIdx.x & 31, step = gridDim.x * kGatherThreads;
@@ -155,9 +157,10 @@ __global__ void __launch_bounds__(kCopyWarps * 32) copy_tokens_kernel(const Gath
     const int piece = int(min(int64_t(kPiece), row_bytes));
     const int ns = a.src[1] ? 2 : 1;
     uint8_t* buf = sm + warp * ns * piece;
-    for (int e = threadIdx.x; e <= p.E; e += blockDim.x) pad[e] = p.poff[e];
     if (lane == 0) mbar_init(&full[warp], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    pdl_begin();
+    for (int e = threadIdx.x; e <= p.E; e += blockDim.x) pad[e] = p.poff[e];
     __syncthreads();
     const uint64_t pol = policy_evict_first();
     uint32_t phase = 0;
@@ -240,6 +243,7 @@ __global__ void __launch_bounds__(kCopyWarps * 32) copy_tokens_kernel(const Gath
 // stands twice, since its blocks plan side by side: it shows here.)
 template <typename T>
 __global__ void __launch_bounds__(256) sum_slots_kernel(const SumSlotsArgs a) {
+    pdl_begin();
     for (int r = blockIdx.x * 256 + threadIdx.x; r < a.plan.poff[a.plan.E]; r += gridDim.x * 256)
         if (is_repeat(a.plan, r, a.plan.row_slot[r])) set_status(a.plan.status, MOE_ERR_DEVICE_CHECK);
     constexpr int V = Vec<T>::N;
@@ -295,6 +299,7 @@ __device__ __forceinline__ RowRef row_ref(const RowPlan& p, int64_t r) {
 
 // One warp per row; gate and up of unit i. (f32; bf16 has both passes in its products' epilogues.)
 __global__ void __launch_bounds__(256) gated_forward_kernel(const GatedArgs a) {
+    pdl_begin();
     using T = float;
     constexpr bool FAST = false;
     const int lane = threadIdx.x & 31;
@@ -317,6 +322,7 @@ __global__ void __launch_bounds__(256) gated_forward_kernel(const GatedArgs a) {
 }
 
 __global__ void __launch_bounds__(256) gated_backward_kernel(const GatedArgs a) {
+    pdl_begin();
     using T = float;
     constexpr bool FAST = false;
     const int lane = threadIdx.x & 31;
@@ -359,6 +365,7 @@ __global__ void __launch_bounds__(256) gated_backward_kernel(const GatedArgs a) 
 
 // One thread per slot: its row's partial sums in order, plus dy . down_b with a down bias.
 __global__ void __launch_bounds__(256) dtopk_kernel(const GatedArgs a, const float* partial, int parts) {
+    pdl_begin();
     for (int64_t slot = int64_t(blockIdx.x) * 256 + threadIdx.x; slot < a.plan.S; slot += int64_t(gridDim.x) * 256) {
         const int64_t r = row_of_slot(a.plan, int(slot));
         float dw = 0.0f;
@@ -376,6 +383,7 @@ __global__ void __launch_bounds__(256) dtopk_kernel(const GatedArgs a, const flo
 constexpr int kColVecs = 64, kColRows = 4, kColDeep = 8;
 template <typename T>
 __global__ void __launch_bounds__(kColVecs * kColRows) colsum_kernel(const ColsumArgs a0, const ColsumArgs a1, int blocks0) {
+    pdl_begin();
     constexpr int V = Vec<T>::N;
     const bool second = int(blockIdx.y) >= blocks0;
     const ColsumArgs& a = second ? a1 : a0;
@@ -437,6 +445,7 @@ __global__ void __launch_bounds__(kColVecs * kColRows) colsum_kernel(const Colsu
 // `parts` rows of one matrix.
 template <typename T>
 __global__ void __launch_bounds__(256) colsum_finish_kernel(const ColsumArgs a0, const ColsumArgs a1, int blocks0, int parts) {
+    pdl_begin();
     __shared__ float sm[8][33];
     const int e = blockIdx.y;
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
@@ -467,6 +476,7 @@ __global__ void __launch_bounds__(256) colsum_finish_kernel(const ColsumArgs a0,
 // blocks per SM.
 template <typename T>
 __global__ void __launch_bounds__(kColVecs * kColRows, 4) dact_kernel(const DactArgs a, int splits) {
+    pdl_begin();
     constexpr int V = Vec<T>::N;
     constexpr bool FAST = V == 8;
     const int64_t per = (a.T + splits - 1) / splits;
@@ -530,10 +540,10 @@ cudaError_t launch_gather_padded(const GatherArgs& a, cudaStream_t s) {
     const unsigned grid = grid_for(a.plan.max_rows, kGatherThreads / 32, 148 * 4);
     // few rows: one launch that copies as it plans; else (and for the bias products) two
     if (!a.down_b && a.plan.S * a.K * a.es < kCopyBytes) {
-        gather_padded_kernel<<<grid, kGatherThreads, 0, s>>>(a);
+        launch_chained(gather_padded_kernel, grid, kGatherThreads, 0, s, a);
         return cudaGetLastError();
     }
-    plan_rows_kernel<<<grid_for(a.plan.max_rows, kGatherThreads, 148 * 2), kGatherThreads, 0, s>>>(a);
+    launch_chained(plan_rows_kernel, grid_for(a.plan.max_rows, kGatherThreads, 148 * 2), kGatherThreads, 0, s, a);
     const int64_t row = int64_t(a.K) * a.es;
     const int smem = int(std::min<int64_t>(kPiece, row)) * (a.src[1] ? 2 : 1) * kCopyWarps;
     static std::atomic<uint64_t> allowed{0};
@@ -554,18 +564,18 @@ cudaError_t launch_gather_padded(const GatherArgs& a, cudaStream_t s) {
 cudaError_t launch_sum_slots(const SumSlotsArgs& a, cudaStream_t s) {
     const int V = a.dtype == MOE_DTYPE_F32 ? 4 : 8;
     const unsigned grid = grid_for(a.plan.T * (a.K / V), 256, 148 * 16);
-    if (a.dtype == MOE_DTYPE_F32) sum_slots_kernel<float><<<grid, 256, 0, s>>>(a);
-    else sum_slots_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
+    if (a.dtype == MOE_DTYPE_F32) launch_spread(sum_slots_kernel<float>, grid, 256, s, a);
+    else launch_spread(sum_slots_kernel<__nv_bfloat16>, grid, 256, s, a);
     return cudaGetLastError();
 }
 
 cudaError_t launch_gated_forward(const GatedArgs& a, cudaStream_t s) {
-    gated_forward_kernel<<<grid_for(a.plan.max_rows, 8, 148 * 8), 256, 0, s>>>(a);
+    launch_chained(gated_forward_kernel, grid_for(a.plan.max_rows, 8, 148 * 8), 256, 0, s, a);
     return cudaGetLastError();
 }
 
 cudaError_t launch_gated_backward(const GatedArgs& a, cudaStream_t s) {
-    gated_backward_kernel<<<grid_for(a.plan.max_rows, 8, 148 * 8), 256, 0, s>>>(a);
+    launch_chained(gated_backward_kernel, grid_for(a.plan.max_rows, 8, 148 * 8), 256, 0, s, a);
     return cudaGetLastError();
 }
 
@@ -581,11 +591,11 @@ cudaError_t launch_colsum(const ColsumArgs (&a)[2], cudaStream_t s) {
     const int f0 = (a[0].cols + 31) / 32, f1 = (a[1].cols + 31) / 32;
     const dim3 grid(unsigned(tiles), c0 + c1), fin(f0 + f1, a[0].plan.E);
     if (a[0].dtype == MOE_DTYPE_F32) {
-        colsum_kernel<float><<<grid, kColVecs * kColRows, 0, s>>>(a[0], a[1], c0);
-        colsum_finish_kernel<float><<<fin, 256, 0, s>>>(a[0], a[1], f0, int(tiles));
+        launch_spread(colsum_kernel<float>, grid, kColVecs * kColRows, s, a[0], a[1], c0);
+        launch_chained(colsum_finish_kernel<float>, fin, 256, 0, s, a[0], a[1], f0, int(tiles));
     } else {
-        colsum_kernel<__nv_bfloat16><<<grid, kColVecs * kColRows, 0, s>>>(a[0], a[1], c0);
-        colsum_finish_kernel<__nv_bfloat16><<<fin, 256, 0, s>>>(a[0], a[1], f0, int(tiles));
+        launch_spread(colsum_kernel<__nv_bfloat16>, grid, kColVecs * kColRows, s, a[0], a[1], c0);
+        launch_chained(colsum_finish_kernel<__nv_bfloat16>, fin, 256, 0, s, a[0], a[1], f0, int(tiles));
     }
     return cudaGetLastError();
 }
@@ -599,16 +609,16 @@ cudaError_t launch_dact(const DactArgs& a, cudaStream_t s) {
     const int V = a.dtype == MOE_DTYPE_F32 ? 4 : 8;
     const int splits = dact_splits(a.T, a.N);
     const dim3 grid((a.N / V + kColVecs - 1) / kColVecs, splits);
-    if (a.dtype == MOE_DTYPE_F32) dact_kernel<float><<<grid, kColVecs * kColRows, 0, s>>>(a, splits);
-    else dact_kernel<__nv_bfloat16><<<grid, kColVecs * kColRows, 0, s>>>(a, splits);
+    if (a.dtype == MOE_DTYPE_F32) launch_chained(dact_kernel<float>, grid, kColVecs * kColRows, 0, s, a, splits);
+    else launch_chained(dact_kernel<__nv_bfloat16>, grid, kColVecs * kColRows, 0, s, a, splits);
     if (a.partial) {
         ColsumArgs c;
         c.cols = a.N;
         c.out = a.db;
         c.partial = a.partial;
         const unsigned fin = (a.N + 31) / 32;
-        if (a.dtype == MOE_DTYPE_F32) colsum_finish_kernel<float><<<fin, 256, 0, s>>>(c, c, fin, splits);
-        else colsum_finish_kernel<__nv_bfloat16><<<fin, 256, 0, s>>>(c, c, fin, splits);
+        if (a.dtype == MOE_DTYPE_F32) launch_chained(colsum_finish_kernel<float>, fin, 256, 0, s, c, c, fin, splits);
+        else launch_chained(colsum_finish_kernel<__nv_bfloat16>, fin, 256, 0, s, c, c, fin, splits);
     }
     return cudaGetLastError();
 }

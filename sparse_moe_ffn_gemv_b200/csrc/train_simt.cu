@@ -188,6 +188,7 @@ struct Simt {
 template <typename F, bool FWD>
 __global__ void __launch_bounds__(F::THREADS) simt_gemm_kernel(const __grid_constant__ Simt S) {
     __shared__ typename F::Shared sh;
+    pdl_begin();
     constexpr int kBM = F::B, kBN = F::B;
     int64_t t = blockIdx.x;
     int i = 0;
@@ -216,8 +217,8 @@ cudaError_t launch_form(Simt& S, cudaStream_t s) {
         S.end[i] = tiles;
     }
     if (tiles >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-    if (S.p[0].kind == kNT) simt_gemm_kernel<F, true><<<unsigned(tiles), F::THREADS, 0, s>>>(S);
-    else simt_gemm_kernel<F, false><<<unsigned(tiles), F::THREADS, 0, s>>>(S);
+    if (S.p[0].kind == kNT) launch_chained(simt_gemm_kernel<F, true>, unsigned(tiles), F::THREADS, 0, s, S);
+    else launch_chained(simt_gemm_kernel<F, false>, unsigned(tiles), F::THREADS, 0, s, S);
     return cudaGetLastError();
 }
 

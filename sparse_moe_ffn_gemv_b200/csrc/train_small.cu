@@ -49,17 +49,12 @@ __global__ void __launch_bounds__(kSmallThreads, GATED ? 1 : TT <= 2 ? 8 : 4) sm
     }
     float acc[TT][R] = {};
     const bool live = n0 < a.N;
-    if (a.wait_input) {
-        // the launch before this one writes x: bring the first weights under way, then wait
-        if (live)
-            for (int c = kw * 32 + lane; c < min(vecs, 2 * U * step); c += step)
+    launch_next();
+    if (a.prefetch && live)  // the first weights come under way while the launch before ends
+        for (int c = kw * 32 + lane; c < min(vecs, 2 * U * step); c += step)
 #pragma unroll
-                for (int r = 0; r < R; ++r)
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(w[r] + int64_t(c) * V));
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-    } else {
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    }
+            for (int r = 0; r < R; ++r) asm volatile("prefetch.global.L2 [%0];" ::"l"(w[r] + int64_t(c) * V));
+    wait_before();
     if (live) {
         for (int c0 = kw * 32 + lane; c0 < vecs; c0 += U * step) {
             uint4 wv[U][R];
@@ -67,7 +62,7 @@ __global__ void __launch_bounds__(kSmallThreads, GATED ? 1 : TT <= 2 ? 8 : 4) sm
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int r = 0; r < R; ++r)
-                    wv[u][r] = c0 + u * step < vecs ? ld_stream16(w[r] + int64_t(c0 + u * step) * V) : make_uint4(0, 0, 0, 0);
+                    wv[u][r] = c0 + u * step < vecs ? ld_once16(w[r] + int64_t(c0 + u * step) * V) : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (c0 + u * step >= vecs) break;
@@ -163,17 +158,8 @@ cudaError_t launch_tt(SmallArgs a, cudaStream_t s) {
     a.ks = 1;
     while (a.ks < 8 && int64_t(groups) * a.ks < 148 * 32 && vecs >= 64 * a.ks) a.ks *= 2;
     const int per = 8 / a.ks;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((groups + per - 1) / per);
-    cfg.blockDim = dim3(kSmallThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = a.wait_input ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, small_kernel<T, TT, GATED>, a);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    launch_chained(small_kernel<T, TT, GATED>, dim3((groups + per - 1) / per), dim3(kSmallThreads), 0, s, a);
+    return cudaGetLastError();
 }
 
 template <typename T, bool GATED>

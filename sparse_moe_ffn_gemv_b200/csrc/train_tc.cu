@@ -294,7 +294,7 @@ __device__ __forceinline__ void add_bias(const __nv_bfloat16* b, int c, int limi
     for (int q = 0; q < 4; ++q) {
         if (c + 8 * q >= limit) break;
         float t[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(b + c + 8 * q)), t);
+        unpack8(*reinterpret_cast<const uint4*>(b + c + 8 * q), t);
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[8 * q + j] += t[j];
     }
@@ -502,15 +502,6 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
     // this CTA's reduction blocks of a tile
     auto kb_begin = [&](const Tile& t) { return SPLIT ? t.nk * srank / splits : 0; };
     auto kb_end = [&](const Tile& t) { return SPLIT ? t.nk * (srank + 1) / splits : t.nk; };
-    if (warp == 0) {
-        if constexpr (PAIR) {
-            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(tmem_slot)));
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-        } else {
-            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(tmem_slot)));
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-        }
-    }
     if (warp == 1 && lane == 0) {
         for (int s = 0; s < S::STAGES; ++s) {
             mbar_init(&full[s], 1);
@@ -523,6 +514,18 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
         mbar_init(drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    // no TMEM before the wait, no leave for the next launch before TMEM is had: neither side can hold
+    // what the other waits for
+    wait_before();
+    if (warp == 0) {
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(tmem_slot)));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(tmem_slot)));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        }
     }
     if (P.offsets) {
         for (int e = threadIdx.x; e <= P.E; e += kThreads) {
@@ -557,6 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
     __syncthreads();
     if constexpr (PAIR) cluster_sync();
     fence_after();
+    launch_next();
     const uint32_t tmem = *tmem_slot;
     // tiles of the problems one after the other
     auto tiles_of = [&](const TcTrain& p) {
@@ -1270,12 +1274,17 @@ cudaError_t launch_t(const TcTrain* P, int np, int64_t max_tiles, cudaStream_t s
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = S::SMEM;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = PAIR ? 2 : SPLIT ? P->splits : 1;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = PAIR || SPLIT ? 1 : 0;
+    // Not chained: experts' tiles on single CTAs over more than one round. Their blocks' places, which
+    // share operands by neighbourhood, would be those of the tail before (gate/up after the row copy
+    // 338 -> 344 us, down after gate/up 200 -> 218 us; on pairs 527 -> 516 us).
+    cfg.numAttrs = PAIR || SPLIT || !P->offsets || max_tiles <= sms() ? 2 : 0;
     if (SPLIT) {
         cfg.gridDim = dim3(unsigned(max_tiles) * P->splits);
         if ((err = cudaLaunchKernelEx(&cfg, kern, args)) != cudaSuccess) return err;

@@ -786,6 +786,76 @@ def test_captured_and_replayed_in_two_graphs():
             for (name, _), o, w in zip(calls, outs, want):
                 assert all(torch.equal(a, b) for a, b in zip(o, w)), name
 
+def chain(g, dtype, T, sync):
+    """Operators of every form, one on the other's results, whose inputs are overwritten as soon as
+    the call that reads them is launched. `sync` waits after each."""
+    H = 264
+    spec = spec_of(num_experts=6, top_k=2, hidden=H, intermediate=72, act_dtype=dtype, has_expert_bias=True)
+    dense = spec_of(hidden=H, intermediate=136, act_dtype=dtype)
+    lin, ffn, mlp, norm = (train.Linear(H, H, "gelu", dtype=dtype), train.GatedFfn(spec), train.GatedFfn(dense),
+                           train.Norm(H, "layer", dtype=dtype))
+    w, b = rand(g, (H, H), dtype, H ** -0.5), rand(g, (H,), dtype)
+    wf, wm = planes(spec, g), planes(dense, g)
+    off, slots, wts = R.make_routing(T, spec, g, "cuda")
+    start = rand(g, (T, H), dtype)
+    x, nan = torch.empty_like(start), float("nan")
+
+    def step(y):
+        if sync:
+            torch.cuda.synchronize()
+        return y
+
+    def run():
+        out = []
+        x.copy_(start)                                   # a copy before, a fill after the call
+        y, stats = step(norm.forward(x, b, bias=b))
+        z, pre = step(lin.forward(y, w, bias=b, keep=True))
+        u, _ = step(mlp.forward(z, wm, residual=y, keep=False))
+        v, vpre = step(ffn.forward(u, wf, routing=(off, slots, wts), residual=u))
+        gf = step(ffn.backward(v, u, wf, vpre, routing=(off, slots, wts)))
+        v.fill_(nan)
+        vpre.fill_(nan)
+        dz = gf["x"]
+        dy, dw, db = step(lin.backward(dz, y, w, pre))
+        dz.fill_(nan)
+        dx, dn, dnb = step(norm.backward(dy, x, b, stats))
+        x.fill_(nan)
+        y.fill_(nan)
+        dy.fill_(nan)
+        out += [u, dw, db, dx, dn, dnb, gf["topk_w"]] + [gf[n] for n in sorted(wf)]
+        return out
+
+    return run
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 3, 40, 700])
+def test_calls_one_behind_the_other(dtype, T):
+    """Launches overlap their neighbours' ends; the results are those of calls with a wait between."""
+    want = chain(gen(31), dtype, T, True)()
+    run = chain(gen(31), dtype, T, False)
+    for _ in range(20):
+        for a, b in zip(run(), want):
+            assert torch.isfinite(b).all() and torch.equal(a, b)
+    # the same as a graph, whose calls follow copies, fills and a join of two branches
+    stream, side = torch.cuda.Stream(), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    flag = torch.zeros(1 << 20, device="cuda")
+    with torch.cuda.stream(stream):
+        run()
+        stream.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            side.wait_stream(stream)
+            with torch.cuda.stream(side):
+                flag.zero_()
+            stream.wait_stream(side)
+            got = run()
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
 
 def test_ffn_offsets_past_32_bits():
     """Routed rows whose element offsets pass 2^31: 40,000 tokens in 8 slots each of 7168 values.
