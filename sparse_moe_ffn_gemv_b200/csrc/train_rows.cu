@@ -122,22 +122,14 @@ __global__ void __launch_bounds__(kGatherThreads) gather_padded_kernel(const Gat
     }
 }
 
-// Many rows: the plan, a thread per padded row, and the zero rows; copy_tokens_kernel does the rest.
+// Many rows: the plan, a thread per padded row; copy_tokens_kernel does the rest.
 __global__ void __launch_bounds__(kGatherThreads) plan_rows_kernel(const GatherArgs a) {
     __shared__ PlanSmem sm;
     pdl_begin();
     const RowPlan& p = a.plan;
     const int total = build_plan(p, sm);
-    const int lane = threadIdx.x & 31, step = gridDim.x * kGatherThreads;
-    for (int r0 = blockIdx.x * kGatherThreads + threadIdx.x - lane; r0 < total; r0 += step) {
-        const int r = r0 + lane;  // total is a multiple of 32
-        const int e = expert_of_row(sm.pad, p.E, r);
-        const int slot = plan_row(p, sm, r, e, true);
-        const int i = r - sm.pad[e];
-        unsigned zero = __ballot_sync(0xffffffffu, slot < 0 && (i < sm.cnt[e] || (a.zero_pad && i < (sm.cnt[e] + kRowPad - 1) /
-                                                                                                    kRowPad * kRowPad)));
-        for (; zero; zero &= zero - 1) zero_row(a, r0 + __ffs(zero) - 1, lane);
-    }
+    for (int r = blockIdx.x * kGatherThreads + threadIdx.x; r < total; r += gridDim.x * kGatherThreads)
+        plan_row(p, sm, r, expert_of_row(sm.pad, p.E, r), true);
 }
 
 // Token by token: a token's rows of the sources (a piece of up to kPiece bytes each) come to
@@ -226,15 +218,25 @@ __global__ void __launch_bounds__(kCopyWarps * 32) copy_tokens_kernel(const Gath
             }
         }
     }
-    // rows that no token names (a slot that stands twice): zeros, and of no slot
-    const int total = pad[p.E], step = gridDim.x * blockDim.x;
-    for (int r0 = blockIdx.x * blockDim.x + threadIdx.x - lane; r0 < total; r0 += step) {
-        const bool repeat = is_repeat(p, r0 + lane, p.row_slot[r0 + lane]);
-        if (repeat) {
-            p.row_slot[r0 + lane] = -1;
-            set_status(p.status, MOE_ERR_DEVICE_CHECK);
+    // rows that no token names: padding as far as a reduction reads, dropped slots, and the second
+    // row of a slot that stands twice (of no slot from here on) are zeros. Neighbouring rows go to
+    // different warps, since padding stands together.
+    const int total = pad[p.E], warps = gridDim.x * kCopyWarps;
+    for (int r0 = blockIdx.x * kCopyWarps + warp; r0 < total; r0 += 32 * warps) {
+        const int64_t rl = r0 + int64_t(lane) * warps;
+        bool zero = false;
+        if (rl < total) {
+            const int r = int(rl), slot = p.row_slot[r];
+            if (slot < 0) {
+                const int e = expert_of_row(pad, p.E, r), i = r - pad[e], cnt = p.uoff[e + 1] - p.uoff[e];
+                zero = i < cnt || (a.zero_pad && i < (cnt + kRowPad - 1) / kRowPad * kRowPad);
+            } else if (is_repeat(p, r, slot)) {
+                p.row_slot[r] = -1;
+                set_status(p.status, MOE_ERR_DEVICE_CHECK);
+                zero = true;
+            }
         }
-        for (unsigned m = __ballot_sync(0xffffffffu, repeat); m; m &= m - 1) zero_row(a, r0 + __ffs(m) - 1, lane);
+        for (unsigned m = __ballot_sync(0xffffffffu, zero); m; m &= m - 1) zero_row(a, r0 + (__ffs(m) - 1) * warps, lane);
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
