@@ -1145,9 +1145,14 @@ __global__ void __launch_bounds__(kThreads, 1) tc_train_kernel(const __grid_cons
                         pack_row(f, w);
                         store_rows(sm, lane, w, P.pre + row * P.ldp + col, P.ldp * 2, vrows, bytes);
                     }
-                    if (P.act != MOE_LINEAR_NONE) {
+                    // a loop per activation: its 32 chains run side by side (chosen inside, GELU added 8 us
+                    // to a launch of few tiles, 128 tokens 512 -> 2048 9.0 -> 17.1 us)
+                    if (P.act == MOE_LINEAR_GELU) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) f[j] = linear_act<true>(P.act, f[j]);
+                        for (int j = 0; j < 32; ++j) f[j] = linear_act<true>(MOE_LINEAR_GELU, f[j]);
+                    } else if (P.act == MOE_LINEAR_SILU) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) f[j] = linear_act<true>(MOE_LINEAR_SILU, f[j]);
                     }
                     if (P.row_scale) {
 #pragma unroll
@@ -1412,21 +1417,20 @@ int clusters_of(int s) {
     return n;
 }
 
+// What a tile of nk reduction blocks takes when s CTAs share it, in 10 ns: a block 0.39 us with its
+// weights coming from HBM, the clusters' meeting 0.6 us + 0.2 to 1 us per CTA by the tile's rows
+// (measured whole / by 2 / 4 / 8, us: 16 rows, 16 blocks 11.6 / 9.8 / 8.2 / 8.9, 32 blocks 16.0 /
+// 12.2 / 9.6 / 9.8; 64 rows, 16 blocks 11.9 / 10.3 / 9.2 / 10.4; 128 rows, 8 blocks 9.2 / 10.0 / 10.7 /
+// 13.7, 16 blocks 12.6 / 11.8 / 11.8 / 14.9, 32 blocks 16.9 / 14.2 / 13.3 / 15.7).
+int64_t split_cost(int64_t nk, int s, int64_t rows) {
+    return 39 * ((nk + s - 1) / s) + (s > 1 ? 60 + (rows <= 32 ? 20 : rows <= 64 ? 40 : 100) * s : 0);
+}
 // CTAs per tile (1, 2, 4, 8; at most `most`, what the columns divide into): as many as pay and
-// the SMs hold at once. A reduction block takes a CTA about 0.26 us (four 128 x 256 x 16
-// products), the clusters' meeting 2.5 us + 0.2 to 0.6 us per CTA by the tile's rows (measured:
-// 16 x 256 x 64 5.0 us whole, 7.1 us split in two; 16 x 4096 x 64 about 21 us whole, 10.1 us split
-// in eight; 128 rows over 2048 13.4 us split in eight).
+// the SMs hold at once.
 int splits_of(int64_t tiles, int64_t nk, int most, int64_t rows) {
     int best = 1;
-    int64_t cost = 26 * nk;
-    for (int s = 2; s <= most; s *= 2) {
-        const int64_t c = 26 * ((nk + s - 1) / s) + 250 + (rows > 32 ? 60 : 20) * s;
-        if (c < cost && tiles <= clusters_of(s)) {
-            cost = c;
-            best = s;
-        }
-    }
+    for (int s = 2; s <= most; s *= 2)
+        if (split_cost(nk, s, rows) < split_cost(nk, best, rows) && tiles <= clusters_of(s)) best = s;
     return best;
 }
 
@@ -1549,18 +1553,22 @@ cudaError_t launch_tc_gemms(const GemmArgs* a, int n, cudaStream_t s) {
     if (n > kMaxMix) return cudaErrorInvalidValue;
     for (int i = 0; i < n; ++i)
         if (!set_up(a[i], P[i], pair[i], tiles[i])) return cudaErrorInvalidValue;
-    // together no more tiles than SMs: one launch, split by the longest reduction. Gradients that
-    // were not asked for count here too, so that the others do not depend on them.
-    int64_t sum = 0, nk = 0, rows = 0;
+    // together no more tiles than SMs: one launch, split by the longest reduction, unless one after
+    // the other each is split better and that is worth the launches (7508 tokens 400 -> 1864 60 us
+    // together, 44 apart). Gradients that were not asked for count here too, so that the others do
+    // not depend on them.
+    int64_t sum = 0, nk = 0, rows = 0, apart = 0;
     bool any_pair = false;
     for (int i = 0; i < n; ++i) {
+        const int64_t r = P[i].tn ? P[i].mrows : row_hint(a[i].plan, a[i].M);
         sum += tiles[i];
         nk = std::max<int64_t>(nk, P[i].nk);
-        rows = std::max<int64_t>(rows, P[i].tn ? P[i].mrows : row_hint(a[i].plan, a[i].M));
+        rows = std::max(rows, r);
+        apart += split_cost(P[i].nk, P[i].splits, r) + 250;
         any_pair = any_pair || pair[i];
     }
-    if (n > 1 && !any_pair && sum <= sms()) {
-        const int splits = splits_of(sum, nk, 8, rows);
+    const int splits = splits_of(sum, nk, 8, rows);
+    if (n > 1 && !any_pair && sum <= sms() && split_cost(nk, splits, rows) + 250 <= apart) {
         int m = 0;
         sum = 0;
         for (int i = 0; i < n; ++i) {
