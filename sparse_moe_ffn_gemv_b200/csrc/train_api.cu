@@ -280,7 +280,7 @@ moe_status moe_linear_forward(const moe_linear_desc* d, const void* x, int64_t l
     MOE_CHECK(check_ws(ws, ws_bytes, linear_ws(d, T, false).total));
     MOE_CHECK(apart(x, ldx, K, y, ldy, N, T, d->dtype, false));
     MOE_CHECK(apart(residual, ldr, N, y, ldy, N, T, d->dtype, true));
-    if (small_form(T, int64_t(K) * N, d->dtype)) {
+    if (small_form(T, int64_t(K) * N, false, d->dtype)) {
         SmallArgs a;
         a.T = int(T); a.K = K; a.N = N; a.dtype = d->dtype; a.act = d->activation;
         a.x = x; a.ldx = ldx; a.w = w; a.bias = bias;
@@ -410,7 +410,7 @@ moe_status moe_ffn_forward(const moe_config* cfg, const moe_weights* w, const vo
     MOE_CHECK(apart(residual, ldr, f.K, y, ldy, f.K, T, f.dtype, true));
     cudaStream_t s = (cudaStream_t)stream;
     const RowPlan p = row_plan(f, expert_offsets, sorted_slot, ws, L, device_status);
-    if (dense && small_form(T, 3 * int64_t(f.K) * f.I, f.dtype)) {
+    if (dense && small_form(T, 3 * int64_t(f.K) * f.I, true, f.dtype)) {
         SmallArgs a;
         a.T = int(T); a.K = f.K; a.N = f.I; a.dtype = f.dtype;
         a.gated = true; a.interleaved = f.il; a.act = cfg->activation; a.limit = cfg->swiglu_limit;

@@ -104,12 +104,14 @@ cudaError_t launch_tc_gemms(const GemmArgs* a, int n, cudaStream_t s);
 
 // The forward products for a few tokens, both types.
 constexpr int kSmallT = 4;
-// Whether they take this form: one or two tokens, or up to four over at most 10 MB of weights
-// (weights cold, us, this / tensor cores: 2048 x 2048 1 token 6.2 / 11.4, 4 tokens 10.2 / 11.5;
-// 3584 x 7168 1 token 15.4 / 19.1, 2 tokens 20.3 / 19.1, 4 tokens 28.8 / 19.1; gated FFN 2048 x 768
-// 4 tokens 18.7 / 21.3, 7168 x 2048 2 tokens 37.5 / 39.4, 4 tokens 57.1 / 39.4).
-inline bool small_form(int64_t T, int64_t weights, int dtype) {
-    return T <= 2 || (T <= kSmallT && (dtype == MOE_DTYPE_F32 || weights <= 5 << 20));
+// Whether they take this form: one or two tokens, or up to four over at most 20 MB of weights, a
+// gated FFN's three planes at most 48 MB (its other form is two launches of few tiles). Weights cold,
+// back to back, us, this / tensor cores: 2048 x 2048 4 tokens 8.4 / 9.9, 4096 x 2048 10.9 / 11.7, 3584 x
+// 3584 (26 MB) 14.3 / 12.2, 3584 x 7168 2 tokens 13.9 / 15.6, 4 tokens 21.9 / 16.0; gated FFN 4 tokens
+// 2048 x 768 12.7 / 17.5, 7168 x 768 23.4 / 26.4, 3584 x 2048 (44 MB) 24.6 / 25.1, 7168 x 2048 (88 MB)
+// 2 tokens 26.6 / 36, 4 tokens 57 / 36.
+inline bool small_form(int64_t T, int64_t weights, bool gated, int dtype) {
+    return T <= 2 || (T <= kSmallT && (dtype == MOE_DTYPE_F32 || weights <= (gated ? 24 << 20 : 10 << 20)));
 }
 struct SmallArgs {
     int T = 0, K = 0, N = 0;  // N: outputs (gated: units)
