@@ -147,53 +147,71 @@ __global__ void __launch_bounds__(kNormThreads) norm_forward_kernel(const NormAr
     }
 }
 
+// The thread's 16 bytes at src to its place in shared memory, asynchronously; read once.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint64_t pol) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(pol) : "memory");
+}
+// Until at most n of the thread's groups of copies are under way (the instruction takes a constant).
+__device__ __forceinline__ void copies_left(int n) {
+    switch (n) {
+        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+        case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+        case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+    }
+}
+
 // Backward for rows of up to 4 vectors per thread: one read of x and dy serves dx, dw and db.
-// Two blocks per SM walk the rows; x and dy of the next rows are brought to shared memory by
-// bulk copies meanwhile (registers hold the running column sums, so they cannot hold loads in
-// flight as well). Each thread keeps its columns' sums over all of the block's rows; the
-// block's rows groups add up in order at the end, then norm_finish_kernel adds the blocks.
+// Two blocks per SM walk the rows; x and dy of the next rows are brought to shared memory
+// meanwhile (registers hold the running column sums, so they cannot hold loads in flight as
+// well). Each thread copies the vectors that it reads itself and waits for them in hardware, so
+// that no wait can give up: the call has no status to say so in. Each thread keeps its columns'
+// sums over all of the block's rows; the block's row groups add up in order at the end, then
+// norm_finish_kernel adds the blocks.
 constexpr int kNormStages = 8;
 template <typename T, bool LAYER>
 __global__ void __launch_bounds__(kNormThreads, 2) norm_backward_rows_kernel(const NormArgs a, int tpr, int stages) {
     constexpr int V = Vec<T>::N;
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ float2 red[2][kNormThreads / 32];
-    __shared__ uint64_t full[kNormStages];
     const int n = a.H / V, G = kNormThreads / tpr, g = threadIdx.x / tpr, c0 = threadIdx.x % tpr;
     const uint32_t row_bytes = uint32_t(a.H) * sizeof(T);
     const uint4* sw = reinterpret_cast<const uint4*>(sm);
     uint8_t* ring = sm + (row_bytes + 127) / 128 * 128;
     const uint32_t stage_bytes = 2 * G * row_bytes;
     const int64_t groups = (a.T + G - 1) / G;
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
     pdl_begin();
+    const uint64_t pol = policy_evict_first();
+    // the thread's vectors of row group grp, one group of copies (empty past the last row)
+    auto fill = [&](int64_t grp, int st) {
+        const int64_t t = grp * G + g;
+        if (t < a.T) {
+            const uint32_t d = su32(ring + st * stage_bytes + g * 2 * row_bytes);
+            const T* x = static_cast<const T*>(a.x) + t * a.ldx;
+            const T* dy = static_cast<const T*>(a.dy) + t * a.lddy;
+#pragma unroll
+            for (int i = 0; i < kVpt; ++i) {
+                const int c = c0 + i * tpr;
+                if (c >= n) break;
+                copy16(d + c * 16, x + c * V, pol);
+                copy16(d + row_bytes + c * 16, dy + c * V, pol);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int i = 0; i < stages - 1; ++i) fill(blockIdx.x + int64_t(i) * gridDim.x, i);
     for (int c = threadIdx.x; c < n; c += kNormThreads)
         reinterpret_cast<uint4*>(sm)[c] = reinterpret_cast<const uint4*>(a.w)[c];
     __syncthreads();
-    const uint64_t pol = policy_evict_first();
-    auto fill = [&](int64_t grp, int st) {  // one thread
-        const int64_t t0 = grp * G;
-        const int rows = int(min(int64_t(G), a.T - t0));
-        mbar_expect_tx(&full[st], 2 * rows * row_bytes);
-        for (int r = 0; r < rows; ++r) {
-            uint8_t* d = ring + st * stage_bytes + r * 2 * row_bytes;
-            bulk_g2s(d, static_cast<const T*>(a.x) + (t0 + r) * a.ldx, row_bytes, &full[st], pol);
-            bulk_g2s(d + row_bytes, static_cast<const T*>(a.dy) + (t0 + r) * a.lddy, row_bytes, &full[st], pol);
-        }
-    };
-    if (threadIdx.x == 0)
-        for (int i = 0; i < stages; ++i)
-            if (blockIdx.x + int64_t(i) * gridDim.x < groups) fill(blockIdx.x + int64_t(i) * gridDim.x, i);
     float2 aw[kVpt][V / 2], ab[kVpt][V / 2];
 #pragma unroll
     for (int i = 0; i < kVpt; ++i)
 #pragma unroll
         for (int q = 0; q < V / 2; ++q) aw[i][q] = ab[i][q] = make_float2(0.f, 0.f);
     int st = 0, it = 0;
-    uint32_t phase = 0;
     auto stats_of = [&](int64_t grp) {
         const int64_t t = grp * G + g;
         return t < a.T ? *reinterpret_cast<const float2*>(a.cstats + 2 * t) : make_float2(0.f, 0.f);
@@ -204,7 +222,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_backward_rows_kernel(con
         const bool live = t < a.T;
         const float mean = ms.x, rstd = ms.y;
         ms = stats_of(grp + gridDim.x);  // of the next row, while this one is worked on
-        if (!mbar_try(&full[st], phase) && !mbar_wait(&full[st], phase, gtimer() + 2000000000ull)) break;
+        copies_left(stages - 2);
         const uint4* sx = reinterpret_cast<const uint4*>(ring + st * stage_bytes + g * 2 * row_bytes);
         const uint4* sd = reinterpret_cast<const uint4*>(ring + st * stage_bytes + g * 2 * row_bytes + row_bytes);
         float2 t1 = make_float2(0.f, 0.f), t2 = t1;  // sums of dy w and dy w (x - mean)
@@ -232,12 +250,8 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_backward_rows_kernel(con
         float s1 = t1.x + t1.y, s2 = (t2.x + t2.y) * rstd;
         group_sum2(s1, s2, tpr, red[it & 1]);
         // every thread is done with the rows before these: bring that stage's next rows
-        const int64_t nxt = grp + int64_t(stages - 1) * gridDim.x;
-        if (threadIdx.x == 0 && it > 0 && nxt < groups) fill(nxt, st == 0 ? stages - 1 : st - 1);
-        if (++st == stages) {
-            st = 0;
-            phase ^= 1u;
-        }
+        fill(grp + int64_t(stages - 1) * gridDim.x, st == 0 ? stages - 1 : st - 1);
+        if (++st == stages) st = 0;
         if (!live || !a.dx) continue;
         // dx = rstd g - rstd mean(g) - (x - mean) rstd^2 mean(g xh)
         const float k1 = -rstd * (s1 / float(a.H)), k2 = -rstd * rstd * (s2 / float(a.H));
@@ -262,7 +276,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_backward_rows_kernel(con
         }
     }
     if (!a.partial) return;
-    // the row groups' sums, one group after the other (the ring is free: every copy was waited for)
+    // the row groups' sums, one group after the other (the ring is free: the copies still under way are empty)
     __syncthreads();
     float* acc = reinterpret_cast<float*>(ring);
     for (int j = 0; j < G; ++j) {
