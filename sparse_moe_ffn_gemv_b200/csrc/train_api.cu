@@ -89,14 +89,10 @@ cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t s) {
     return g.dtype == MOE_DTYPE_F32 ? launch_simt_gemm(&g, 1, s) : launch_tc_gemm_nt(g, s);
 }
 
-// A backward pass's independent products; those without an output are left out.
+// A backward pass's independent products. Those without an output are not computed, but count in the
+// choice of form, so that the others do not depend on what was asked for.
 cudaError_t launch_gemms(const GemmArgs* g, int n, cudaStream_t s) {
-    if (g[0].dtype != MOE_DTYPE_F32) return launch_tc_gemms(g, n, s);
-    GemmArgs want[kMaxSimt];
-    int m = 0;
-    for (int i = 0; i < n; ++i)
-        if (g[i].out) want[m++] = g[i];
-    return m ? launch_simt_gemm(want, m, s) : cudaSuccess;
+    return g[0].dtype == MOE_DTYPE_F32 ? launch_simt_gemm(g, n, s) : launch_tc_gemms(g, n, s);
 }
 
 struct LinearWs {

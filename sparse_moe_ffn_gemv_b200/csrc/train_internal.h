@@ -94,7 +94,7 @@ struct GemmArgs {
     int dtype = MOE_DTYPE_BF16;        // a, b, bias, residual, pre
     int out_f32 = 0;                   // out is f32 instead
 };
-// f32: n independent products (at most kMaxSimt) in one launch.
+// f32: n independent products (at most kMaxSimt) in one launch; those without an output are not computed.
 constexpr int kMaxSimt = 3;
 cudaError_t launch_simt_gemm(const GemmArgs* a, int n, cudaStream_t s);
 // bf16: one kNT product; up to three independent kNN and kTN products of one plan (those

@@ -226,14 +226,16 @@ cudaError_t launch_form(Simt& S, cudaStream_t s) {
 
 cudaError_t launch_simt_gemm(const GemmArgs* a, int n, cudaStream_t s) {
     Simt S;
-    S.n = n;
-    int64_t tiles = 0;  // of 64 x 64
+    S.n = 0;
+    if (n > kMaxSimt) return cudaErrorInvalidValue;
+    int64_t tiles = 0;  // of 64 x 64, of all products: the form, and with it the order of their sums, is the pass's
     for (int i = 0; i < n; ++i) {
-        S.p[i] = a[i];
+        if (a[i].out) S.p[S.n++] = a[i];
         const bool grouped = a[i].plan.offsets != nullptr;
         const int64_t rows = a[i].kind != kTN && grouped ? a[i].plan.S : a[i].M;
         tiles += ((rows + 63) / 64) * ((a[i].N + 63) / 64) * (a[i].kind == kTN && grouped ? a[i].plan.E : 1);
     }
+    if (S.n == 0) return cudaSuccess;
     return tiles >= 2 * 148 ? launch_form<Form<16, 1, 32>>(S, s) : launch_form<Form<8, 4, 16>>(S, s);
 }
 

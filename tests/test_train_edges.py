@@ -5,7 +5,7 @@ import torch
 
 import train_ref as R
 from sparse_moe_ffn_gemv_b200 import train
-from test_train_ops import padded, rand, gen, ok
+from test_train_ops import ffn_case, gen, ok, padded, rand, spec_of
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +33,39 @@ def test_norm_backward_over_many_rows(dtype, T, H, kind, pad):
     again = op.backward(dy, x, w, stats)
     assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
     assert torch.equal(op.backward(dy, x, w, stats, input_grad=False)[1], dw)
+
+
+# ------------------------------------------------------------------ f32 products past a threshold
+@pytest.mark.parametrize("T,K,N,act", [(1200, 768, 768, "silu"), (1201, 772, 764, "none"), (2600, 516, 1028, "gelu")])
+def test_f32_gradients_do_not_depend_on_the_others(T, K, N, act):
+    """Sizes at which the products of the pass together, but not each alone, take the form of large
+    problems: a gradient asked for alone has the same bits."""
+    g = gen(T + K)
+    x, w, dy = rand(g, (T, K), "f32"), rand(g, (N, K), "f32", K ** -0.5), rand(g, (T, N), "f32")
+    pre = rand(g, (T, N), "f32", 1.5) if act != "none" else None
+    op = train.Linear(K, N, activation=act, dtype="f32")
+    dx, dw, db = op.backward(dy, x, w, pre=pre)
+    want = R.linear_backward(dy, x, w, pre, act)
+    for got, ref, name in zip((dx, dw, db), want, ("dx", "dw", "db")):
+        R.check(got, ref, name)
+    for kw in (dict(input_grad=False), dict(weight_grad=False), dict(bias_grad=False), dict(input_grad=False, bias_grad=False),
+               dict(weight_grad=False, bias_grad=False), dict(input_grad=False, weight_grad=False)):
+        for alone, got in zip(op.backward(dy, x, w, pre=pre, **kw), (dx, dw, db)):
+            assert alone is None or torch.equal(alone, got)
+    ok(op)
+
+
+@pytest.mark.parametrize("T,kw", [
+    (2000, dict(hidden=388, intermediate=260)), (1300, dict(num_experts=3, top_k=2, hidden=260, intermediate=132, has_expert_bias=True)),
+])
+def test_f32_ffn_weight_gradients_do_not_depend_on_the_input_gradient(T, kw):
+    spec, g, w, routing = ffn_case(T, None, dict(kw, act_dtype="f32"))
+    x, dy = (rand(g, (T, spec.hidden), "f32") for _ in range(2))
+    pre = rand(g, (T * spec.top_k, 2 * spec.intermediate), "f32", 1.2)
+    op = train.GatedFfn(spec)
+    got = op.backward(dy, x, w, pre, routing=routing)
+    less = op.backward(dy, x, w, pre, routing=routing, input_grad=False)
+    ok(op)
+    assert set(got) - set(less) == {"x"}
+    for n in less:
+        assert torch.equal(less[n], got[n]), n
