@@ -69,3 +69,44 @@ def test_f32_ffn_weight_gradients_do_not_depend_on_the_input_gradient(T, kw):
     assert set(got) - set(less) == {"x"}
     for n in less:
         assert torch.equal(less[n], got[n]), n
+
+
+LARGE_F32 = [  # at least 296 tiles of 64 x 64 in each product, with remainders
+    (2100, None, dict(hidden=580, intermediate=324)),
+    (2101, None, dict(hidden=580, intermediate=324, gate_up_interleaved=True, has_expert_bias=True,
+                      activation="swiglu_clamped", swiglu_limit=1.0)),
+    (900, 44, dict(num_experts=46, top_k=4, hidden=324, intermediate=164, has_expert_bias=True)),
+]
+
+
+@pytest.mark.parametrize("T,K,N", [(1501, 772, 836), (4099, 36, 324), (330, 2500, 4100)])
+def test_large_f32_linear(T, K, N):
+    g = gen(T + K)
+    x, w, b = padded(g, T, K, 4, "f32"), rand(g, (N, K), "f32", K ** -0.5), rand(g, (N,), "f32", 0.3)
+    r, dy = padded(g, T, N, 8, "f32"), padded(g, T, N, 4, "f32")
+    op = train.Linear(K, N, activation="silu", dtype="f32")
+    y, pre = op.forward(x, w, bias=b, residual=r, keep=True)
+    want_y, want_z = R.linear_forward(x, w, b, r, "silu")
+    R.check(y, want_y, "y")
+    R.check(pre, want_z, "pre")
+    want = R.linear_backward(dy, x, w, pre, "silu")
+    for got, ref, name in zip(op.backward(dy, x, w, pre=pre), want, ("dx", "dw", "db")):
+        R.check(got, ref, name)
+    ok(op)
+
+
+@pytest.mark.parametrize("T,experts,kw", LARGE_F32)
+def test_large_f32_ffn(T, experts, kw):
+    spec, g, w, routing = ffn_case(T, experts, dict(kw, act_dtype="f32"))
+    x, dy = (padded(g, T, spec.hidden, 4, "f32") for _ in range(2))
+    op = train.GatedFfn(spec)
+    y, pre = op.forward(x, w, routing=routing)
+    want_y, want_pre = R.ffn_forward(x, w, spec, routing, None)
+    R.check(pre, want_pre, "pre")
+    R.check(y, want_y, "y")
+    got = op.backward(dy, x, w, pre, routing=routing)
+    ok(op)
+    want = R.ffn_backward(dy, x, w, pre, spec, routing)
+    assert set(got) == set(want)
+    for name in want:
+        R.check(got[name], want[name], name)
