@@ -446,8 +446,7 @@ cudaError_t backward_rows(const NormArgs& a, int parts, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         allowed.fetch_or(bit);
     }
-    launch_chained(norm_backward_rows_kernel<T, LAYER>, parts, kNormThreads, ring.bytes, s, a, tpr, ring.stages);
-    return cudaGetLastError();
+    return launch_chained(norm_backward_rows_kernel<T, LAYER>, parts, kNormThreads, ring.bytes, s, a, tpr, ring.stages);
 }
 
 template <typename T>
@@ -462,24 +461,22 @@ cudaError_t backward_t(NormArgs a, cudaStream_t s) {
         const cudaError_t e = a.kind == MOE_NORM_LAYER ? backward_rows<T, true>(a, parts, s) : backward_rows<T, false>(a, parts, s);
         if (e != cudaSuccess) return e;
     } else {
-        if (a.dx) launch_chained(norm_dx_kernel<T>, unsigned(std::min<int64_t>(a.T, 148 * 8)), kNormThreads, 0, s, a);
-        if (sums) launch_chained(norm_dw_kernel<T>, dim3((a.H / V + kColVecs - 1) / kColVecs, parts), kColVecs * kColRows, 0, s, a);
+        if (a.dx) MOE_LAUNCH(launch_chained(norm_dx_kernel<T>, unsigned(std::min<int64_t>(a.T, 148 * 8)), kNormThreads, 0, s, a));
+        if (sums) MOE_LAUNCH(launch_chained(norm_dw_kernel<T>, dim3((a.H / V + kColVecs - 1) / kColVecs, parts), kColVecs * kColRows, 0, s, a));
     }
-    if (sums) launch_chained(norm_finish_kernel<T>, dim3((a.H + 31) / 32, a.db ? 2 : 1), 256, 0, s, a, parts);
-    return cudaGetLastError();
+    if (sums) MOE_LAUNCH(launch_chained(norm_finish_kernel<T>, dim3((a.H + 31) / 32, a.db ? 2 : 1), 256, 0, s, a, parts));
+    return cudaSuccess;
 }
 
 template <typename T>
 cudaError_t forward_t(const NormArgs& a, cudaStream_t s) {
     const int tpr = threads_per_row(a.H, Vec<T>::N);
     if (!tpr) {
-        launch_chained(norm_forward_kernel<T>, unsigned(std::min<int64_t>(a.T, 148 * 8)), kNormThreads, 0, s, a);
-        return cudaGetLastError();
+        return launch_chained(norm_forward_kernel<T>, unsigned(std::min<int64_t>(a.T, 148 * 8)), kNormThreads, 0, s, a);
     }
     const unsigned grid = unsigned((a.T + kNormThreads / tpr - 1) / (kNormThreads / tpr));
-    if (a.kind == MOE_NORM_LAYER) launch_chained(norm_forward_rows_kernel<T, true>, grid, kNormThreads, 0, s, a, tpr);
-    else launch_chained(norm_forward_rows_kernel<T, false>, grid, kNormThreads, 0, s, a, tpr);
-    return cudaGetLastError();
+    if (a.kind == MOE_NORM_LAYER) return launch_chained(norm_forward_rows_kernel<T, true>, grid, kNormThreads, 0, s, a, tpr);
+    return launch_chained(norm_forward_rows_kernel<T, false>, grid, kNormThreads, 0, s, a, tpr);
 }
 
 }  // namespace

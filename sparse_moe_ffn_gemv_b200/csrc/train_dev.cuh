@@ -249,8 +249,15 @@ __device__ __forceinline__ uint4 ld_once16(const void* p) {
     return r;
 }
 
+// The launches return their own error and leave none behind; what starts several returns the first
+// (a launch that fails and one after it that does not is an error too).
+#define MOE_LAUNCH(expr)                         \
+    do {                                         \
+        const cudaError_t e_ = (expr);           \
+        if (e_ != cudaSuccess) return e_;        \
+    } while (0)
 template <typename... P, typename... A>
-cudaError_t launch_chained(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
+[[nodiscard]] cudaError_t launch_chained(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
@@ -261,11 +268,13 @@ cudaError_t launch_chained(void (*kern)(P...), dim3 grid, dim3 block, size_t sme
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, P(args)...);
+    if (e != cudaSuccess) (void)cudaGetLastError();
+    return e;
 }
 // The same where the grid is small, else plain.
 template <typename... P, typename... A>
-cudaError_t launch_spread(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t s, A... args) {
+[[nodiscard]] cudaError_t launch_spread(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t s, A... args) {
     if (int64_t(grid.x) * grid.y <= 64) return launch_chained(kern, grid, block, 0, s, args...);
     kern<<<grid, block, 0, s>>>(args...);
     return cudaGetLastError();

@@ -542,10 +542,9 @@ cudaError_t launch_gather_padded(const GatherArgs& a, cudaStream_t s) {
     const unsigned grid = grid_for(a.plan.max_rows, kGatherThreads / 32, 148 * 4);
     // few rows: one launch that copies as it plans; else (and for the bias products) two
     if (!a.down_b && a.plan.S * a.K * a.es < kCopyBytes) {
-        launch_chained(gather_padded_kernel, grid, kGatherThreads, 0, s, a);
-        return cudaGetLastError();
+        return launch_chained(gather_padded_kernel, grid, kGatherThreads, 0, s, a);
     }
-    launch_chained(plan_rows_kernel, grid_for(a.plan.max_rows, kGatherThreads, 148 * 2), kGatherThreads, 0, s, a);
+    MOE_LAUNCH(launch_chained(plan_rows_kernel, grid_for(a.plan.max_rows, kGatherThreads, 148 * 2), kGatherThreads, 0, s, a));
     const int64_t row = int64_t(a.K) * a.es;
     const int smem = int(std::min<int64_t>(kPiece, row)) * (a.src[1] ? 2 : 1) * kCopyWarps;
     static std::atomic<uint64_t> allowed{0};
@@ -566,19 +565,16 @@ cudaError_t launch_gather_padded(const GatherArgs& a, cudaStream_t s) {
 cudaError_t launch_sum_slots(const SumSlotsArgs& a, cudaStream_t s) {
     const int V = a.dtype == MOE_DTYPE_F32 ? 4 : 8;
     const unsigned grid = grid_for(a.plan.T * (a.K / V), 256, 148 * 16);
-    if (a.dtype == MOE_DTYPE_F32) launch_spread(sum_slots_kernel<float>, grid, 256, s, a);
-    else launch_spread(sum_slots_kernel<__nv_bfloat16>, grid, 256, s, a);
-    return cudaGetLastError();
+    if (a.dtype == MOE_DTYPE_F32) return launch_spread(sum_slots_kernel<float>, grid, 256, s, a);
+    return launch_spread(sum_slots_kernel<__nv_bfloat16>, grid, 256, s, a);
 }
 
 cudaError_t launch_gated_forward(const GatedArgs& a, cudaStream_t s) {
-    launch_chained(gated_forward_kernel, grid_for(a.plan.max_rows, 8, 148 * 8), 256, 0, s, a);
-    return cudaGetLastError();
+    return launch_chained(gated_forward_kernel, grid_for(a.plan.max_rows, 8, 148 * 8), 256, 0, s, a);
 }
 
 cudaError_t launch_gated_backward(const GatedArgs& a, cudaStream_t s) {
-    launch_chained(gated_backward_kernel, grid_for(a.plan.max_rows, 8, 148 * 8), 256, 0, s, a);
-    return cudaGetLastError();
+    return launch_chained(gated_backward_kernel, grid_for(a.plan.max_rows, 8, 148 * 8), 256, 0, s, a);
 }
 
 cudaError_t launch_dtopk(const GatedArgs& a, const float* partial, int parts, cudaStream_t s) {
@@ -593,13 +589,13 @@ cudaError_t launch_colsum(const ColsumArgs (&a)[2], cudaStream_t s) {
     const int f0 = (a[0].cols + 31) / 32, f1 = (a[1].cols + 31) / 32;
     const dim3 grid(unsigned(tiles), c0 + c1), fin(f0 + f1, a[0].plan.E);
     if (a[0].dtype == MOE_DTYPE_F32) {
-        launch_spread(colsum_kernel<float>, grid, kColVecs * kColRows, s, a[0], a[1], c0);
-        launch_chained(colsum_finish_kernel<float>, fin, 256, 0, s, a[0], a[1], f0, int(tiles));
+        MOE_LAUNCH(launch_spread(colsum_kernel<float>, grid, kColVecs * kColRows, s, a[0], a[1], c0));
+        MOE_LAUNCH(launch_chained(colsum_finish_kernel<float>, fin, 256, 0, s, a[0], a[1], f0, int(tiles)));
     } else {
-        launch_spread(colsum_kernel<__nv_bfloat16>, grid, kColVecs * kColRows, s, a[0], a[1], c0);
-        launch_chained(colsum_finish_kernel<__nv_bfloat16>, fin, 256, 0, s, a[0], a[1], f0, int(tiles));
+        MOE_LAUNCH(launch_spread(colsum_kernel<__nv_bfloat16>, grid, kColVecs * kColRows, s, a[0], a[1], c0));
+        MOE_LAUNCH(launch_chained(colsum_finish_kernel<__nv_bfloat16>, fin, 256, 0, s, a[0], a[1], f0, int(tiles)));
     }
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 int dact_splits(int64_t T, int N) {
@@ -611,18 +607,18 @@ cudaError_t launch_dact(const DactArgs& a, cudaStream_t s) {
     const int V = a.dtype == MOE_DTYPE_F32 ? 4 : 8;
     const int splits = dact_splits(a.T, a.N);
     const dim3 grid((a.N / V + kColVecs - 1) / kColVecs, splits);
-    if (a.dtype == MOE_DTYPE_F32) launch_chained(dact_kernel<float>, grid, kColVecs * kColRows, 0, s, a, splits);
-    else launch_chained(dact_kernel<__nv_bfloat16>, grid, kColVecs * kColRows, 0, s, a, splits);
+    if (a.dtype == MOE_DTYPE_F32) MOE_LAUNCH(launch_chained(dact_kernel<float>, grid, kColVecs * kColRows, 0, s, a, splits));
+    else MOE_LAUNCH(launch_chained(dact_kernel<__nv_bfloat16>, grid, kColVecs * kColRows, 0, s, a, splits));
     if (a.partial) {
         ColsumArgs c;
         c.cols = a.N;
         c.out = a.db;
         c.partial = a.partial;
         const unsigned fin = (a.N + 31) / 32;
-        if (a.dtype == MOE_DTYPE_F32) launch_chained(colsum_finish_kernel<float>, fin, 256, 0, s, c, c, fin, splits);
-        else launch_chained(colsum_finish_kernel<__nv_bfloat16>, fin, 256, 0, s, c, c, fin, splits);
+        if (a.dtype == MOE_DTYPE_F32) MOE_LAUNCH(launch_chained(colsum_finish_kernel<float>, fin, 256, 0, s, c, c, fin, splits));
+        else MOE_LAUNCH(launch_chained(colsum_finish_kernel<__nv_bfloat16>, fin, 256, 0, s, c, c, fin, splits));
     }
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 }  // namespace moe

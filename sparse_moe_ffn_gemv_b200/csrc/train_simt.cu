@@ -217,9 +217,8 @@ cudaError_t launch_form(Simt& S, cudaStream_t s) {
         S.end[i] = tiles;
     }
     if (tiles >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-    if (S.p[0].kind == kNT) launch_chained(simt_gemm_kernel<F, true>, unsigned(tiles), F::THREADS, 0, s, S);
-    else launch_chained(simt_gemm_kernel<F, false>, unsigned(tiles), F::THREADS, 0, s, S);
-    return cudaGetLastError();
+    if (S.p[0].kind == kNT) return launch_chained(simt_gemm_kernel<F, true>, unsigned(tiles), F::THREADS, 0, s, S);
+    return launch_chained(simt_gemm_kernel<F, false>, unsigned(tiles), F::THREADS, 0, s, S);
 }
 
 }  // namespace

@@ -158,8 +158,7 @@ cudaError_t launch_tt(SmallArgs a, cudaStream_t s) {
     a.ks = 1;
     while (a.ks < 8 && int64_t(groups) * a.ks < 148 * 32 && vecs >= 64 * a.ks) a.ks *= 2;
     const int per = 8 / a.ks;
-    launch_chained(small_kernel<T, TT, GATED>, dim3((groups + per - 1) / per), dim3(kSmallThreads), 0, s, a);
-    return cudaGetLastError();
+    return launch_chained(small_kernel<T, TT, GATED>, dim3((groups + per - 1) / per), dim3(kSmallThreads), 0, s, a);
 }
 
 template <typename T, bool GATED>

@@ -18,3 +18,14 @@ def test_calls_without_a_status_have_no_wait_that_gives_up():
     for call in re.findall(r"moe_norm_\w+\((.*?)\);", header, flags=re.S):
         assert "device_status" not in call
     assert not re.findall(r"\b(mbar_\w+|gtimer|globaltimer|wait_bar|grid_barrier)\b", code("norm.cu"))
+
+
+def test_no_launch_error_is_dropped():
+    """Every launch's status is returned or checked: a failed one between two that work would be
+    answered with MOE_OK."""
+    for name in sorted(os.listdir(CSRC)):
+        if not (name.startswith("train_") or name == "norm.cu") or not name.endswith(".cu"):
+            continue
+        for line in code(name).splitlines():
+            if re.search(r"\blaunch_(chained|spread)\(", line):
+                assert re.search(r"return launch_|MOE_LAUNCH\(", line), f"{name}: {line.strip()}"
