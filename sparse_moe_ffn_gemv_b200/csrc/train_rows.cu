@@ -384,12 +384,12 @@ __global__ void __launch_bounds__(256) dtopk_kernel(const GatedArgs a, const flo
 // 16-byte column vectors; each thread one vector and every 4th row, 8 rows' loads in flight.
 constexpr int kColVecs = 64, kColRows = 4, kColDeep = 8;
 template <typename T>
-__global__ void __launch_bounds__(kColVecs * kColRows) colsum_kernel(const ColsumArgs a0, const ColsumArgs a1, int blocks0) {
+__global__ void __launch_bounds__(kColVecs * kColRows) colsum_kernel(const ColsumArgs a0, const ColsumArgs a1, int blocks0,
+                                                                     int blocks) {
     pdl_begin();
     constexpr int V = Vec<T>::N;
-    const bool second = int(blockIdx.y) >= blocks0;
-    const ColsumArgs& a = second ? a1 : a0;
-    const RowPlan& p = a.plan;
+    __shared__ float sm[kColRows][kColVecs][V + 1];
+    const RowPlan& p = a0.plan;
     const int64_t b = int64_t(blockIdx.x) * kRowTile;
     int64_t end = p.T;
     if (p.offsets) {
@@ -398,46 +398,50 @@ __global__ void __launch_bounds__(kColVecs * kColRows) colsum_kernel(const Colsu
         end = p.poff[e] + (p.uoff[e + 1] - p.uoff[e]);
     }
     end = min(end, b + kRowTile);
-    const int c = ((blockIdx.y - (second ? blocks0 : 0)) * kColVecs + threadIdx.x % kColVecs) * V;
     const int ry = threadIdx.x / kColVecs;
-    float acc[V] = {};
-    if (c < a.cols) {
-        for (int64_t r = b + ry; r < end; r += kColDeep * kColRows) {
-            uint4 f[kColDeep];
-            float sc[kColDeep];
+    for (int cb = blockIdx.y; cb < blocks; cb += gridDim.y) {  // one, up to 65535 column blocks
+        const bool second = cb >= blocks0;
+        const ColsumArgs& a = second ? a1 : a0;
+        const int c = ((cb - (second ? blocks0 : 0)) * kColVecs + threadIdx.x % kColVecs) * V;
+        float acc[V] = {};
+        if (c < a.cols) {
+            for (int64_t r = b + ry; r < end; r += kColDeep * kColRows) {
+                uint4 f[kColDeep];
+                float sc[kColDeep];
 #pragma unroll
-            for (int u = 0; u < kColDeep; ++u) {
-                const int64_t ru = r + u * kColRows;
-                f[u] = make_uint4(0, 0, 0, 0);
-                sc[u] = 1.0f;
-                if (ru >= end) continue;
-                f[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + ru * a.ldx + c);
-                if (a.row_scale) {
-                    const int slot = p.row_slot[ru];
-                    sc[u] = slot < 0 ? 0.0f : a.row_scale[slot];
+                for (int u = 0; u < kColDeep; ++u) {
+                    const int64_t ru = r + u * kColRows;
+                    f[u] = make_uint4(0, 0, 0, 0);
+                    sc[u] = 1.0f;
+                    if (ru >= end) continue;
+                    f[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + ru * a.ldx + c);
+                    if (a.row_scale) {
+                        const int slot = p.row_slot[ru];
+                        sc[u] = slot < 0 ? 0.0f : a.row_scale[slot];
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kColDeep; ++u) {
+                    float v[V];
+                    unpack_vec<T>(f[u], v);
+#pragma unroll
+                    for (int q = 0; q < V; ++q) acc[q] = fmaf(v[q], sc[u], acc[q]);
                 }
             }
-#pragma unroll
-            for (int u = 0; u < kColDeep; ++u) {
-                float v[V];
-                unpack_vec<T>(f[u], v);
-#pragma unroll
-                for (int q = 0; q < V; ++q) acc[q] = fmaf(v[q], sc[u], acc[q]);
-            }
         }
-    }
-    __shared__ float sm[kColRows][kColVecs][V + 1];
+        __syncthreads();  // the column block before has been read
 #pragma unroll
-    for (int q = 0; q < V; ++q) sm[ry][threadIdx.x % kColVecs][q] = acc[q];
-    __syncthreads();
-    if (ry == 0 && c < a.cols) {
-        float* o = a.partial + int64_t(blockIdx.x) * a.cols + c;
+        for (int q = 0; q < V; ++q) sm[ry][threadIdx.x % kColVecs][q] = acc[q];
+        __syncthreads();
+        if (ry == 0 && c < a.cols) {
+            float* o = a.partial + int64_t(blockIdx.x) * a.cols + c;
 #pragma unroll
-        for (int q = 0; q < V; ++q) {
-            float s = 0.f;
+            for (int q = 0; q < V; ++q) {
+                float s = 0.f;
 #pragma unroll
-            for (int y = 0; y < kColRows; ++y) s += sm[y][threadIdx.x][q];
-            o[q] = s;
+                for (int y = 0; y < kColRows; ++y) s += sm[y][threadIdx.x][q];
+                o[q] = s;
+            }
         }
     }
 }
@@ -587,12 +591,12 @@ cudaError_t launch_colsum(const ColsumArgs (&a)[2], cudaStream_t s) {
     const int64_t tiles = (a[0].plan.max_rows + kRowTile - 1) / kRowTile;
     const int c0 = (a[0].cols + per - 1) / per, c1 = (a[1].cols + per - 1) / per;
     const int f0 = (a[0].cols + 31) / 32, f1 = (a[1].cols + 31) / 32;
-    const dim3 grid(unsigned(tiles), c0 + c1), fin(f0 + f1, a[0].plan.E);
+    const dim3 grid(unsigned(tiles), std::min(c0 + c1, 65535)), fin(f0 + f1, a[0].plan.E);
     if (a[0].dtype == MOE_DTYPE_F32) {
-        MOE_LAUNCH(launch_spread(colsum_kernel<float>, grid, kColVecs * kColRows, s, a[0], a[1], c0));
+        MOE_LAUNCH(launch_spread(colsum_kernel<float>, grid, kColVecs * kColRows, s, a[0], a[1], c0, c0 + c1));
         MOE_LAUNCH(launch_chained(colsum_finish_kernel<float>, fin, 256, 0, s, a[0], a[1], f0, int(tiles)));
     } else {
-        MOE_LAUNCH(launch_spread(colsum_kernel<__nv_bfloat16>, grid, kColVecs * kColRows, s, a[0], a[1], c0));
+        MOE_LAUNCH(launch_spread(colsum_kernel<__nv_bfloat16>, grid, kColVecs * kColRows, s, a[0], a[1], c0, c0 + c1));
         MOE_LAUNCH(launch_chained(colsum_finish_kernel<__nv_bfloat16>, fin, 256, 0, s, a[0], a[1], f0, int(tiles)));
     }
     return cudaSuccess;

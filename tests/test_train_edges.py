@@ -110,3 +110,21 @@ def test_large_f32_ffn(T, experts, kw):
     assert set(got) == set(want)
     for name in want:
         R.check(got[name], want[name], name)
+
+
+def test_ffn_bias_gradients_of_very_wide_planes():
+    """2^24 gate and up columns: more blocks of column sums than a launch has in its second
+    dimension."""
+    spec = spec_of(hidden=8, intermediate=1 << 23, act_dtype="f32", has_expert_bias=True)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    new = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    I = spec.intermediate
+    w = {"gate_w": new(1, I, 8), "up_w": new(1, I, 8), "down_w": new(1, 8, I), "gate_b": new(1, I), "up_b": new(1, I),
+         "down_b": new(1, 8)}
+    x, dy, pre = new(3, 8), new(3, 8), new(3, 2 * I)
+    op = train.GatedFfn(spec)
+    got = op.backward(dy, x, w, pre, input_grad=False)
+    ok(op)
+    want = R.ffn_backward(dy, x, w, pre, spec, None)
+    for n in ("gate_b", "up_b", "down_b", "gate_w", "down_w"):
+        R.check(got[n], want[n], n)
