@@ -23,7 +23,8 @@
  * Outputs overlap no input of the call and no other output, except that y may be the residual's
  * tensor (linear, ffn), u (ffn) or x (norm) with its stride. Rows against rows are checked
  * (MOE_ERR_INVALID_ARGUMENT); side by side in wider rows is fine. Widths above 2^28, more than
- * 2^30 rows or slots, and tensors above 2^46 elements are refused (MOE_ERR_SHAPE_OVERFLOW).
+ * 2^30 rows or slots, tensors above 2^46 elements, and matrix products of 2^29 or more tiles of
+ * 64 x 64 results (bf16: 128 x 256) are refused (MOE_ERR_SHAPE_OVERFLOW), by the size calls too.
  *
  * Workspace: ws of at least the matching *_workspace_size bytes for that T, any contents. Calls that may
  * overlap on the GPU (two streams, two graphs) each need their own. NULL is accepted where the

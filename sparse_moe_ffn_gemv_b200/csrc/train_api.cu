@@ -23,7 +23,15 @@ constexpr int64_t kMaxRows = int64_t(1) << 30;   // slots (their padded rows fit
 constexpr int64_t kMaxElems = int64_t(1) << 46;  // elements of any one tensor
 constexpr int kMaxWidth = 1 << 28;               // columns (twice as many, and tiles of them, fit 32 bits)
 
+constexpr int64_t kMaxTiles = int64_t(1) << 29;  // output tiles of a product (three in one launch stay below 2^31)
+
 int esize(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
+
+// Whether the tiles of `planes` products [M, N] are few enough for the kernels' 32-bit tile numbers.
+bool tiles_fit(int64_t M, int64_t N, int64_t planes, int dtype) {
+    const int64_t bm = dtype == MOE_DTYPE_F32 ? 64 : 128, bn = dtype == MOE_DTYPE_F32 ? 64 : 256;
+    return ((M + bm - 1) / bm) * ((N + bn - 1) / bn) * planes < kMaxTiles;
+}
 
 moe_status need(const void* p) {
     return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0 ? MOE_OK : MOE_ERR_INVALID_ARGUMENT;
@@ -80,7 +88,10 @@ moe_status check_linear(const moe_linear_desc* d, int64_t T) {
     if (d->in_features % q || d->out_features % q) return MOE_ERR_INVALID_ARGUMENT;
     if (T < 0) return MOE_ERR_INVALID_ARGUMENT;
     if (d->in_features > kMaxWidth || d->out_features > kMaxWidth) return MOE_ERR_SHAPE_OVERFLOW;
-    if (T > kMaxRows || T * std::max(d->in_features, d->out_features) > kMaxElems) return MOE_ERR_SHAPE_OVERFLOW;
+    const int64_t K = d->in_features, N = d->out_features;
+    if (T > kMaxRows || T * std::max(K, N) > kMaxElems || N * K > kMaxElems) return MOE_ERR_SHAPE_OVERFLOW;
+    if (!tiles_fit(T, N, 1, d->dtype) || !tiles_fit(T, K, 1, d->dtype) || !tiles_fit(N, K, 1, d->dtype))
+        return MOE_ERR_SHAPE_OVERFLOW;
     return MOE_OK;
 }
 
@@ -136,7 +147,11 @@ moe_status check_ffn(const moe_config* c, int64_t T, bool dense, FfnShape* f) {
     if (T > kMaxRows || T * f->k > kMaxRows) return MOE_ERR_SHAPE_OVERFLOW;
     f->S = T * f->k;
     f->rows = dense ? T : max_padded_rows(f->S, f->E);
-    if (f->rows * std::max<int64_t>(f->K, 2 * int64_t(f->I)) > kMaxElems) return MOE_ERR_SHAPE_OVERFLOW;
+    const int64_t K = f->K, I = f->I;  // the planes' own size: moe_config_validate
+    if (f->rows * std::max(K, 2 * I) > kMaxElems) return MOE_ERR_SHAPE_OVERFLOW;
+    if (!tiles_fit(f->rows, 2 * I, 1, f->dtype) || !tiles_fit(f->rows, K, 1, f->dtype) ||
+        !tiles_fit(2 * I, K, f->E, f->dtype) || !tiles_fit(K, I, f->E, f->dtype))
+        return MOE_ERR_SHAPE_OVERFLOW;
     return MOE_OK;
 }
 

@@ -1,0 +1,51 @@
+"""include/moe_train.h on the host (no GPU): sizes past the limits, what an import needs."""
+import ctypes
+import os
+import subprocess
+import sys
+
+import pytest
+
+from sparse_moe_ffn_gemv_b200 import build, inputs
+from sparse_moe_ffn_gemv_b200 import moe as M
+from sparse_moe_ffn_gemv_b200 import train
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OVERFLOW = M.STATUS_CODE["MOE_ERR_SHAPE_OVERFLOW"]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built_library():
+    build.build()
+    yield
+
+
+def size(fn, desc, T, backward):
+    out = ctypes.c_size_t(123)
+    return getattr(train.lib(), fn)(ctypes.byref(desc), T, backward, ctypes.byref(out))
+
+
+@pytest.mark.parametrize("fields,T,status", [
+    ((1 << 24, 1 << 24, 0, 1), 1, OVERFLOW),           # a weight plane of 2^48 elements
+    ((1 << 24, 1 << 24, 0, 0), 0, OVERFLOW),
+    ((1 << 23, 1 << 23, 0, 0), 1, OVERFLOW),           # 2^46 elements: 2^34 tiles of f32
+    ((8, 1 << 28, 0, 1), 1 << 18, OVERFLOW),           # 2^31 tiles of the forward product,
+    ((1 << 28, 8, 0, 1), 1 << 18, OVERFLOW),           # of the input gradient
+    ((8, 1 << 28, 0, 1), 1 << 15, 0), ((8, 1 << 28, 0, 0), 1 << 12, 0),
+    ((1 << 18, 1 << 18, 0, 1), 16, 0),                 # 137 GB of weights
+])
+def test_linear_planes_and_tiles(fields, T, status):
+    for backward in (0, 1):
+        assert size("moe_linear_workspace_size", train.MoeLinearDesc(*fields), T, backward) == status
+
+
+@pytest.mark.parametrize("kw,T,status", [
+    (dict(hidden=1 << 17, intermediate=1 << 19, num_experts=512), 1, OVERFLOW),     # planes of 2^46 elements
+    (dict(hidden=1 << 14, intermediate=1 << 21, num_experts=512), 1, OVERFLOW),     # 2^45: 2^30 tiles of a weight gradient
+    (dict(hidden=8, intermediate=1 << 27, num_experts=1, top_k=1), 1 << 18, OVERFLOW),  # 2^31 tiles of gate and up
+    (dict(hidden=1 << 12, intermediate=1 << 12, num_experts=512), 1 << 14, 0),
+])
+def test_ffn_planes_and_tiles(kw, T, status):
+    spec = inputs.MoeSpec(**{**dict(name="t", config_id=0, num_experts=4, top_k=2), **kw})
+    for backward in (0, 1):
+        assert size("moe_ffn_workspace_size", M.config_from_spec(spec), T, backward) == status
