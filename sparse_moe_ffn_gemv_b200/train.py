@@ -37,10 +37,11 @@ _DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16}
 # What a call needs of PyTorch's CUDA runtime, without the checks of the public wrappers (a current
 # device, a stream and a workspace cost 2 us less per call). The allocator is the same one: memory
 # freed after the launch is handed out again on that stream only, in a graph's pool within it.
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
-_allocate = torch._C._cuda_cudaCachingAllocator_raw_alloc
-_free = torch._C._cuda_cudaCachingAllocator_raw_delete
+# A PyTorch without CUDA has none of them: the module imports there too, and a handle says what is
+# missing.
+_current_device, _current_stream, _allocate, _free = (getattr(torch._C, n, None) for n in (
+    "_cuda_getDevice", "_cuda_getCurrentRawStream", "_cuda_cudaCachingAllocator_raw_alloc",
+    "_cuda_cudaCachingAllocator_raw_delete"))
 
 
 class MoeLinearDesc(ctypes.Structure):

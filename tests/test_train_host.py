@@ -49,3 +49,25 @@ def test_ffn_planes_and_tiles(kw, T, status):
     spec = inputs.MoeSpec(**{**dict(name="t", config_id=0, num_experts=4, top_k=2), **kw})
     for backward in (0, 1):
         assert size("moe_ffn_workspace_size", M.config_from_spec(spec), T, backward) == status
+
+
+def test_import_without_cuda_in_torch():
+    """A PyTorch built without CUDA lacks the runtime's functions: the module imports, the size calls
+    work, and a handle raises."""
+    prog = """
+import torch
+for n in [n for n in dir(torch._C) if n.startswith("_cuda_")]:
+    delattr(torch._C, n)
+import ctypes
+from sparse_moe_ffn_gemv_b200 import train
+n = ctypes.c_size_t()
+assert train.lib().moe_linear_workspace_size(ctypes.byref(train.MoeLinearDesc(64, 64, 1, 1)), 5, 1, ctypes.byref(n)) == 0
+for make in (lambda: train.Linear(64, 64), lambda: train.Norm(64, device="cuda:0")):
+    try:
+        make()
+    except (RuntimeError, AssertionError, AttributeError) as e:
+        print("raised", type(e).__name__)
+"""
+    run = subprocess.run([sys.executable, "-c", prog], cwd=ROOT, capture_output=True, text=True)
+    assert run.returncode == 0, run.stderr
+    assert run.stdout.count("raised") == 2
