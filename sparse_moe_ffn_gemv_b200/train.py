@@ -8,7 +8,8 @@ Argument marshalling only: every step runs in the library's CUDA kernels. A hand
 operator's shape and one status word; weights are passed at each call (a training step changes
 them), outputs and workspaces come from PyTorch's allocator at each call, so calls on several
 streams and captured graphs share nothing but the status word. Tensors are [rows, width], rows
-may be strided. A call runs on `stream`, or on the current stream of the handle's device.
+may be strided. A call runs on `stream`, or on the current stream of the handle's device; with
+`stream` its tensors may be dropped at once, and what it returns belongs to that stream.
 """
 from __future__ import annotations
 
@@ -121,14 +122,19 @@ class _Operator:
         return stream is not None or _current_device() != self._index
 
     @contextlib.contextmanager
-    def _on(self, stream):
+    def _on(self, stream, *tensors):
         """The handle's device and the call's stream made current: what is allocated in the
-        call belongs to the stream that uses it."""
+        call belongs to the stream that uses it. The caller's tensors are marked as in use on a
+        stream that the call names, so that one that is dropped after the call is not handed
+        out again before that stream has passed it."""
         if stream is not None:
             if stream.device != self.device:
                 raise ValueError(f"stream of {stream.device}, handle of {self.device}")
             with torch.cuda.stream(stream):
                 yield
+            for t in (*tensors, self.status):
+                if t is not None:
+                    t.record_stream(stream)
         else:
             with torch.cuda.device(self.device):
                 yield
@@ -204,7 +210,7 @@ class Linear(_Operator):
     def forward(self, x, w, bias=None, residual=None, keep: bool = False, out=None, stream=None):
         """y, or (y, pre) with keep: pre = x W^T + b is what backward needs of an activation."""
         if self._elsewhere(stream):
-            with self._on(stream):
+            with self._on(stream, x, w, bias, residual, out):
                 return self.forward(x, w, bias, residual, keep, out)
         T, K, N = x.shape[0], self.n_in, self.n_out
         xp, ldx = self._rows("x", x, K)
@@ -226,7 +232,7 @@ class Linear(_Operator):
                  weight_grad: bool = True, stream=None):
         """(dx, dw, db); None for a gradient not asked for. A residual's gradient is dy."""
         if self._elsewhere(stream):
-            with self._on(stream):
+            with self._on(stream, dy, x, w, pre):
                 return self.backward(dy, x, w, pre, bias_grad, input_grad, weight_grad)
         T, K, N = x.shape[0], self.n_in, self.n_out
         gp, ldg = self._rows("dy", dy, N, T)
@@ -266,6 +272,10 @@ class GatedFfn(_Operator):
         self.shapes = shapes
         self._planes_numel = [(f, functools.reduce(int.__mul__, s)) for f, s in shapes.items()]
 
+    def _used(self, tensors):
+        """The entries of a dict of planes that the calls read."""
+        return [tensors.get(f) for f in self.shapes]
+
     def _planes(self, tensors):
         w, dtype, index = M.MoeWeights(), self.dtype, self._index
         for f, n in self._planes_numel:
@@ -292,7 +302,7 @@ class GatedFfn(_Operator):
         """(y, pre): y [T, K], and the pre-activations [T*k, 2I] in sorted order that backward
         takes (None without keep)."""
         if self._elsewhere(stream):
-            with self._on(stream):
+            with self._on(stream, u, *self._used(weights), *(routing or ()), residual, out):
                 return self.forward(u, weights, routing, residual, keep, out)
         T = u.shape[0]
         up, ldu = self._rows("u", u, self.K)
@@ -314,7 +324,7 @@ class GatedFfn(_Operator):
                  stream=None) -> Dict[str, torch.Tensor]:
         """Gradients by name: "x" (of u), "topk_w" (routed), and those of the weight planes."""
         if self._elsewhere(stream):
-            with self._on(stream):
+            with self._on(stream, dy, u, *self._used(weights), pre, *(routing or ())):
                 return self.backward(dy, u, weights, pre, routing, input_grad)
         T = u.shape[0]
         gp, ldg = self._rows("dy", dy, self.K, T)
@@ -354,7 +364,7 @@ class Norm(_Operator):
     def forward(self, x, w, bias=None, out=None, stream=None):
         """(y, stats): stats [T, 2] f32 (mean, 1 / sqrt(var + eps)) is what backward takes."""
         if self._elsewhere(stream):
-            with self._on(stream):
+            with self._on(stream, x, w, bias, out):
                 return self.forward(x, w, bias, out)
         T, H = x.shape[0], self.width
         xp, ldx = self._rows("x", x, H)
@@ -375,7 +385,7 @@ class Norm(_Operator):
                  stream=None):
         """(dx, dw, db); db is None for RMS norm or with bias_grad False."""
         if self._elsewhere(stream):
-            with self._on(stream):
+            with self._on(stream, dy, x, w, stats):
                 return self.backward(dy, x, w, stats, bias_grad, input_grad)
         T, H = x.shape[0], self.width
         if bias_grad and self.kind == "rms":
