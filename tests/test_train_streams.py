@@ -75,3 +75,22 @@ def test_a_stream_of_another_operators_results():
     torch.cuda.current_stream().wait_stream(a)
     ok(op)
     assert torch.equal(z, want)
+
+
+def test_captured_on_a_named_stream():
+    """Calls that name the stream which a graph is captured on, with tensors of another stream."""
+    s = torch.cuda.Stream()
+    for op, name, tensors, call in calls():
+        flat = lambda o: [o] if torch.is_tensor(o) else list(o)  # noqa: E731
+        want = flat(call(tensors, torch.cuda.current_stream()))
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            got = flat(call(tensors, s))
+        for _ in range(2):
+            for t in got:
+                t.zero_()
+            torch.cuda.synchronize()
+            graph.replay()
+            ok(op)
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), name
