@@ -99,6 +99,10 @@ typedef struct moe_ffn_grads {
 
 MOE_API moe_status moe_ffn_workspace_size(const moe_config *cfg, int64_t T, int32_t backward, size_t *bytes);
 
+/* The same for calls without a routing (num_experts == 1, top_k == 1), which hold no second copy of
+ * the rows: 101 MB in place of 580 MB for the backward pass of 8192 tokens, 7168 x 2048, bf16. */
+MOE_API moe_status moe_ffn_dense_workspace_size(const moe_config *cfg, int64_t T, int32_t backward, size_t *bytes);
+
 /* y [T, K] (row stride ldy) from u [T, K] (row stride ldu), plus residual [T, K] (row stride
  * ldr) or NULL. pre (optional) is kept for the backward pass; its rows behind the last sorted
  * position (slots that moe_permute dropped) are not written. bf16: h is rounded to bf16 before the down product (the operand type of the

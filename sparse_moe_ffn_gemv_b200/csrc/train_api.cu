@@ -390,8 +390,15 @@ moe_status moe_ffn_workspace_size(const moe_config* cfg, int64_t T, int32_t back
     FfnShape f;
     MOE_CHECK(check_ffn(cfg, T, false, &f));
     if (!bytes) return MOE_ERR_INVALID_ARGUMENT;
-    size_t n = ffn_ws(f, backward != 0).total;
-    *bytes = n;
+    *bytes = ffn_ws(f, backward != 0).total;
+    return MOE_OK;
+}
+
+moe_status moe_ffn_dense_workspace_size(const moe_config* cfg, int64_t T, int32_t backward, size_t* bytes) {
+    FfnShape f;
+    MOE_CHECK(check_ffn(cfg, T, true, &f));
+    if (!bytes) return MOE_ERR_INVALID_ARGUMENT;
+    *bytes = ffn_ws(f, backward != 0).total;
     return MOE_OK;
 }
 

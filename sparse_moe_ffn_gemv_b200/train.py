@@ -26,7 +26,7 @@ from . import moe as M
 # The entry points include/moe_train.h declares.
 EXPORTS = [
     "moe_linear_workspace_size", "moe_linear_forward", "moe_linear_backward",
-    "moe_ffn_workspace_size", "moe_ffn_forward", "moe_ffn_backward",
+    "moe_ffn_workspace_size", "moe_ffn_dense_workspace_size", "moe_ffn_forward", "moe_ffn_backward",
     "moe_norm_workspace_size", "moe_norm_forward", "moe_norm_backward",
 ]
 
@@ -72,6 +72,7 @@ def lib():
         "moe_linear_forward": [lin, vp, i64, vp, vp, vp, i64, i64, vp, i64, vp, vp, sz, vp, vp],
         "moe_linear_backward": [lin, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, sz, vp, vp],
         "moe_ffn_workspace_size": [cfg, i64, i32, szp],
+        "moe_ffn_dense_workspace_size": [cfg, i64, i32, szp],
         "moe_ffn_forward": [cfg, wts, vp, i64, i64, vp, vp, vp, vp, i64, vp, i64, vp, vp, sz, vp, vp],
         "moe_ffn_backward": [cfg, wts, vp, i64, i64, vp, vp, vp, vp, vp, i64, vp, i64, vp, gr, vp, sz, vp, vp],
         "moe_norm_workspace_size": [nrm, i64, i32, szp],
@@ -108,7 +109,7 @@ class _Operator:
         self.lib = lib()
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._tail = (self.status.data_ptr(),)  # what follows the workspace in a call
-        self._ws_bytes: Dict[Tuple[int, int], int] = {}
+        self._ws_bytes: Dict[Tuple[int, int], int] = {}  # by tokens and direction
 
     def device_status(self) -> int:
         """The status device-side checks left since the last call (0: none). Synchronises."""
@@ -160,20 +161,22 @@ class _Operator:
             raise ValueError(f"{name}: strides {(ld, unit)}: the columns of a row must be contiguous")
         return t.data_ptr(), ld if n > 1 else width
 
-    def _size(self, size_fn, desc_ref, T: int, backward: int) -> int:
+    @staticmethod
+    def _size(size_fn, desc_ref, known: Dict, T: int, backward: int) -> int:
         """Bytes of workspace; also the library's check of the operator's shape."""
         out = ctypes.c_size_t(0)
         M._check(size_fn(desc_ref, T, backward, ctypes.byref(out)), size_fn.__name__)
-        if len(self._ws_bytes) >= 1024:
-            self._ws_bytes.clear()
-        self._ws_bytes[(T, backward)] = out.value
+        if len(known) >= 1024:
+            known.clear()
+        known[(T, backward)] = out.value
         return out.value
 
-    def _launch(self, fn, size_fn, desc_ref, T: int, backward: int, *args):
-        """fn(desc, args, workspace, its size, status, stream) on the current stream."""
-        n = self._ws_bytes.get((T, backward))
+    def _launch(self, fn, size_fn, desc_ref, known: Dict, T: int, backward: int, *args):
+        """fn(desc, args, workspace, its size, status, stream) on the current stream. known: what
+        size_fn said before."""
+        n = known.get((T, backward))
         if n is None:
-            n = self._size(size_fn, desc_ref, T, backward)
+            n = self._size(size_fn, desc_ref, known, T, backward)
         stream = _current_stream(self._index)
         ws = _allocate(n, stream) if n else None
         try:
@@ -205,7 +208,7 @@ class Linear(_Operator):
         self.n_in, self.n_out, self.activation = in_features, out_features, activation
         self.desc = MoeLinearDesc(in_features, out_features, LINEAR_ACTIVATION[activation], inputs.DTYPE[dtype])
         self._desc = ctypes.byref(self.desc)
-        self._size(self.lib.moe_linear_workspace_size, self._desc, 0, 0)  # checks the shape
+        self._size(self.lib.moe_linear_workspace_size, self._desc, self._ws_bytes, 0, 0)  # checks the shape
 
     def forward(self, x, w, bias=None, residual=None, keep: bool = False, out=None, stream=None):
         """y, or (y, pre) with keep: pre = x W^T + b is what backward needs of an activation."""
@@ -224,7 +227,7 @@ class Linear(_Operator):
             y = out
             yp, ldy = self._rows("out", out, N, T)
         pre = self._empty(T, N) if keep else None
-        self._launch(self.lib.moe_linear_forward, self.lib.moe_linear_workspace_size, self._desc, T, 0,
+        self._launch(self.lib.moe_linear_forward, self.lib.moe_linear_workspace_size, self._desc, self._ws_bytes, T, 0,
                      xp, ldx, wp, bp, rp, ldr, T, yp, ldy, _p(pre))
         return (y, pre) if keep else y
 
@@ -242,7 +245,7 @@ class Linear(_Operator):
         dx = self._like(x, (T, K)) if input_grad else None
         dw = self._like(w, (N, K)) if weight_grad else None
         db = self._empty(N) if bias_grad else None
-        self._launch(self.lib.moe_linear_backward, self.lib.moe_linear_workspace_size, self._desc, T, 1,
+        self._launch(self.lib.moe_linear_backward, self.lib.moe_linear_workspace_size, self._desc, self._ws_bytes, T, 1,
                      gp, ldg, xp, ldx, wp, pp, T, _p(dx), K, _p(dw), _p(db))
         return dx, dw, db
 
@@ -263,7 +266,9 @@ class GatedFfn(_Operator):
         M._check(M.moe_config_validate(self.cfg), "moe_config_validate")
         E, I, K = spec.num_experts, spec.intermediate, spec.expert_in
         self.E, self.k, self.I, self.K = E, spec.top_k, I, K
-        self._size(self.lib.moe_ffn_workspace_size, self._cfg, 0, 0)  # checks the weight format
+        self._size(self.lib.moe_ffn_workspace_size, self._cfg, self._ws_bytes, 0, 0)  # checks the weight format
+        self._routed = (self.lib.moe_ffn_workspace_size, self._cfg, self._ws_bytes)
+        self._dense = (self.lib.moe_ffn_dense_workspace_size, self._cfg, {})
         shapes = {"gate_up_w": (E, 2 * I, K)} if spec.gate_up_interleaved else {"gate_w": (E, I, K), "up_w": (E, I, K)}
         shapes["down_w"] = (E, K, I)
         if spec.has_expert_bias:
@@ -316,7 +321,7 @@ class GatedFfn(_Operator):
             y = out
             yp, ldy = self._rows("out", out, self.K, T)
         pre = self._empty(T * self.k, 2 * self.I) if keep else None
-        self._launch(self.lib.moe_ffn_forward, self.lib.moe_ffn_workspace_size, self._cfg, T, 0,
+        self._launch(self.lib.moe_ffn_forward, *(self._dense if routing is None else self._routed), T, 0,
                      ctypes.byref(w), up, ldu, T, off, slots, wts, rp, ldr, yp, ldy, _p(pre))
         return y, pre
 
@@ -338,7 +343,7 @@ class GatedFfn(_Operator):
             setattr(g, f, t.data_ptr())
         dwt = None if off is None else self._empty(T, self.k, dtype=torch.float32)
         du = self._like(u, (T, self.K)) if input_grad else None
-        self._launch(self.lib.moe_ffn_backward, self.lib.moe_ffn_workspace_size, self._cfg, T, 1,
+        self._launch(self.lib.moe_ffn_backward, *(self._dense if routing is None else self._routed), T, 1,
                      ctypes.byref(w), up, ldu, T, off, slots, wts, pp, gp, ldg, _p(du), self.K, _p(dwt),
                      ctypes.byref(g))
         if du is not None:
@@ -358,7 +363,7 @@ class Norm(_Operator):
         self.width, self.kind = width, kind
         self.desc = MoeNormDesc(width, NORM_KIND[kind], inputs.DTYPE[dtype], eps)
         self._desc = ctypes.byref(self.desc)
-        self._size(self.lib.moe_norm_workspace_size, self._desc, 0, 0)  # checks the shape
+        self._size(self.lib.moe_norm_workspace_size, self._desc, self._ws_bytes, 0, 0)  # checks the shape
         self._tail = ()  # these calls take no status
 
     def forward(self, x, w, bias=None, out=None, stream=None):
@@ -399,6 +404,6 @@ class Norm(_Operator):
         dx = self._like(x, (T, H)) if input_grad else None
         dw = self._like(w, (H,))
         db = self._like(w, (H,)) if bias_grad else None
-        self._launch(self.lib.moe_norm_backward, self.lib.moe_norm_workspace_size, self._desc, T, 1,
+        self._launch(self.lib.moe_norm_backward, self.lib.moe_norm_workspace_size, self._desc, self._ws_bytes, T, 1,
                      gp, ldg, xp, ldx, wp, sp, T, _p(dx), H, _p(dw), _p(db))
         return dx, dw, db

@@ -1,5 +1,7 @@
 """The training operators on the GPU where their kernels change form: rings that wrap, sums of many
 rows, problems past a threshold (tests/train_ref.py has the 64-bit definitions)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -128,3 +130,64 @@ def test_ffn_bias_gradients_of_very_wide_planes():
     want = R.ffn_backward(dy, x, w, pre, spec, None)
     for n in ("gate_b", "up_b", "down_b", "gate_w", "down_w"):
         R.check(got[n], want[n], n)
+
+
+# ------------------------------------------------------------------ workspace of the dense FFN
+@pytest.mark.parametrize("T,kw", [(2, dict(hidden=512, intermediate=512)), (1500, dict(hidden=2048, intermediate=512)),
+                                  (700, dict(hidden=1024, intermediate=264, has_expert_bias=True)),
+                                  (300, dict(hidden=516, intermediate=260, act_dtype="f32", has_expert_bias=True))])
+def test_dense_ffn_takes_no_second_copy_of_its_rows(T, kw):
+    """What a call allocates beside its results: the hidden rows and the sums' partial rows."""
+    spec, g, w, _ = ffn_case(T, None, kw)
+    x, dy = rand(g, (T, spec.hidden), spec.act_dtype), rand(g, (T, spec.hidden), spec.act_dtype)
+    op = train.GatedFfn(spec)
+    y, pre = op.forward(x, w)
+    want = op.backward(dy, x, w, pre)
+    ok(op)
+    I, H, es = spec.intermediate, spec.hidden, x.element_size()
+    partial = -(-T // 128) * (2 * I + H) * 4 if spec.has_expert_bias else 0
+    room = 3 << 20  # blocks of the allocator are rounded up
+    for call, most in ((lambda: op.forward(x, w, keep=False)[0], T * H * es + T * I * es * (5 if es == 4 else 1)),
+                       (lambda: list(op.backward(dy, x, w, pre).values()),
+                        sum(t.numel() * es for t in want.values()) + T * I * es * (4 if es == 4 else 3) + partial)):
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        out = call()
+        used = torch.cuda.max_memory_allocated() - before
+        assert used <= most + room, (used, most)
+        del out
+
+
+@pytest.mark.parametrize("kw", [dict(hidden=264, intermediate=200, has_expert_bias=True),
+                                dict(hidden=132, intermediate=68, act_dtype="f32", has_expert_bias=True)])
+@pytest.mark.parametrize("T", [1, 3, 5, 129, 1000])
+def test_dense_ffn_stays_in_its_workspace(T, kw):
+    """The C calls with a workspace of exactly the size asked for, which lies between marked bytes."""
+    spec, g, w, _ = ffn_case(T, None, kw)
+    dt = x_dt = spec.act_dtype
+    x, dy = rand(g, (T, spec.hidden), x_dt), rand(g, (T, spec.hidden), dt)
+    op = train.GatedFfn(spec)
+    y, pre = op.forward(x, w)
+    want = op.backward(dy, x, w, pre)
+    lib, p = op.lib, lambda t: t.data_ptr()  # noqa: E731
+    stream = torch.cuda.current_stream().cuda_stream
+    for backward in (0, 1):
+        n = ctypes.c_size_t()
+        assert lib.moe_ffn_dense_workspace_size(op._cfg, T, backward, ctypes.byref(n)) == 0
+        room = torch.full((n.value + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+        ws = p(room) + 4096
+        if backward:
+            got = {k: torch.empty_like(v) for k, v in want.items()}
+            grads = train.MoeFfnGrads(**{k: p(v) for k, v in got.items() if k != "x"})
+            assert lib.moe_ffn_backward(op._cfg, ctypes.byref(op._planes(w)), p(x), spec.hidden, T, None, None, None, p(pre),
+                                        p(dy), spec.hidden, p(got["x"]), spec.hidden, None, ctypes.byref(grads), ws, n.value,
+                                        p(op.status), stream) == 0
+            assert all(torch.equal(got[k], want[k]) for k in want)
+        else:
+            out = torch.empty_like(y)
+            assert lib.moe_ffn_forward(op._cfg, ctypes.byref(op._planes(w)), p(x), spec.hidden, T, None, None, None, None, 0,
+                                       p(out), spec.hidden, None, ws, n.value, p(op.status), stream) == 0
+            assert torch.equal(out, y)
+        ok(op)
+        assert (room[:4096] == 0xA5).all() and (room[4096 + n.value:] == 0xA5).all()

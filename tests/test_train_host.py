@@ -71,3 +71,31 @@ for make in (lambda: train.Linear(64, 64), lambda: train.Norm(64, device="cuda:0
     run = subprocess.run([sys.executable, "-c", prog], cwd=ROOT, capture_output=True, text=True)
     assert run.returncode == 0, run.stderr
     assert run.stdout.count("raised") == 2
+
+
+def dense_size(spec, T, backward):
+    out = ctypes.c_size_t(123)
+    fn = train.lib().moe_ffn_dense_workspace_size
+    return fn(ctypes.byref(M.config_from_spec(spec)), T, backward, ctypes.byref(out)), out.value
+
+
+ONE = inputs.MoeSpec(name="t", config_id=0, hidden=7168, num_experts=1, top_k=1, intermediate=2048)
+
+
+@pytest.mark.parametrize("spec", [ONE, ONE.replace(has_expert_bias=True), ONE.replace(act_dtype="f32", weight_format="f32")])
+def test_dense_ffn_workspace(spec):
+    """h forward; dg, dv, w h (and the f32 dh) and the bias gradients' partial sums backward, each
+    rounded up to 256 bytes: no copy of the rows."""
+    I, es = spec.intermediate, 4 if spec.act_dtype == "f32" else 2
+    for T in (0, 1, 300, 8192):
+        status, fwd = dense_size(spec, T, 0)
+        assert status == 0 and fwd <= T * I * es * (5 if es == 4 else 1) + 512
+        status, back = dense_size(spec, T, 1)
+        partial = -(-T // 128) * (2 * I + spec.hidden) * 4 if spec.has_expert_bias else 0
+        assert status == 0 and back <= T * I * es * (4 if es == 4 else 3) + partial + 1024
+        out = ctypes.c_size_t()
+        assert train.lib().moe_ffn_workspace_size(ctypes.byref(M.config_from_spec(spec)), T, 1, ctypes.byref(out)) == 0
+        assert out.value >= back
+    invalid = M.STATUS_CODE["MOE_ERR_INVALID_ARGUMENT"]
+    assert dense_size(spec.replace(num_experts=4), 10, 0)[0] == invalid
+    assert dense_size(spec, -1, 0) == (invalid, 123)
