@@ -175,12 +175,11 @@ __device__ __forceinline__ float gated_h(int act, float g, float v, float limit,
     const float gc = clamp_above(g, limit), vc = -clamp_above(-clamp_above(v, limit), limit);
     return gc * logistic<FAST>(alpha * gc) * (vc + 1.0f);
 }
-// ... with dh/dg and dh/dv. At the clamp's borders the derivative is that of the inside.
-template <bool FAST>
+// ... with dh/dg and dh/dv, in full f32. At the clamp's borders the derivative is that of the inside.
 __device__ __forceinline__ void gated_grad(int act, float g, float v, float limit, float alpha, float& h, float& hg,
                                            float& hv) {
     if (act == MOE_ACT_SWIGLU) {
-        const float p = logistic<FAST>(g);
+        const float p = logistic<false>(g);
         const float gp = g * p;
         h = gp * v;
         hg = (p + gp * (1.0f - p)) * v;
@@ -188,7 +187,7 @@ __device__ __forceinline__ void gated_grad(int act, float g, float v, float limi
         return;
     }
     const float gc = clamp_above(g, limit), vc = -clamp_above(-clamp_above(v, limit), limit);
-    const float p = logistic<FAST>(alpha * gc);
+    const float p = logistic<false>(alpha * gc);
     const float gp = gc * p, v1 = vc + 1.0f;
     h = gp * v1;
     hg = g > limit ? 0.0f : (p + alpha * gp * (1.0f - p)) * v1;

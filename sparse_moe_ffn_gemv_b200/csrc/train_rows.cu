@@ -302,22 +302,20 @@ __device__ __forceinline__ RowRef row_ref(const RowPlan& p, int64_t r) {
 // One warp per row; gate and up of unit i. (f32; bf16 has both passes in its products' epilogues.)
 __global__ void __launch_bounds__(256) gated_forward_kernel(const GatedArgs a) {
     pdl_begin();
-    using T = float;
-    constexpr bool FAST = false;
     const int lane = threadIdx.x & 31;
     const int64_t rows = plan_rows(a.plan), warps = int64_t(gridDim.x) * 8;
     for (int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); r < rows; r += warps) {
         const RowRef o = row_ref(a.plan, r);
         const float* gp = a.gp + r * 2 * a.I;
-        T* h = static_cast<T*>(a.h) + r * a.I;
-        T* pre = a.pre && o.pos >= 0 ? static_cast<T*>(a.pre) + o.pos * 2 * a.I : nullptr;
+        float* h = static_cast<float*>(a.h) + r * a.I;
+        float* pre = a.pre && o.pos >= 0 ? static_cast<float*>(a.pre) + o.pos * 2 * a.I : nullptr;
         for (int i = lane; i < a.I; i += 32) {
             const int cg = a.interleaved ? 2 * i : i, cv = a.interleaved ? 2 * i + 1 : a.I + i;
             const float g = gp[cg], v = gp[cv];
-            h[i] = from_f<T>(gated_h<FAST>(a.act, g, v, a.limit, a.alpha));
+            h[i] = gated_h<false>(a.act, g, v, a.limit, a.alpha);
             if (pre) {
-                pre[cg] = from_f<T>(g);
-                pre[cv] = from_f<T>(v);
+                pre[cg] = g;
+                pre[cv] = v;
             }
         }
     }
@@ -325,15 +323,13 @@ __global__ void __launch_bounds__(256) gated_forward_kernel(const GatedArgs a) {
 
 __global__ void __launch_bounds__(256) gated_backward_kernel(const GatedArgs a) {
     pdl_begin();
-    using T = float;
-    constexpr bool FAST = false;
     const int lane = threadIdx.x & 31;
     const int64_t rows = plan_rows(a.plan), warps = int64_t(gridDim.x) * 8;
     for (int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); r < rows; r += warps) {
         const RowRef o = row_ref(a.plan, r);
-        T* dgu = static_cast<T*>(a.dgu) + r * 2 * a.I;
-        T* hw = static_cast<T*>(a.hw) + r * a.I;
-        const T* pre = static_cast<const T*>(a.pre) + o.pos * 2 * a.I;
+        float* dgu = static_cast<float*>(a.dgu) + r * 2 * a.I;
+        float* hw = static_cast<float*>(a.hw) + r * a.I;
+        const float* pre = static_cast<const float*>(a.pre) + o.pos * 2 * a.I;
         const float wt = a.topk_w && o.slot >= 0 ? a.topk_w[o.slot] : 1.0f;
         float dw = 0.0f;
         for (int i = lane; i < a.I; i += 32) {
@@ -341,22 +337,22 @@ __global__ void __launch_bounds__(256) gated_backward_kernel(const GatedArgs a) 
             float dg = 0.f, dv = 0.f, hh = 0.f;
             if (o.pos >= 0) {
                 float hg, hv;
-                gated_grad<FAST>(a.act, to_f<T>(pre[cg]), to_f<T>(pre[cv]), a.limit, a.alpha, hh, hg, hv);
+                gated_grad(a.act, pre[cg], pre[cv], a.limit, a.alpha, hh, hg, hv);
                 const float d = a.dh[r * a.I + i];
                 dw += d * hh;
                 dg = d * wt * hg;
                 dv = d * wt * hv;
                 hh *= wt;
             }
-            dgu[cg] = from_f<T>(dg);
-            dgu[cv] = from_f<T>(dv);
-            hw[i] = from_f<T>(hh);
+            dgu[cg] = dg;
+            dgu[cv] = dv;
+            hw[i] = hh;
         }
         if (!a.dtopk_w || o.slot < 0 || !a.plan.offsets) continue;
         if (a.down_b)
             for (int c = lane; c < a.K; c += 32)
-                dw += to_f<T>(static_cast<const T*>(a.dyp)[r * a.K + c]) *
-                      to_f<T>(static_cast<const T*>(a.down_b)[int64_t(o.e) * a.K + c]);
+                dw += static_cast<const float*>(a.dyp)[r * a.K + c] *
+                      static_cast<const float*>(a.down_b)[int64_t(o.e) * a.K + c];
         dw = warp_sum(dw);
         if (lane == 0) a.dtopk_w[o.slot] = dw;
     }
