@@ -86,6 +86,13 @@ def lib():
     return L
 
 
+def _c_int(**sizes):
+    """The C structures hold sizes in 32 bits, and ctypes drops what does not fit."""
+    for name, n in sizes.items():
+        if not -2 ** 31 <= n < 2 ** 31:
+            raise M.MoeError(M.STATUS_CODE["MOE_ERR_SHAPE_OVERFLOW"], f"{name} = {n}")
+
+
 def _p(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -204,6 +211,7 @@ class Linear(_Operator):
                  device="cuda"):
         if activation not in LINEAR_ACTIVATION:
             raise ValueError(f"activation {activation!r}: one of {sorted(LINEAR_ACTIVATION)}")
+        _c_int(in_features=in_features, out_features=out_features)
         super().__init__(dtype, device)
         self.n_in, self.n_out, self.activation = in_features, out_features, activation
         self.desc = MoeLinearDesc(in_features, out_features, LINEAR_ACTIVATION[activation], inputs.DTYPE[dtype])
@@ -259,6 +267,7 @@ class GatedFfn(_Operator):
     (expert_offsets, sorted_slot, topk_w) from moe_route and moe_permute."""
 
     def __init__(self, spec, device="cuda"):
+        _c_int(**{n: getattr(spec, n) for n in ("hidden", "latent_dim", "intermediate", "num_experts", "top_k")})
         super().__init__(spec.act_dtype, device)
         self.spec = spec
         self.cfg = M.config_from_spec(spec)
@@ -359,6 +368,7 @@ class Norm(_Operator):
     def __init__(self, width: int, kind: str = "rms", eps: float = 1e-6, dtype: str = "bf16", device="cuda"):
         if kind not in NORM_KIND:
             raise ValueError(f"kind {kind!r}: one of {sorted(NORM_KIND)}")
+        _c_int(width=width)
         super().__init__(dtype, device)
         self.width, self.kind = width, kind
         self.desc = MoeNormDesc(width, NORM_KIND[kind], inputs.DTYPE[dtype], eps)

@@ -99,3 +99,16 @@ def test_dense_ffn_workspace(spec):
     invalid = M.STATUS_CODE["MOE_ERR_INVALID_ARGUMENT"]
     assert dense_size(spec.replace(num_experts=4), 10, 0)[0] == invalid
     assert dense_size(spec, -1, 0) == (invalid, 123)
+
+
+@pytest.mark.parametrize("make,name", [
+    (lambda n: train.Linear(n, 64), "in_features"), (lambda n: train.Linear(64, n), "out_features"),
+    (lambda n: train.Norm(n), "width"), (lambda n: train.GatedFfn(ONE.replace(hidden=n)), "hidden"),
+    (lambda n: train.GatedFfn(ONE.replace(intermediate=n)), "intermediate"),
+])
+def test_sizes_that_a_c_int_does_not_hold(make, name):
+    """2^32 + 64 is not 64: refused before anything else is asked of the device."""
+    for n in (2 ** 32 + 64, 2 ** 31, -2 ** 31 - 8):
+        with pytest.raises(M.MoeError, match=name) as e:
+            make(n)
+        assert e.value.name == "MOE_ERR_SHAPE_OVERFLOW"
