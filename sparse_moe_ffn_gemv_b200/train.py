@@ -116,7 +116,6 @@ class _Operator:
         self.lib = lib()
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._tail = (self.status.data_ptr(),)  # what follows the workspace in a call
-        self._ws_bytes: Dict[Tuple[int, int], int] = {}  # by tokens and direction
 
     def device_status(self) -> int:
         """The status device-side checks left since the last call (0: none). Synchronises."""
@@ -169,8 +168,9 @@ class _Operator:
         return t.data_ptr(), ld if n > 1 else width
 
     @staticmethod
-    def _size(size_fn, desc_ref, known: Dict, T: int, backward: int) -> int:
+    def _size(sizes, T: int, backward: int) -> int:
         """Bytes of workspace; also the library's check of the operator's shape."""
+        size_fn, desc_ref, known = sizes
         out = ctypes.c_size_t(0)
         M._check(size_fn(desc_ref, T, backward, ctypes.byref(out)), size_fn.__name__)
         if len(known) >= 1024:
@@ -178,12 +178,13 @@ class _Operator:
         known[(T, backward)] = out.value
         return out.value
 
-    def _launch(self, fn, size_fn, desc_ref, known: Dict, T: int, backward: int, *args):
-        """fn(desc, args, workspace, its size, status, stream) on the current stream. known: what
-        size_fn said before."""
+    def _launch(self, fn, sizes, T: int, backward: int, *args):
+        """fn(desc, args, workspace, its size, status, stream) on the current stream. sizes: the call
+        that says how large a workspace is, the desc, and what it said before (by tokens and direction)."""
+        _, desc_ref, known = sizes
         n = known.get((T, backward))
         if n is None:
-            n = self._size(size_fn, desc_ref, known, T, backward)
+            n = self._size(sizes, T, backward)
         stream = _current_stream(self._index)
         ws = _allocate(n, stream) if n else None
         try:
@@ -216,7 +217,8 @@ class Linear(_Operator):
         self.n_in, self.n_out, self.activation = in_features, out_features, activation
         self.desc = MoeLinearDesc(in_features, out_features, LINEAR_ACTIVATION[activation], inputs.DTYPE[dtype])
         self._desc = ctypes.byref(self.desc)
-        self._size(self.lib.moe_linear_workspace_size, self._desc, self._ws_bytes, 0, 0)  # checks the shape
+        self._sizes = (self.lib.moe_linear_workspace_size, self._desc, {})
+        self._size(self._sizes, 0, 0)  # checks the shape
 
     def forward(self, x, w, bias=None, residual=None, keep: bool = False, out=None, stream=None):
         """y, or (y, pre) with keep: pre = x W^T + b is what backward needs of an activation."""
@@ -235,7 +237,7 @@ class Linear(_Operator):
             y = out
             yp, ldy = self._rows("out", out, N, T)
         pre = self._empty(T, N) if keep else None
-        self._launch(self.lib.moe_linear_forward, self.lib.moe_linear_workspace_size, self._desc, self._ws_bytes, T, 0,
+        self._launch(self.lib.moe_linear_forward, self._sizes, T, 0,
                      xp, ldx, wp, bp, rp, ldr, T, yp, ldy, _p(pre))
         return (y, pre) if keep else y
 
@@ -253,7 +255,7 @@ class Linear(_Operator):
         dx = self._like(x, (T, K)) if input_grad else None
         dw = self._like(w, (N, K)) if weight_grad else None
         db = self._empty(N) if bias_grad else None
-        self._launch(self.lib.moe_linear_backward, self.lib.moe_linear_workspace_size, self._desc, self._ws_bytes, T, 1,
+        self._launch(self.lib.moe_linear_backward, self._sizes, T, 1,
                      gp, ldg, xp, ldx, wp, pp, T, _p(dx), K, _p(dw), _p(db))
         return dx, dw, db
 
@@ -275,9 +277,9 @@ class GatedFfn(_Operator):
         M._check(M.moe_config_validate(self.cfg), "moe_config_validate")
         E, I, K = spec.num_experts, spec.intermediate, spec.expert_in
         self.E, self.k, self.I, self.K = E, spec.top_k, I, K
-        self._size(self.lib.moe_ffn_workspace_size, self._cfg, self._ws_bytes, 0, 0)  # checks the weight format
-        self._routed = (self.lib.moe_ffn_workspace_size, self._cfg, self._ws_bytes)
+        self._routed = (self.lib.moe_ffn_workspace_size, self._cfg, {})
         self._dense = (self.lib.moe_ffn_dense_workspace_size, self._cfg, {})
+        self._size(self._routed, 0, 0)  # checks the weight format
         shapes = {"gate_up_w": (E, 2 * I, K)} if spec.gate_up_interleaved else {"gate_w": (E, I, K), "up_w": (E, I, K)}
         shapes["down_w"] = (E, K, I)
         if spec.has_expert_bias:
@@ -330,7 +332,7 @@ class GatedFfn(_Operator):
             y = out
             yp, ldy = self._rows("out", out, self.K, T)
         pre = self._empty(T * self.k, 2 * self.I) if keep else None
-        self._launch(self.lib.moe_ffn_forward, *(self._dense if routing is None else self._routed), T, 0,
+        self._launch(self.lib.moe_ffn_forward, self._dense if routing is None else self._routed, T, 0,
                      ctypes.byref(w), up, ldu, T, off, slots, wts, rp, ldr, yp, ldy, _p(pre))
         return y, pre
 
@@ -352,7 +354,7 @@ class GatedFfn(_Operator):
             setattr(g, f, t.data_ptr())
         dwt = None if off is None else self._empty(T, self.k, dtype=torch.float32)
         du = self._like(u, (T, self.K)) if input_grad else None
-        self._launch(self.lib.moe_ffn_backward, *(self._dense if routing is None else self._routed), T, 1,
+        self._launch(self.lib.moe_ffn_backward, self._dense if routing is None else self._routed, T, 1,
                      ctypes.byref(w), up, ldu, T, off, slots, wts, pp, gp, ldg, _p(du), self.K, _p(dwt),
                      ctypes.byref(g))
         if du is not None:
@@ -373,7 +375,8 @@ class Norm(_Operator):
         self.width, self.kind = width, kind
         self.desc = MoeNormDesc(width, NORM_KIND[kind], inputs.DTYPE[dtype], eps)
         self._desc = ctypes.byref(self.desc)
-        self._size(self.lib.moe_norm_workspace_size, self._desc, self._ws_bytes, 0, 0)  # checks the shape
+        self._sizes = (self.lib.moe_norm_workspace_size, self._desc, {})
+        self._size(self._sizes, 0, 0)  # checks the shape
         self._tail = ()  # these calls take no status
 
     def forward(self, x, w, bias=None, out=None, stream=None):
@@ -414,6 +417,6 @@ class Norm(_Operator):
         dx = self._like(x, (T, H)) if input_grad else None
         dw = self._like(w, (H,))
         db = self._like(w, (H,)) if bias_grad else None
-        self._launch(self.lib.moe_norm_backward, self.lib.moe_norm_workspace_size, self._desc, self._ws_bytes, T, 1,
+        self._launch(self.lib.moe_norm_backward, self._sizes, T, 1,
                      gp, ldg, xp, ldx, wp, sp, T, _p(dx), H, _p(dw), _p(db))
         return dx, dw, db
