@@ -1,5 +1,8 @@
 /*
- * moe_train.h -- C ABI of the operators that train the block, and of their serving forms.
+ * moe_train.h -- C ABI of the operators that train the block's experts, projections and norm, and
+ * of their serving forms. The router (scores, top-k and its normalisation, the blend's coefficients)
+ * has no backward pass here beyond dtopk_w, and there is none of the whole block: the caller
+ * chains these calls.
  *
  * Same library (libmoe_b200.so), status codes and conventions as moe.h: device pointers,
  * caller-owned buffers, no allocation, every call asynchronous on `stream`, every host check
@@ -34,7 +37,8 @@
  * MOE_ERR_DEVICE_CHECK (a slot id or an offset out of range: such rows are dropped; or a slot
  * that stands twice, seen where y or du is computed: the results are not valid) or
  * MOE_ERR_DEVICE_TIMEOUT (a bounded wait gave up; the results are not valid). The first
- * error stays.
+ * error stays. The norm calls take none: they check nothing on the device and hold no wait that
+ * can give up.
  *
  * Results do not depend on the run: no sum uses atomics.
  */
@@ -117,7 +121,8 @@ MOE_API moe_status moe_ffn_forward(const moe_config *cfg, const moe_weights *w, 
  * (routed; may be NULL) and the gradients of the planes, [E, rows, cols] like the planes
  * (experts without rows get zeros). Required gradients: those of the planes that the config
  * has; du may be NULL. The activations are recomputed from pre. bf16: dg, dv and w h are
- * rounded to bf16 before their products; the slots' rows of du are summed in f32; dtopk_w keeps the
+ * rounded to bf16 before their products, and the gate and up bias gradients are f32 sums of dg and
+ * dv so rounded (down_b's of w dy unrounded); the slots' rows of du are summed in f32; dtopk_w keeps the
  * matrix instructions' truncated additions (up to 3e-6 of its value low). T == 0 clears the
  * gradients. */
 MOE_API moe_status moe_ffn_backward(const moe_config *cfg, const moe_weights *w, const void *u, int64_t ldu,

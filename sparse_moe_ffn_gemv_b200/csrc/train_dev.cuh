@@ -48,7 +48,7 @@ __device__ __forceinline__ void store_vec(T* p, const float (&f)[Vec<T>::N]) {
 // Logistic function. expf overflows to inf for z < -88, where 1 / (1 + inf) = 0 is the
 // rounded value; FAST: the hardware exponential and divide (relative error about 2^-21),
 // for results that are rounded to bf16 next. __fdividef returns 0 for a divisor in
-// (2^126, 2^128), which is again the rounded value here.
+// (2^126, 2^128), that is for z < -87.3, where the value is below 2^-125.
 template <bool FAST>
 __device__ __forceinline__ float logistic(float z) {
     if constexpr (FAST) return __fdividef(1.0f, 1.0f + __expf(-z));
@@ -235,8 +235,9 @@ __device__ __forceinline__ float2 gated_h2(float2 g, float2 v, float limit, floa
 // start when its blocks leave, and itself waits for the launch before it to complete, with its
 // memory visible, before it touches memory: what precedes the wait (barriers, TMEM, bringing
 // weights into L2) runs in the other's tail. Every block waits, so that a launch's completion
-// implies that of all before it. What it gives: 8192 tokens 7168 -> 3584 353 -> 335 us, dense gated
-// backward 1240 -> 1182, one token 3584 -> 7168 12.3 -> 11.5, RMS norm 8192 x 3584 24.5 -> 22.9.
+// implies that of all before it. What it gives: 8192 tokens 7168 -> 3584 351 -> 337 us, dense gated
+// backward (8192 x 7168 x 2048) 1227 -> 1190, one token 3584 -> 7168 12.3 -> 11.6, RMS norm 8192 x 3584
+// 24.5 -> 23.0.
 //
 // Launches that follow a long tail and spread over the GPU by themselves stay plain: their blocks
 // would crowd on the first SMs that are free (behind an expert product dtopk_kernel's 128 blocks took

@@ -23,6 +23,9 @@
 //               products: one accumulator row per lane, 32 columns at a time, results turned
 //               through 2 KB of shared memory per warp so that global rows are written and
 //               read in whole 32-byte sectors
+// The gated derivative's epilogue is at the 168 registers that 320 threads can have and spills: 36
+// bytes stored, 56 loaded per thread (interleaved planes 8 and 8); the split forms, whose CTAs run one
+// tile each, 204 and 152.
 // Every wait gives up after 2 s, records MOE_ERR_DEVICE_TIMEOUT, lets its own copies and
 // products finish and returns; TMEM is always freed.
 #include <cuda.h>

@@ -1,4 +1,5 @@
-"""Python binding of include/moe_train.h: the operators that train the block.
+"""Python binding of include/moe_train.h: the operators that train the block's experts,
+projections and norm.
 
     Linear    y = act(x W^T + b) + r        forward, backward
     GatedFfn  the routed experts of a MoeSpec, or one dense gated FFN   forward, backward
@@ -10,6 +11,10 @@ them), outputs and workspaces come from PyTorch's allocator at each call, so cal
 streams and captured graphs share nothing but the status word. Tensors are [rows, width], rows
 may be strided. A call runs on `stream`, or on the current stream of the handle's device; with
 `stream` its tensors may be dropped at once, and what it returns belongs to that stream.
+
+The calls are no autograd functions: what a forward call returns does not require a gradient,
+whatever its tensors do, and the caller runs the backward calls. The router has none beyond
+"topk_w".
 """
 from __future__ import annotations
 
