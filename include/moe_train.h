@@ -123,8 +123,8 @@ MOE_API moe_status moe_ffn_forward(const moe_config *cfg, const moe_weights *w, 
  * has; du may be NULL. The activations are recomputed from pre. bf16: dg, dv and w h are
  * rounded to bf16 before their products, and the gate and up bias gradients are f32 sums of dg and
  * dv so rounded (down_b's of w dy unrounded); the slots' rows of du are summed in f32; dtopk_w keeps the
- * matrix instructions' truncated additions (up to 3e-6 of its value low). T == 0 clears the
- * gradients. */
+ * matrix instructions' truncated additions (low by about 1.5e-8 of its value per 16 of K: 2.6e-6 at
+ * K = 2880, 7e-6 at 7168). T == 0 clears the gradients. */
 MOE_API moe_status moe_ffn_backward(const moe_config *cfg, const moe_weights *w, const void *u, int64_t ldu,
                                     int64_t T, const int32_t *expert_offsets, const int32_t *sorted_slot,
                                     const float *topk_w, const void *pre, const void *dy, int64_t lddy, void *du,
