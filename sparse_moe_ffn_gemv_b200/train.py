@@ -10,7 +10,8 @@ operator's shape and one status word; weights are passed at each call (a trainin
 them), outputs and workspaces come from PyTorch's allocator at each call, so calls on several
 streams and captured graphs share nothing but the status word. Tensors are [rows, width], rows
 may be strided. A call runs on `stream`, or on the current stream of the handle's device; with
-`stream` its tensors may be dropped at once, and what it returns belongs to that stream.
+`stream` its tensors may be dropped at once (not with a torch.cuda.ExternalStream, whose end
+PyTorch does not know), and what it returns belongs to that stream.
 
 The calls are no autograd functions: what a forward call returns does not require a gradient,
 whatever its tensors do, and the caller runs the backward calls. The router has none beyond
@@ -144,9 +145,10 @@ class _Operator:
                 raise ValueError(f"stream of {stream.device}, handle of {self.device}")
             with torch.cuda.stream(stream):
                 yield
-            for t in (*tensors, self.status):
-                if t is not None:
-                    t.record_stream(stream)
+            if not isinstance(stream, torch.cuda.ExternalStream):  # which may be gone when they are freed
+                for t in (*tensors, self.status):
+                    if t is not None:
+                        t.record_stream(stream)
         else:
             with torch.cuda.device(self.device):
                 yield

@@ -94,3 +94,29 @@ def test_captured_on_a_named_stream():
             graph.replay()
             ok(op)
             assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+
+
+def test_external_stream():
+    """A stream that PyTorch did not make runs the calls, and no tensor is recorded on it: it may be
+    gone when the tensor is freed."""
+    inner = torch.cuda.Stream()
+    s = torch.cuda.ExternalStream(inner.cuda_stream)
+    recorded = []
+
+    class Marked(torch.Tensor):
+        def record_stream(self, stream):
+            recorded.append(stream)
+            super().record_stream(stream)
+
+    for op, name, tensors, call in calls():
+        flat = lambda o: [o] if torch.is_tensor(o) else list(o)  # noqa: E731
+        want = flat(call(tensors, torch.cuda.current_stream()))
+        torch.cuda.synchronize()
+        got = flat(call([t.as_subclass(Marked) for t in tensors], s))
+        ok(op)
+        assert all(torch.equal(a.as_subclass(torch.Tensor), b) for a, b in zip(got, want)), name
+        assert not recorded
+    lin, _, tensors, call = calls()[0]
+    call([t.as_subclass(Marked) for t in tensors], inner)
+    ok(lin)
+    assert len(recorded) == len(tensors)
